@@ -292,11 +292,15 @@ def _plain_resize(s):
     to, have = s["to"].long(), lens.long()
     col = torch.arange(table.shape[1], device=to.device)
     start = torch.minimum(to, have)
+    # a length inside a page that the window has given up is refused
+    there = table.gather(1, (start // page).clamp(max=table.shape[1] - 1)[:, None])[:, 0] >= 0
+    good = there | (start % page == 0)
+    to = torch.where(good, to, have)
     up = lambda x: (x + page - 1) // page  # noqa: E731
     drop = (col >= up(to)[:, None]) & (col < up(have)[:, None])
     if s["window"]:
         drop |= (col >= up(s["sinks"])) & ((col + 1) * page - 1 <= (start - s["window"])[:, None])
-    drop &= table >= 0
+    drop &= (table >= 0) & good[:, None]
     _add_refs(refs, table, -drop.int())
     table.masked_fill_(drop, -1)
     grow = (to > have) & (to <= table.shape[1] * page)
@@ -314,7 +318,7 @@ def _plain_resize(s):
     shared &= fits
     _add_refs(refs, last_page, -shared.int())
     _copy_rows(s, last_page[shared], table.gather(1, last[:, None])[:, 0].long()[shared], (have % page)[shared])
-    s["pos"].copy_(torch.where(fits, start, -1))
+    s["pos"].copy_(torch.where(fits & good, start, -1))
     lens.copy_(torch.where(fits, to, have))
     return {"k": s["k"], "v": s["v"], "ints": s["ints"], "pos": s["pos"]}
 
