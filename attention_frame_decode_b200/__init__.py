@@ -18,7 +18,7 @@ if not os.path.exists(LIB_PATH):
 _lib = C.CDLL(LIB_PATH)
 
 VC_OK, VC_ERR_INVALID_ARG, VC_ERR_UNSUPPORTED, VC_ERR_CUDA, VC_ERR_CAPACITY, VC_ERR_STATE = range(6)
-VC_DEV_CAPACITY, VC_DEV_NONFINITE, VC_DEV_TIMEOUT = 1, 2, 4
+VC_DEV_CAPACITY, VC_DEV_NONFINITE, VC_DEV_TIMEOUT, VC_DEV_INVALID = 1, 2, 4, 8
 W_BF16, W_INT8_SYM, W_INT4_ASYM, W_INT3_ASYM = 0, 1, 2, 3
 OPT_GRAPH, OPT_PDL, OPT_FRAME, OPT_GEMV_SHAPE = 1, 2, 3, 4
 
@@ -54,6 +54,26 @@ class VcTokenEmbeddings(C.Structure):
 class VcState(C.Structure):
     _fields_ = [("ssm", C.c_void_p), ("conv", C.c_void_p), ("k", C.c_void_p), ("v", C.c_void_p),
                 ("ctx_len", C.c_void_p), ("status", C.c_void_p)]
+
+
+class VcPagedKv(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("table", C.c_void_p), ("len", C.c_void_p),
+                ("refs", C.c_void_p), ("status", C.c_void_p), ("workspace", C.c_void_p),
+                ("workspace_bytes", C.c_size_t), ("layers", C.c_int), ("pages", C.c_int), ("page_size", C.c_int),
+                ("kv_heads", C.c_int), ("head_dim", C.c_int), ("q_heads", C.c_int), ("f16", C.c_int),
+                ("seqs", C.c_int), ("columns", C.c_int), ("window", C.c_int), ("sinks", C.c_int)]
+
+
+class VcSessionPart(C.Structure):
+    _fields_ = [("base", C.c_void_p), ("bytes", C.c_int64), ("stride", C.c_int64), ("outer_stride", C.c_int64),
+                ("outer", C.c_int)]
+
+
+class VcAttnRows(C.Structure):
+    _fields_ = [("q", C.c_void_p), ("k", C.c_void_p), ("v", C.c_void_p), ("out", C.c_void_p),
+                ("q_stride", C.c_int64), ("k_stride", C.c_int64), ("v_stride", C.c_int64), ("out_stride", C.c_int64),
+                ("seqs", C.c_void_p), ("pos", C.c_void_p), ("cu_rows", C.c_void_p), ("batch", C.c_int),
+                ("rows", C.c_int), ("scale", C.c_float)]
 
 
 _p = C.c_void_p
@@ -92,6 +112,12 @@ _lib.vc_debug_mamba_prefill_scratch_bytes.argtypes = [C.POINTER(VcConfig), _i]
 _lib.vc_debug_mamba_prefill_scratch_bytes.restype = C.c_size_t
 _lib.vc_debug_mamba_prefill.argtypes = [C.POINTER(VcConfig), C.POINTER(VcLayerWeights), _p, _i, _p, _p, _p, _p, _p,
                                         _p]
+_lib.vc_paged_workspace_bytes.argtypes = [C.POINTER(VcPagedKv)]
+_lib.vc_paged_workspace_bytes.restype = C.c_size_t
+_lib.vc_paged_resize.argtypes = [C.POINTER(VcPagedKv), _i, _p, _p, _i, _p, _p]
+_lib.vc_paged_fork.argtypes = [C.POINTER(VcPagedKv), _i, _p, _p, C.POINTER(VcSessionPart), _i, _p, _p]
+_lib.vc_paged_compact.argtypes = [C.POINTER(VcPagedKv), _p, _p]
+_lib.vc_paged_attend.argtypes = [C.POINTER(VcPagedKv), _i, C.POINTER(VcAttnRows), _p]
 _lib.vc_destroy.argtypes = [_p]
 _lib.vc_destroy.restype = None
 _lib.vc_status_string.argtypes = [_i]
@@ -102,7 +128,8 @@ for _f in ("vc_quantize_weight", "vc_pack_bf16_weight", "vc_pack_weight", "vc_de
            "vc_set_option", "vc_step", "vc_step_fused", "vc_step_host", "vc_prefill", "vc_debug_set_taps",
            "vc_debug_set_prefill_taps", "vc_debug_set_zx_taps", "vc_debug_mamba_step",
            "vc_debug_gemv", "vc_debug_gemm", "vc_debug_mamba_prefill", "vc_debug_gemv_noalloc",
-           "vc_gemv_noalloc_status", "vc_gemv_noalloc_reset"):
+           "vc_gemv_noalloc_status", "vc_gemv_noalloc_reset", "vc_paged_resize", "vc_paged_fork", "vc_paged_compact",
+           "vc_paged_attend"):
     getattr(_lib, _f).restype = _i
 
 EXPORTS = ("vc_weight_bytes", "vc_quantize_weight", "vc_pack_bf16_weight", "vc_pack_weight", "vc_debug_dequant",
@@ -112,7 +139,8 @@ EXPORTS = ("vc_weight_bytes", "vc_quantize_weight", "vc_pack_bf16_weight", "vc_p
            "vc_gemv_scratch_bytes",
            "vc_debug_gemv", "vc_debug_gemm", "vc_gemv_noalloc_scratch_bytes", "vc_debug_gemv_noalloc",
            "vc_gemv_noalloc_status", "vc_gemv_noalloc_reset",
-           "vc_debug_mamba_prefill_scratch_bytes", "vc_debug_mamba_prefill", "vc_destroy",
+           "vc_debug_mamba_prefill_scratch_bytes", "vc_debug_mamba_prefill", "vc_paged_workspace_bytes",
+           "vc_paged_resize", "vc_paged_fork", "vc_paged_compact", "vc_paged_attend", "vc_destroy",
            "vc_status_string", "vc_last_cuda_error")
 
 
@@ -387,3 +415,6 @@ class Backbone:
             self.close()
         except Exception:
             pass
+
+
+from .paged import PagedCache, SessionParts, session_parts  # noqa: E402  (needs the bound library above)

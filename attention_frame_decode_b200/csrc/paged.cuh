@@ -1,0 +1,63 @@
+// paged.cuh -- the paged KV cache: what its page calls and its attention kernels share.
+#pragma once
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "../../include/vc.h"
+
+namespace vc {
+
+// vc_paged_kv as the kernels take it (one layer's pages for attention, every layer's for page calls)
+struct PagedKv {
+    uint16_t *k, *v;
+    int *table, *len, *refs, *status;
+    int layers, pages, page, page_shift, Hk, Dh, Hq, seqs, columns, window, sinks;
+};
+
+struct PagedWorkspace {
+    int* head;        // [0] copies listed by a resize or fork
+    int* merge;       // arrival counters of split attention work [kMergeCounters] (zero between calls)
+    int* copies;      // [seqs][3]: source page, destination page, positions to copy
+    int* ok;          // [seqs]: rows of a fork that are done
+    int* first;       // [seqs]: the lowest row that names a session
+    int4* rows;       // [seqs]: a resize's rows
+    int* need;        // [seqs][2]: a row's first page request and how many it has
+    int* chunk_live;  // compaction: pages in use per chunk of kCompactChunk
+    int* rename;      // [pages]: resize and fork: the free pages to hand out; compact: a page's move, -1: none
+    int* moves;       // [pages][2]: source and destination of each move of a compaction
+    float* partial;   // split attention work
+    size_t bytes;
+};
+
+static constexpr int kMaxSms = 256;
+static constexpr int kCompactChunk = 4096;
+static constexpr int kMaxSplitCtas = 2 * kMaxSms;      // CTAs of an attention launch that splits the key axis
+static constexpr int kTileRows = 128;                  // rows of the largest attention tile
+
+// the workspace's parts, in order; false where the sizes are outside the documented limits
+bool paged_sizes_ok(const vc_paged_kv& c);
+PagedWorkspace paged_carve(const vc_paged_kv& c, void* base);
+
+struct PagedAttnArgs {
+    PagedKv c;                   // k, v: this layer's
+    const uint16_t *q, *kn, *vn; // new rows
+    uint16_t* out;
+    long long q_ld, k_ld, v_ld, out_ld;
+    const int *seqs, *pos, *cu_rows;
+    int batch, rows, f16, num_sms;
+    float scale_log2;            // scale * log2(e)
+    int* merge;
+    float* partial;
+};
+
+cudaError_t launch_paged_append(const PagedAttnArgs& a, cudaStream_t s);
+cudaError_t launch_paged_tiles(const PagedAttnArgs& a, cudaStream_t s);
+
+cudaError_t launch_paged_resize(const PagedKv& c, const PagedWorkspace& w, int n, const int* seqs, const int* lens,
+                                int add, int* pos, cudaStream_t s);
+cudaError_t launch_paged_fork(const PagedKv& c, const PagedWorkspace& w, int n, const int* src, const int* dst,
+                              const vc_session_part* parts, int n_parts, int* done, cudaStream_t s);
+cudaError_t launch_paged_compact(const PagedKv& c, const PagedWorkspace& w, int* live, cudaStream_t s);
+
+}  // namespace vc

@@ -1,0 +1,344 @@
+// paged_attn.cu -- windowed attention over the paged KV cache: appending rows, and the attention of row
+// tiles on warp-level matrix instructions.
+//
+// For a query at position p of session s and KV head j, with the keys t that it sees (t <= p, t < sinks or
+// t > p - window, the page of t mapped):
+//     o = sum_t w_t V_t / sum_t w_t,   w_t = exp2(z_t - max z),   z_t = scale log2(e) q . K_t.
+// The queries of a session's rows and of the Hq / Hk heads that share KV head j are packed into one list of
+// rows (row r: token r / G, head j G + r % G, G = Hq / Hk), which is cut into tiles: a KV tile that is loaded
+// once serves all the heads of a group, and a window of W keys is read by a tile that spans few positions.
+#include "paged_dev.cuh"
+
+namespace vc {
+
+// ------------------------------------------------------------------------------------------
+// append: the new rows' keys and values into their pages, 16 bytes per thread.  Bound: HBM (4 Hk Dh bytes
+// read and written per row).
+// ------------------------------------------------------------------------------------------
+__global__ void __launch_bounds__(256) paged_append_kernel(const PagedAttnArgs a) {
+    const int width = a.c.Hk * a.c.Dh / 8;   // 16-byte chunks per row
+    const long long idx = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+    const int row = (int)(idx / width), chunk = (int)(idx % width);
+    if (row >= a.rows) return;
+    int i = row;
+    if (a.cu_rows) {   // the last session that starts at or before the row
+        int lo = 0, hi = a.batch;
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (a.cu_rows[mid + 1] <= row) lo = mid + 1;
+            else hi = mid;
+        }
+        i = lo;
+        if (i >= a.batch) return;   // behind the last session
+    }
+    AttnSession o;
+    if (!attn_session(a, i, o)) return;
+    if (row < o.row0 || row >= o.row0 + o.n) return;
+    const int t = o.p0 + row - o.row0;
+    const int e = page_of(a.c, o.s, t >> a.c.page_shift);
+    if (e < 0) return;
+    const int j = chunk * 8 / a.c.Dh, d = chunk * 8 % a.c.Dh;
+    const size_t to = (((size_t)e * a.c.Hk + j) * a.c.page + (t & (a.c.page - 1))) * a.c.Dh + d;
+    *reinterpret_cast<uint4*>(a.c.k + to) = *reinterpret_cast<const uint4*>(a.kn + (size_t)row * a.k_ld + chunk * 8);
+    *reinterpret_cast<uint4*>(a.c.v + to) = *reinterpret_cast<const uint4*>(a.vn + (size_t)row * a.v_ld + chunk * 8);
+}
+
+cudaError_t launch_paged_append(const PagedAttnArgs& a, cudaStream_t s) {
+    const long long n = (long long)a.rows * (a.c.Hk * a.c.Dh / 8);
+    paged_append_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+// ------------------------------------------------------------------------------------------
+// row tiles: 64 packed rows per CTA, 16 per warp, key blocks of 64 positions double-buffered with cp.async.
+// The key axis is split over `splits` CTAs where there are few tiles; the last CTA of a tile to arrive joins
+// them in split order.
+// ------------------------------------------------------------------------------------------
+static constexpr int kTR = 64, kTK = 64, kTThreads = 128;
+
+// the session and the tile within it of the launch's `tile`-th tile; false behind the last (a whole warp calls)
+VC_DEV bool find_tile(const PagedAttnArgs& a, int group, int tile_rows, int tile, int& session, int& t) {
+    const int lane = threadIdx.x & 31;
+    long long before = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += 32) {
+        const int b = b0 + lane;
+        const long long mine = b < a.batch ? ((long long)session_rows(a, b) * group + tile_rows - 1) / tile_rows : 0;
+        long long incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long u = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += u;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, before + incl > tile);
+        if (hit) {
+            const int l = __ffs(hit) - 1;
+            session = b0 + l;
+            t = (int)(tile - (before + __shfl_sync(0xffffffffu, incl - mine, l)));
+            return true;
+        }
+        before += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    return false;
+}
+
+template <int DH>
+static constexpr size_t tile_smem_bytes() { return (size_t)5 * 64 * (DH + 8) * 2; }
+
+template <int DH, bool F16>
+__global__ void __launch_bounds__(kTThreads) paged_tile_kernel(const PagedAttnArgs a, int splits) {
+    constexpr int SK = DH + 8, CH = DH / 8, NT = DH / 8;
+    extern __shared__ __align__(16) uint8_t smem[];
+    uint16_t* Qs = reinterpret_cast<uint16_t*>(smem);   // [64][SK]
+    uint16_t* KV = Qs + kTR * SK;                         // [2 stages][K, V][64][SK]
+    __shared__ int last_flag;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tq = lane & 3;
+    const int G = a.c.Hq / a.c.Hk, j = blockIdx.y, split = blockIdx.z;
+
+    int session, tile;
+    if (blockIdx.x == 0 && j == 0 && split == 0)   // reports every session whose indices do not fit
+        for (int i = tid; i < a.batch; i += kTThreads) {
+            AttnSession o;
+            attn_session(a, i, o);
+        }
+    if (!find_tile(a, G, kTR, blockIdx.x, session, tile)) return;
+    AttnSession o;
+    if (!attn_session(a, session, o)) return;
+    const int n_rows = o.n * G, r0 = tile * kTR;
+    const int p_lo = o.p0 + r0 / G, p_hi = o.p0 + (min(r0 + kTR, n_rows) - 1) / G;
+    const KeyBlocks kb = key_blocks<kTK>(a.c.window, a.c.sinks, p_lo, p_hi);
+    const int i0 = (int)((long long)kb.total * split / splits), i1 = (int)((long long)kb.total * (split + 1) / splits);
+
+    auto load = [&](int i) {
+        if (i < i1) {
+            const int t0 = kb.block(i) * kTK;
+            uint16_t* Ks = KV + (i & 1) * 2 * kTK * SK;
+            uint16_t* Vs = Ks + kTK * SK;
+            for (int idx = tid; idx < kTK * CH; idx += kTThreads) {
+                const int r = idx / CH, c = idx % CH, t = t0 + r;
+                const int e = t <= p_hi ? page_of(a.c, o.s, t >> a.c.page_shift) : -1;
+                const size_t from = (((size_t)max(e, 0) * a.c.Hk + j) * a.c.page + (t & (a.c.page - 1))) * DH + c * 8;
+                cp_async16(Ks + r * SK + c * 8, a.c.k + from, e >= 0);
+                cp_async16(Vs + r * SK + c * 8, a.c.v + from, e >= 0);
+            }
+        }
+        cp_async_commit();
+    };
+    for (int idx = tid; idx < kTR * CH; idx += kTThreads) {
+        const int r = idx / CH, c = idx % CH, rr = r0 + r;
+        const bool in = rr < n_rows;
+        const size_t from = (size_t)(o.row0 + (in ? rr / G : 0)) * a.q_ld + (size_t)(j * G + (in ? rr % G : 0)) * DH + c * 8;
+        cp_async16(Qs + r * SK + c * 8, a.q + from, in);
+    }
+    load(i0);
+
+    float acc[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+    const int pr[2] = {o.p0 + (r0 + 16 * warp + g) / G, o.p0 + (r0 + 16 * warp + g + 8) / G};
+    const int mi = lane >> 3, lr = lane & 7;
+
+    for (int i = i0; i < i1; ++i) {
+        load(i + 1);
+        cp_async_wait<1>();
+        __syncthreads();
+        const int t0 = kb.block(i) * kTK;
+        uint16_t* Ks = KV + (i & 1) * 2 * kTK * SK;
+        uint16_t* Vs = Ks + kTK * SK;
+        // 16-key groups whose page is mapped
+        unsigned mapped = 0;
+#pragma unroll
+        for (int u = 0; u < kTK / 16; ++u) {
+            const int t = t0 + 16 * u;
+            if (t <= p_hi && page_of(a.c, o.s, t >> a.c.page_shift) >= 0) mapped |= 1u << u;
+        }
+        const bool whole = mapped == (1u << (kTK / 16)) - 1u && t0 + kTK - 1 <= p_lo &&
+                           (a.c.window == 0 || t0 > p_hi - a.c.window || t0 + kTK - 1 < a.c.sinks);
+        float s[kTK / 8][4];
+#pragma unroll
+        for (int n = 0; n < kTK / 8; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
+#pragma unroll
+        for (int ks = 0; ks < DH / 16; ++ks) {
+            uint32_t qa[4];
+            ldsm4(qa, Qs + (16 * warp + 8 * (mi & 1) + lr) * SK + ks * 16 + 8 * (mi >> 1));
+#pragma unroll
+            for (int n = 0; n < kTK / 16; ++n) {
+                uint32_t b[4];
+                ldsm4(b, Ks + (16 * n + 8 * (mi >> 1) + lr) * SK + ks * 16 + 8 * (mi & 1));
+                mma16<F16>(s[2 * n], qa, b[0], b[1]);
+                mma16<F16>(s[2 * n + 1], qa, b[2], b[3]);
+            }
+        }
+        auto seen = [&](int h, int key) {
+            const int t = t0 + key;
+            return ((mapped >> (key >> 4)) & 1u) && t <= pr[h] &&
+                   (a.c.window == 0 || t < a.c.sinks || t > pr[h] - a.c.window);
+        };
+        float mx[2] = {m[0], m[1]};
+#pragma unroll
+        for (int n = 0; n < kTK / 8; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int h = e >> 1;
+                s[n][e] *= a.scale_log2;
+                if (!whole && !seen(h, 8 * n + 2 * tq + (e & 1))) s[n][e] = -INFINITY;
+                mx[h] = fmaxf(mx[h], s[n][e]);
+            }
+        float corr[2], base[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
+            mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
+            base[h] = mx[h] == -INFINITY ? 0.0f : mx[h];   // nothing seen so far: every weight 0
+            corr[h] = exp2_approx(m[h] - base[h]);
+            m[h] = mx[h];
+            l[h] *= corr[h];
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            acc[n][0] *= corr[0]; acc[n][1] *= corr[0];
+            acc[n][2] *= corr[1]; acc[n][3] *= corr[1];
+        }
+#pragma unroll
+        for (int n = 0; n < kTK / 8; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                s[n][e] = exp2_approx(s[n][e] - base[e >> 1]);
+                l[e >> 1] += s[n][e];
+            }
+        // a value that is not finite may be under a weight of 0 for some rows and seen by others: rare, and then
+        // it is added to the rows that see it and taken out of the tile before the products
+        if (!whole) {
+            bool odd = false;
+            for (int idx = tid; idx < kTK * (DH / 2); idx += kTThreads)
+                odd |= nonfinite2<F16>(*reinterpret_cast<const uint32_t*>(Vs + (idx / (DH / 2)) * SK + 2 * (idx % (DH / 2))));
+            if (__syncthreads_or(odd)) {
+                for (int key = 0; key < kTK; ++key)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint16_t u = Vs[key * SK + 8 * n + 2 * tq + (e & 1)];
+                            if ((u & exponent_mask<F16>()) == exponent_mask<F16>() && seen(e >> 1, key))
+                                acc[n][e] += unpack16<F16>(u);
+                        }
+                __syncthreads();
+                for (int idx = tid; idx < kTK * DH; idx += kTThreads) {
+                    uint16_t* p = Vs + (idx / DH) * SK + idx % DH;
+                    if ((*p & exponent_mask<F16>()) == exponent_mask<F16>()) *p = 0;
+                }
+                __syncthreads();
+            }
+        }
+        // P in 16 bits, as the matrix instruction takes it: 2^-9 (bf16) or 2^-12 (fp16) of each weight
+#pragma unroll
+        for (int ks = 0; ks < kTK / 16; ++ks) {
+            uint32_t pa[4];
+            pa[0] = pack16<F16>(s[2 * ks][0], s[2 * ks][1]);
+            pa[1] = pack16<F16>(s[2 * ks][2], s[2 * ks][3]);
+            pa[2] = pack16<F16>(s[2 * ks + 1][0], s[2 * ks + 1][1]);
+            pa[3] = pack16<F16>(s[2 * ks + 1][2], s[2 * ks + 1][3]);
+#pragma unroll
+            for (int n = 0; n < DH / 16; ++n) {
+                uint32_t b[4];
+                ldsm4_t(b, Vs + (16 * ks + 8 * (mi & 1) + lr) * SK + 16 * n + 8 * (mi >> 1));
+                mma16<F16>(acc[2 * n], pa, b[0], b[1]);
+                mma16<F16>(acc[2 * n + 1], pa, b[2], b[3]);
+            }
+        }
+        __syncthreads();
+    }
+    cp_async_wait<0>();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+        l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+    }
+    auto out_row = [&](int rr) { return a.out + (size_t)(o.row0 + rr / G) * a.out_ld + (size_t)(j * G + rr % G) * DH; };
+    if (splits == 1) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int rr = r0 + 16 * warp + g + 8 * h;
+            if (rr >= n_rows) continue;
+            const float inv = l[h] == 0.0f ? 0.0f : 1.0f / l[h];
+            uint16_t* to = out_row(rr);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                *reinterpret_cast<uint32_t*>(to + 8 * n + 2 * tq) = pack16<F16>(acc[n][2 * h] * inv, acc[n][2 * h + 1] * inv);
+        }
+        return;
+    }
+    // a split's record: [64][DH] sums, then [64] maxima and [64] sums of weights
+    const int unit = blockIdx.x * gridDim.y + j;
+    constexpr int REC = kTR * (DH + 2);
+    float* rec = a.partial + ((size_t)unit * splits + split) * REC;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int r = 16 * warp + g + 8 * h;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            *reinterpret_cast<float2*>(rec + r * DH + 8 * n + 2 * tq) = make_float2(acc[n][2 * h], acc[n][2 * h + 1]);
+        if (tq == 0) {
+            rec[kTR * DH + r] = m[h];
+            rec[kTR * DH + kTR + r] = l[h];
+        }
+    }
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) {
+        last_flag = atomicAdd(a.merge + unit, 1) == splits - 1;
+        if (last_flag) a.merge[unit] = 0;
+    }
+    __syncthreads();
+    if (!last_flag) return;
+    __threadfence();
+    const float* all = a.partial + (size_t)unit * splits * REC;
+    for (int idx = tid; idx < kTR * (DH / 4); idx += kTThreads) {
+        const int r = idx / (DH / 4), d = 4 * (idx % (DH / 4));
+        if (r0 + r >= n_rows) break;
+        float top = -INFINITY;
+        for (int sp = 0; sp < splits; ++sp) top = fmaxf(top, __ldcg(all + (size_t)sp * REC + kTR * DH + r));
+        if (top == -INFINITY) top = 0.0f;
+        float w_sum = 0.0f, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int sp = 0; sp < splits; ++sp) {
+            const float* p = all + (size_t)sp * REC;
+            const float ls = __ldcg(p + kTR * DH + kTR + r);
+            if (ls == 0.0f) continue;   // the split saw nothing for this row
+            const float w = exp2_approx(__ldcg(p + kTR * DH + r) - top);
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(p + r * DH + d));
+            w_sum = fmaf(ls, w, w_sum);
+            v[0] = fmaf(x.x, w, v[0]); v[1] = fmaf(x.y, w, v[1]);
+            v[2] = fmaf(x.z, w, v[2]); v[3] = fmaf(x.w, w, v[3]);
+        }
+        const float inv = w_sum == 0.0f ? 0.0f : 1.0f / w_sum;
+        *reinterpret_cast<uint2*>(out_row(r0 + r) + d) =
+            make_uint2(pack16<F16>(v[0] * inv, v[1] * inv), pack16<F16>(v[2] * inv, v[3] * inv));
+    }
+}
+
+template <int DH, bool F16>
+static cudaError_t launch_tiles_t(const PagedAttnArgs& a, cudaStream_t s) {
+    auto kern = paged_tile_kernel<DH, F16>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)tile_smem_bytes<DH>());
+    if (e != cudaSuccess) return e;
+    const long long G = a.c.Hq / a.c.Hk;
+    // at most: every session's last tile may be part-filled
+    const long long tiles = a.cu_rows ? (a.rows * G + kTR - 1) / kTR + a.batch : a.batch * ((G + kTR - 1) / kTR);
+    const long long units = tiles * a.c.Hk, most = 2LL * a.num_sms;
+    const int splits = units < most ? (int)(most / units < 64 ? most / units : 64) : 1;
+    if (tiles > INT32_MAX || a.c.Hk > 65535) return cudaErrorInvalidValue;
+    kern<<<dim3((unsigned)tiles, (unsigned)a.c.Hk, (unsigned)splits), kTThreads, tile_smem_bytes<DH>(), s>>>(a, splits);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_paged_tiles(const PagedAttnArgs& a, cudaStream_t s) {
+    switch (a.c.Dh) {
+        case 32: return a.f16 ? launch_tiles_t<32, true>(a, s) : launch_tiles_t<32, false>(a, s);
+        case 64: return a.f16 ? launch_tiles_t<64, true>(a, s) : launch_tiles_t<64, false>(a, s);
+        case 128: return a.f16 ? launch_tiles_t<128, true>(a, s) : launch_tiles_t<128, false>(a, s);
+        case 256: return a.f16 ? launch_tiles_t<256, true>(a, s) : launch_tiles_t<256, false>(a, s);
+    }
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace vc

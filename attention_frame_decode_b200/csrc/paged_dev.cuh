@@ -1,0 +1,121 @@
+// paged_dev.cuh -- device helpers of the paged attention kernels.
+#pragma once
+#include "common.cuh"
+#include "paged.cuh"
+
+namespace vc {
+
+VC_DEV void cp_async16(void* dst_smem, const void* src, bool valid) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst_smem)), "l"(src),
+                 "r"(valid ? 16 : 0)
+                 : "memory");
+}
+VC_DEV void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+VC_DEV void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+VC_DEV void ldsm4(uint32_t (&r)[4], const void* p) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(smem_u32(p)));
+}
+VC_DEV void ldsm4_t(uint32_t (&r)[4], const void* p) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(smem_u32(p)));
+}
+
+template <bool F16>
+VC_DEV void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (F16) mma_f16(d, a, b0, b1);
+    else mma_bf16(d, a, b0, b1);
+}
+
+// two fp32 values as a pair of 16-bit ones (lo in the low half), each rounded once to nearest even
+template <bool F16>
+VC_DEV uint32_t pack16(float lo, float hi) {
+    if constexpr (F16) {
+        const __half2 v = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    } else {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    }
+}
+template <bool F16>
+VC_DEV float unpack16(uint16_t u) {
+    if constexpr (F16) return __half2float(*reinterpret_cast<const __half*>(&u));
+    else return bf16_bits_to_f(u);
+}
+template <bool F16>
+VC_DEV constexpr uint32_t exponent_mask() { return F16 ? 0x7C00u : 0x7F80u; }
+// whether either half of a pair of 16-bit values is an infinity or NaN
+template <bool F16>
+VC_DEV bool nonfinite2(uint32_t u) {
+    constexpr uint32_t m = exponent_mask<F16>();
+    return (u & m) == m || ((u >> 16) & m) == m;
+}
+
+VC_DEV float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// the page of column `col` of session s, or -1 where it has none (or a bad one)
+VC_DEV int page_of(const PagedKv& c, int s, int col) {
+    const int e = c.table[(size_t)s * c.columns + col];
+    return (unsigned)e < (unsigned)c.pages ? e : -1;
+}
+
+// one session of an attention call
+struct AttnSession {
+    int s;      // its index in the cache
+    int row0;   // its first row
+    int n;      // its rows
+    int p0;     // the first row's position
+};
+
+VC_DEV int session_rows(const PagedAttnArgs& a, int i) {
+    if (!a.cu_rows) return 1;
+    const int n = a.cu_rows[i + 1] - a.cu_rows[i];
+    return n < 0 ? 0 : min(n, a.rows);
+}
+
+// fills in session i; false where it is skipped (VC_DEV_INVALID where the caller's indices do not fit)
+VC_DEV bool attn_session(const PagedAttnArgs& a, int i, AttnSession& o) {
+    o.s = a.seqs ? a.seqs[i] : i;
+    o.row0 = a.cu_rows ? a.cu_rows[i] : i;
+    const int end = a.cu_rows ? a.cu_rows[i + 1] : i + 1;
+    o.p0 = a.pos[i];
+    o.n = end - o.row0;
+    if (o.n == 0 || o.p0 < 0) return false;
+    bool ok = (unsigned)o.s < (unsigned)a.c.seqs && o.row0 >= 0 && end <= a.rows && o.n > 0;
+    if (ok) {
+        const int len = min(a.c.len[o.s], a.c.columns << a.c.page_shift);
+        ok = o.p0 <= len - o.n;
+    }
+    if (!ok) atomicOr(a.c.status, VC_DEV_INVALID);
+    return ok;
+}
+
+// the key blocks of BK positions that queries at positions p_lo..p_hi can see: those of the sinks, then those
+// from the window's start on
+struct KeyBlocks {
+    int n_sink, start, total;
+    VC_DEV int block(int i) const { return i < n_sink ? i : start + (i - n_sink); }
+};
+template <int BK>
+VC_DEV KeyBlocks key_blocks(int window, int sinks, int p_lo, int p_hi) {
+    KeyBlocks k{0, 0, 0};
+    const int end = p_hi / BK + 1;
+    if (window > 0) {
+        k.n_sink = (min(sinks, p_hi + 1) + BK - 1) / BK;
+        k.start = max(p_lo - window + 1, 0) / BK;   // p_lo, window >= 0: no overflow
+        if (k.start < k.n_sink) k.start = k.n_sink;
+    }
+    k.total = k.n_sink + max(end - k.start, 0);
+    return k;
+}
+
+}  // namespace vc

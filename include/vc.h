@@ -54,6 +54,7 @@ typedef enum {
 #define VC_DEV_CAPACITY 1   /* a session's KV cache was full; its step was skipped */
 #define VC_DEV_NONFINITE 2  /* a non-finite logit was produced */
 #define VC_DEV_TIMEOUT 4    /* an internal bounded wait ran out */
+#define VC_DEV_INVALID 8    /* a paged call met a bad index or length on the device; that row was skipped */
 
 /* weight storage formats (weight-only, per-group along K) */
 typedef enum {
@@ -322,6 +323,109 @@ vc_status vc_debug_gemv_noalloc(const vc_qmat* w, const void* act, int act_ld, i
 vc_status vc_gemv_noalloc_status(int32_t* status, vc_stream_t stream);
 /* zeroes the no-allocation GEMV's counters and status word on `stream` (a device memset) */
 vc_status vc_gemv_noalloc_reset(vc_stream_t stream);
+
+/* ---- paged KV cache: windowed attention and page calls --------------------------------- */
+
+/* A KV cache in pages, shared by the sessions of a server (device memory, caller-owned).  It has what
+ * sessions that run without end need next to vc_state's fixed rows: attention over a sliding window
+ * with a few first frames that stay visible (sinks), pages given back as the window leaves them, and
+ * sessions that share the pages of a common opening context.  The backbone's attention has no
+ * positional encoding ("pre-RMSNorm residual stack ..." above), so that a window needs no rotation.
+ *   k, v    16-bit [layers][pages][kv_heads][page_size][head_dim]; bf16, or fp16 where f16 is not 0
+ *   table   int32 [seqs][columns]: the page of a session's positions column * page_size ..., -1: none
+ *   len     int32 [seqs]: positions a session holds
+ *   refs    int32 [pages]: how many table entries name the page; 0: the page is free
+ *   status  int32 [1]: device status word (VC_DEV_* bits), never cleared by the library
+ *   workspace  vc_paged_workspace_bytes(kv) bytes, zeroed by the caller before first use; every call
+ *              leaves its counters zero.  Calls that share it run one after another (one stream, or
+ *              ordered streams; that goes for captured graphs too).  A call that set VC_DEV_TIMEOUT
+ *              leaves it undefined: zero it again.
+ * A new cache has table -1, len 0 and refs 0.  page_size: a power of two, 16..256; head_dim: 32, 64,
+ * 128 or 256; kv_heads divides q_heads; columns * page_size is at most 2^30; seqs * columns, seqs * kv_heads and
+ * pages * kv_heads * page_size are below 2^31.  window: a query at position p sees the keys
+ * t <= p with t < sinks or t > p - window; 0: every t <= p.  window and sinks stay as they are while
+ * sessions hold pages.  A key whose page is not in the table is not seen. */
+typedef struct {
+    void *k, *v;
+    int32_t *table, *len, *refs, *status;
+    void* workspace;
+    size_t workspace_bytes;
+    int layers, pages, page_size, kv_heads, head_dim, q_heads, f16;
+    int seqs, columns, window, sinks;
+} vc_paged_kv;
+
+/* bytes of device workspace the calls on this cache need; 0 for sizes outside the limits above
+ * (pointers are not looked at) */
+size_t vc_paged_workspace_bytes(const vc_paged_kv* kv);
+
+/* Sets the lengths of n sessions: row i takes session seqs[i] (NULL: session i) to the length
+ * (lens ? lens[i] : its length) + add, in three steps on the device.
+ *   1. Pages behind the new length are released, and those that no query from the row's first new
+ *      position on can see: whole pages behind the sinks and at or below (that position - window).
+ *   2. A row that grows asks for its new pages, and, where the page that it will write next is shared,
+ *      for a copy of that page (the positions it holds are copied in every layer).  Requests are
+ *      served in row order, each session's in order of position, from the lowest free page up.
+ *   3. pos[i] = the first position whose rows the caller may write now, min(old, new length), or -1:
+ *      too few free pages or columns (the length stays; VC_DEV_CAPACITY) or a bad row (a session out
+ *      of range or named by an earlier row, a length below 0 or inside a page that the window has
+ *      given up; nothing happens; VC_DEV_INVALID).
+ * A length of 0 frees a session.  Positions that the window has given up are gone: a session cut back
+ * to a page's border among them does not see them again.  seqs, lens: int32 [n] (device) or NULL; pos: int32 [n]
+ * (device) or NULL; 1 <= n <= seqs.  At most two launches; no host synchronization. */
+vc_status vc_paged_resize(const vc_paged_kv* kv, int n, const int32_t* seqs, const int32_t* lens, int add,
+                          int32_t* pos, vc_stream_t stream);
+
+/* Dense per-session state that a fork copies beside the pages (vc_state's ssm, conv and ctx_len):
+ * `outer` blocks outer_stride bytes apart, in each a session's `bytes` bytes at stride bytes times its
+ * index.  Sizes and strides are multiples of 4 bytes, base is 16-byte aligned. */
+typedef struct {
+    void* base;
+    int64_t bytes, stride, outer_stride;
+    int outer;
+} vc_session_part;
+
+/* n sessions become copies of others: session dst[i] gives back its pages, then shares src[i]'s whole
+ * pages (refs + 1) and gets a page of its own for a last, partly filled one (its positions are copied in
+ * every layer), src[i]'s length, and its state in each of parts (host array of n_parts, at most 8).
+ * Several rows may have the same src.  Free pages are taken in row order from the lowest up.  done[i] =
+ * 1, or 0: no free page (dst is left empty; VC_DEV_CAPACITY) or a bad row (an index out of range, a dst
+ * that an earlier row names or that is any row's src; nothing happens; VC_DEV_INVALID).  src, dst: int32
+ * [n] (device); done: int32 [n] (device) or NULL; 1 <= n <= seqs. */
+vc_status vc_paged_fork(const vc_paged_kv* kv, int n, const int32_t* src, const int32_t* dst,
+                        const vc_session_part* parts, int n_parts, int32_t* done, vc_stream_t stream);
+
+/* Moves the pages in use to the front: with L pages in use, the k-th lowest of those at L and above goes to
+ * the k-th lowest free page below L, in every layer; the tables and refs follow.  live[0] = L (device int32, or NULL):
+ * the pages from L on are free and may be given back.  Freed pages keep their bytes. */
+vc_status vc_paged_compact(const vc_paged_kv* kv, int32_t* live, vc_stream_t stream);
+
+/* Rows of one attention call: row r of session i (cu_rows[i] <= r < cu_rows[i + 1]; cu_rows NULL: row i)
+ * stands at position pos[i] + r - cu_rows[i].
+ *   q, out  16-bit [rows][q_heads][head_dim], k, v [rows][kv_heads][head_dim], of the cache's type; the
+ *           strides count elements from row to row (multiples of 8, at least a row), so that slices of
+ *           one fused projection do.  k and v are written to their pages before anything attends; both
+ *           NULL: the pages hold these positions already.  out overlaps none of the inputs.
+ *   seqs    int32 [batch] (device): sessions, each named once where k and v are given; NULL: 0..batch-1
+ *   pos     int32 [batch] (device): as vc_paged_resize leaves it; a session with pos < 0 is skipped
+ *   rows    rows in the buffers; rows from cu_rows[batch] on are left as they are
+ *   scale   factor of q.k before the softmax; 0: 1 / sqrt(head_dim) */
+typedef struct {
+    const void *q, *k, *v;
+    void* out;
+    int64_t q_stride, k_stride, v_stride, out_stride;
+    const int32_t *seqs, *pos, *cu_rows;
+    int batch, rows;
+    float scale;
+} vc_attn_rows;
+
+/* Appends the rows' keys and values to one layer's pages and attends, for prompts (many rows of a session) and
+ * single frames (cu_rows NULL): out = sum_t softmax_t(scale q.k_t) v_t over the keys that the row
+ * sees, GQA (query head i reads KV head i kv_heads / q_heads).  Products accumulate in fp32 and so do
+ * the softmax's maximum and sum; out is rounded once.  A row that sees no key gets 0; keys that a
+ * row does not see do not touch it, whatever they hold.  A session is skipped, and its rows of out left, where pos < 0, or
+ * where its index, rows, length or columns do not fit (VC_DEV_INVALID).  1 <= batch <= kv->seqs,
+ * 1 <= rows (rows == batch where cu_rows is NULL). */
+vc_status vc_paged_attend(const vc_paged_kv* kv, int layer, const vc_attn_rows* rows, vc_stream_t stream);
 
 /* Releases the handle and what the library owns for it (host objects, CUDA graphs, its streams
  * and events); the caller's device memory (weights, state, workspace) is left to the caller.
