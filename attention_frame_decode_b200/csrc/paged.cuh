@@ -53,6 +53,8 @@ struct PagedAttnArgs {
 
 cudaError_t launch_paged_append(const PagedAttnArgs& a, cudaStream_t s);
 cudaError_t launch_paged_tiles(const PagedAttnArgs& a, cudaStream_t s);
+// one row per session, appended and attended in one launch; cudaErrorNotSupported: the shape is not covered
+cudaError_t launch_paged_frames(const PagedAttnArgs& a, cudaStream_t s);
 
 cudaError_t launch_paged_resize(const PagedKv& c, const PagedWorkspace& w, int n, const int* seqs, const int* lens,
                                 int add, int* pos, cudaStream_t s);
