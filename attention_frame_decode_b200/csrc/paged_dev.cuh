@@ -56,6 +56,10 @@ VC_DEV bool nonfinite2(uint32_t u) {
     return (u & m) == m || ((u >> 16) & m) == m;
 }
 
+VC_DEV void tma_prefetch_map(const void* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
 VC_DEV float exp2_approx(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -88,13 +92,11 @@ VC_DEV bool attn_session(const PagedAttnArgs& a, int i, AttnSession& o) {
     o.row0 = a.cu_rows ? a.cu_rows[i] : i;
     const int end = a.cu_rows ? a.cu_rows[i + 1] : i + 1;
     o.p0 = a.pos[i];
+    const bool known = (unsigned)o.s < (unsigned)a.c.seqs;
+    const int len = min(a.c.len[known ? o.s : 0], a.c.columns << a.c.page_shift);   // read along with the others
     o.n = end - o.row0;
     if (o.n == 0 || o.p0 < 0) return false;
-    bool ok = (unsigned)o.s < (unsigned)a.c.seqs && o.row0 >= 0 && end <= a.rows && o.n > 0;
-    if (ok) {
-        const int len = min(a.c.len[o.s], a.c.columns << a.c.page_shift);
-        ok = o.p0 <= len - o.n;
-    }
+    const bool ok = known && o.row0 >= 0 && end <= a.rows && o.n > 0 && o.p0 <= len - o.n;
     if (!ok) atomicOr(a.c.status, VC_DEV_INVALID);
     return ok;
 }

@@ -4,14 +4,14 @@
 // each, and does 4 G Dh flops on them (G = q_heads / kv_heads query heads share them).
 //
 // The work of all sessions is one line of units (session, KV head, block of BK keys), cut into equal ranges, one
-// CTA per SM: however ragged the sessions are, every SM reads the same amount.  In a CTA the units go round the
-// warps; each warp keeps a ring of TMA copies ahead of it (K and V blocks, swizzled rows, fetched page by
-// page through the table) and its own running maximum, sum and output of the softmax in registers.  The products
+// for each warp of one CTA per SM: however ragged the sessions are, every SM reads the same amount.  A warp goes
+// through its range without meeting another: it keeps a ring of TMA copies ahead of it (K and V blocks, swizzled
+// rows, fetched page by page through the table) and the running maximum, sum and output of the softmax in registers.  The products
 // run on warp-level matrix instructions with the keys (then the head dims) as the 16 rows and the query heads as
 // the 8 columns, S^T = K Q^T and O^T = V^T P^T: up to 8 heads waste no row, and P^T is S^T's registers transposed.
-// At the end of a (session, KV head) the warps join through shared memory; where a range ends inside one, the
-// CTAs that share it leave records, and the last of them to arrive joins these in order, so that results do not
-// depend on timing.
+// A (session, KV head) inside a range is written where it ends; one that ranges share leaves a record from each:
+// the CTA joins its warps' records at the end, and where CTAs share it the last of them to arrive joins theirs, in
+// order, so that results do not depend on timing.
 // The weights go into the products as a 16-bit value and the 16-bit rest of it: the error of a weight is
 // 2^-16 (bf16), and the products are not what this kernel waits for.
 #include "paged_dev.cuh"
@@ -21,6 +21,9 @@ namespace vc {
 
 static constexpr int kFMaxStages = 4;
 static constexpr int kFMaxBatch = 2048;
+// Whole (session, KV head)s go to warps, and no join is needed, where that gives no warp more than this many units
+// over an equal share: a join costs about as much as four units (2 us).
+static constexpr int kWholeUnits = 4;
 
 template <int DH>
 struct FrameShape {
@@ -50,7 +53,7 @@ template <int DH>
 static FrameLayout frame_layout(int G, int batch, int grid) {
     using S = FrameShape<DH>;
     FrameLayout L{};
-    const int comb = S::WARPS * G * (S::CS + 2) * 4, weights = grid * (2 * G + 1) * 4, sessions = (batch + 1) * 16;
+    const int comb = S::WARPS * ((G * (S::CS + 2) + 3) & ~3) * 4, weights = grid * (2 * G + 1) * 4, sessions = (batch + 1) * 16;
     const int rest = comb + weights + sessions + 1024 + 64;
     L.stages = (227 * 1024 - rest - 512) / (S::WARPS * S::STAGE);
     if (L.stages > kFMaxStages) L.stages = kFMaxStages;
@@ -81,21 +84,31 @@ __global__ void __launch_bounds__(FrameShape<DH>::THREADS, 1)
     constexpr int BK = S::BK, KT = BK / 16, MT = DH / 16, CS = S::CS, kWarps = S::WARPS, kThreads = S::THREADS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    float* comb = reinterpret_cast<float*>(smem + L.off_comb);        // [warps][G][CS], then [warps][G][2]
+    float* comb = reinterpret_cast<float*>(smem + L.off_comb);        // records: [warps]{[G][CS], [G][2]}
     float* wts = reinterpret_cast<float*>(smem + L.off_weights);      // [CTAs][G][2], then [CTAs] records
     LineSession* line = reinterpret_cast<LineSession*>(smem + L.off_sessions);   // [batch + 1]
     __shared__ uint64_t full[kWarps][kFMaxStages];
     __shared__ uint32_t stage_mapped[kWarps][kFMaxStages];
-    __shared__ int warp_total[kWarps], last_flag;
+    __shared__ int warp_total[kWarps], warp_most[kWarps];
+    __shared__ int4 open_seg[2];   // what the CTA shares at its range's start and end: first unit, end, row, KV head
+    __shared__ int open_last[2];   // whether this CTA arrived last
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tq = lane & 3;
     const int G = a.c.Hq / a.c.Hk, Hk = a.c.Hk;
-    if (lane == 0)
+    pdl_trigger();
+    if (lane == 0) {
         for (int s = 0; s < L.stages; ++s) mbar_init(&full[warp][s], 1);
-    fence_mbar_init();
+        fence_mbar_init();
+    }
+    if (tid == 0) {
+        tma_prefetch_map(&tmK);
+        tma_prefetch_map(&tmV);
+    }
+    if (tid < 2) open_seg[tid] = make_int4(0, 0, 0, 0);
+    pdl_wait();
 
     // the line's sessions (every CTA lays out the same line)
-    int units = 0;
+    int units = 0, heads_total = 0, most = 0;   // (session, KV head)s that have units, the most units of one
     for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
         const int b = b0 + tid;
         LineSession me{0, 0, 0, 0};
@@ -113,26 +126,58 @@ __global__ void __launch_bounds__(FrameShape<DH>::THREADS, 1)
             const int u = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += u;
         }
-        if (lane == 31) warp_total[warp] = incl;
+        const int top = __reduce_max_sync(0xffffffffu, me.blocks);
+        if (lane == 31) {
+            warp_total[warp] = incl;
+            warp_most[warp] = top;
+        }
         __syncthreads();
         int before = units;
         for (int w = 0; w < kWarps; ++w) {
             if (w < warp) before += warp_total[w];
             units += warp_total[w];
+            most = max(most, warp_most[w]);
         }
         me.first = before + incl - me.blocks * Hk;
         if (b < a.batch) line[b] = me;
-        __syncthreads();
+        heads_total += Hk * __syncthreads_count(me.blocks > 0);
     }
     if (tid == 0) line[a.batch] = LineSession{units, 0, 0, 0};
     __syncthreads();
     if (units == 0) return;
 
-    const long long grid = min((int)gridDim.x, units);   // ranges, none of them empty
-    if (blockIdx.x >= grid) return;
-    auto range_start = [&](long long c) { return (int)(c * units / grid); };
-    auto owner = [&](int x) { return (int)((((long long)x + 1) * grid - 1) / units); };
-    const int c0 = range_start(blockIdx.x), c1 = range_start(blockIdx.x + 1);
+    const int all_warps = (int)gridDim.x * kWarps;
+    const bool whole_heads = most - (heads_total <= all_warps ? units / all_warps : 0) <= kWholeUnits;
+    // ranges of a unit at least (short lines: fewer records to join), the first `more` one unit longer
+    const int ctas = whole_heads ? (int)gridDim.x : max(1, min((int)gridDim.x, units / kWarps));
+    if ((int)blockIdx.x >= ctas) return;
+    const int ranges = ctas * kWarps, share = units / ranges, more = units - share * ranges;
+    auto range_start = [&](int c) { return c * share + min(c, more); };
+    auto owner = [&](int x) {
+        const int cut = more * (share + 1);
+        return x < cut ? x / (share + 1) : more + (x - cut) / max(share, 1);
+    };
+    auto session_at = [&](int x) {   // the last session that starts at or before unit x
+        int lo = 0, hi = a.batch - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (line[mid].first <= x) lo = mid;
+            else hi = mid - 1;
+        }
+        return lo;
+    };
+    const int range0 = whole_heads ? 0 : (int)blockIdx.x * kWarps;   // the CTA's first range
+    const int range = whole_heads ? warp * (int)gridDim.x + (int)blockIdx.x : range0 + warp;
+    int c0 = range_start(range), c1 = range_start(range + 1);
+    if (whole_heads) {   // the (session, KV head)s whose first unit lies in the range
+        auto next_head = [&](int x) {
+            if (x >= units) return units;
+            const LineSession me = line[session_at(x)];
+            return me.first + (x - me.first + me.blocks - 1) / me.blocks * me.blocks;
+        };
+        c0 = next_head(c0);
+        c1 = next_head(c1);
+    }
 
     // a place on the line: a unit is block `blk` of session b's KV head j
     struct Place {
@@ -152,51 +197,54 @@ __global__ void __launch_bounds__(FrameShape<DH>::THREADS, 1)
             }
         }
     };
-    Place here{0, 0, 0};   // the CTA's first unit
-    {
-        int lo = 0, hi = a.batch - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (line[mid].first <= c0) lo = mid;
-            else hi = mid - 1;
-        }
-        const int rel = c0 - line[lo].first, n = line[lo].blocks;
-        here = Place{lo, rel / n, rel % n};
+    Place here{0, 0, 0};   // the range's first unit
+    if (c0 < c1) {
+        const int b = session_at(c0), rel = c0 - line[b].first, n = line[b].blocks;
+        here = Place{b, rel / n, rel % n};
     }
 
-    // ---- this warp's copies: unit c0 + warp + WARPS i is copy i, in ring slot i % stages ----
+    // ---- this warp's copies: unit c0 + i is copy i, in ring slot i % stages ----
     uint8_t* ring = smem + (size_t)warp * L.stages * S::STAGE;
-    const int box_rows = min(a.c.page, BK), boxes = BK / box_rows;
-    int copy_x = c0 + warp, copy_slot = 0, look_x = copy_x, issued = 0;
+    const int box_rows = min(a.c.page, BK), boxes = BK / box_rows, batch = 32 / boxes;
+    const int copies = max(c1 - c0, 0);
+    int copy = 0, copy_slot = 0, looked = 0;
     Place look = here;
-    if (look_x < c1) forward(look, warp);
-    // looks up the pages of the next copy but those looked up before; lane q < boxes gets the pool row of its q-th
-    // box, -1: no page
-    auto look_up = [&]() {
-        int pool_row = -1;
-        if (look_x < c1) {
-            const LineSession me = line[look.b];
-            const KeyBlocks kb = key_blocks<BK>(a.c.window, a.c.sinks, me.p, me.p);
-            const int t = kb.block(look.blk) * BK + lane * box_rows;
-            if (lane < boxes && t <= me.p) {
-                const int e = page_of(a.c, me.s, t >> a.c.page_shift);
-                if (e >= 0) pool_row = (e * Hk + look.j) * a.c.page + (t & (a.c.page - 1));
-            }
-            look_x += kWarps;
-            if (look_x < c1) forward(look, kWarps);
-        }
-        return pool_row;
+    // looks up the pages of the next `batch` copies: lane batch i + q gets the table entry of copy i's q-th box
+    // (-1: none) and its row within the page; two batches are held, so that no copy waits for its entry
+    struct Look {
+        int entry, row;
     };
-    auto issue = [&](int pool_row) {   // starts the copy of a look-up, in order
-        if (copy_x >= c1) return;
-        const unsigned mapped = __ballot_sync(0xffffffffu, pool_row >= 0);
+    auto look_up = [&]() {
+        Look o{-1, 0};
+        const int i = lane / boxes;
+        if (looked + i < copies) {
+            Place u = look;
+            if (i) forward(u, i);
+            const LineSession me = line[u.b];
+            const KeyBlocks kb = key_blocks<BK>(a.c.window, a.c.sinks, me.p, me.p);
+            const int t = kb.block(u.blk) * BK + (lane & (boxes - 1)) * box_rows;
+            o.row = u.j * a.c.page + (t & (a.c.page - 1));
+            if (t <= me.p) o.entry = a.c.table[(size_t)me.s * a.c.columns + (t >> a.c.page_shift)];
+        }
+        looked += batch;
+        if (looked < copies) forward(look, batch);
+        return o;
+    };
+    Look now = look_up(), next = look_up();
+    auto issue = [&]() {   // starts the next copy
+        if (copy >= copies) return;
+        const int from = copy % batch * boxes + (lane & (boxes - 1));
+        const int entry = __shfl_sync(0xffffffffu, now.entry, from), row = __shfl_sync(0xffffffffu, now.row, from);
+        const bool there = lane < boxes && (unsigned)entry < (unsigned)a.c.pages;
+        const unsigned mapped = __ballot_sync(0xffffffffu, there);
         uint64_t* bar = &full[warp][copy_slot];
         if (lane == 0) {
             stage_mapped[warp][copy_slot] = mapped;
             mbar_arrive_expect_tx(bar, (uint32_t)(__popc(mapped) * box_rows * DH * 4));
         }
         __syncwarp();
-        if (pool_row >= 0) {
+        if (there) {
+            const int pool_row = entry * Hk * a.c.page + row;
             uint8_t* to = ring + copy_slot * S::STAGE + lane * box_rows * S::ROWB;
 #pragma unroll
             for (int part = 0; part < S::PARTS; ++part) {
@@ -204,27 +252,26 @@ __global__ void __launch_bounds__(FrameShape<DH>::THREADS, 1)
                 tma_load_2d(to + S::KBYTES + part * (BK * 128), &tmV, part * 64, pool_row, bar);
             }
         }
-        copy_x += kWarps;
         copy_slot = copy_slot + 1 == L.stages ? 0 : copy_slot + 1;
-        ++issued;
+        if (++copy % batch == 0) {
+            now = next;
+            next = look_up();
+        }
     };
-    {
-        int rows[kFMaxStages];   // the first copies' table reads are in flight together
-#pragma unroll
-        for (int s = 0; s < kFMaxStages; ++s)
-            if (s < L.stages) rows[s] = look_up();
-#pragma unroll
-        for (int s = 0; s < kFMaxStages; ++s)
-            if (s < L.stages) issue(rows[s]);
-    }
-    int next_row = look_up();   // read while the warp computes
+#pragma unroll 1
+    for (int s = 0; s < L.stages; ++s) issue();
+
+    auto out_at = [&](int row, int j, int r, int d) { return a.out + (size_t)row * a.out_ld + (size_t)(j * G + r) * DH + d; };
+    auto rec_a = [&](int w) { return comb + (size_t)w * ((G * (CS + 2) + 3) & ~3); };   // 16-byte aligned
+    auto rec_b = [&](int w) { return reinterpret_cast<float*>(smem + (size_t)w * L.stages * S::STAGE); };
 
     // ---- units ----
     int slot = 0, phase = 0, used = 0;
     bool alive = true;   // false after a copy that never came: nothing more is computed, the barriers are kept
     const int mi = lane >> 3, lr = lane & 7;
-    int x_seg = c0;
-    while (x_seg < c1) {
+    // what two warps of the CTA share: (first unit, end, row, KV head) of the range's first and last segment
+    int4 seg_first = make_int4(0, 0, 0, 0), seg_last = seg_first;
+    for (int x_seg = c0; x_seg < c1;) {
         const Place at0 = here;   // of unit x_seg
         const int b = at0.b;
         const LineSession me = line[b];
@@ -243,6 +290,14 @@ __global__ void __launch_bounds__(FrameShape<DH>::THREADS, 1)
                     qb[ks][h][1] = 8 * h + g < G ? *reinterpret_cast<const uint32_t*>(qr + 8) : 0u;
                 }
         }
+        // the new row's key and value and its page, for the warp that has the segment's last block
+        uint4 new_k = make_uint4(0u, 0u, 0u, 0u), new_v = new_k;
+        int new_page = -1;
+        if (a.kn && s1 <= c1 && lane < S::CH) {
+            new_k = *reinterpret_cast<const uint4*>(a.kn + (size_t)row * a.k_ld + at0.j * DH + lane * 8);
+            new_v = *reinterpret_cast<const uint4*>(a.vn + (size_t)row * a.v_ld + at0.j * DH + lane * 8);
+            new_page = page_of(a.c, me.s, me.p >> a.c.page_shift);
+        }
         float acc[MT][NH][4];   // O^T: dims 16 mt + g (+ 8) of heads 8 h + 2 tq (+ 1)
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
@@ -255,15 +310,12 @@ __global__ void __launch_bounds__(FrameShape<DH>::THREADS, 1)
             l[h][0] = l[h][1] = 0.0f;
         }
 
-        // the first unit from x_seg on that is this warp's
-        static_assert((kWarps & (kWarps - 1)) == 0, "a power of two");
-        int x = x_seg + ((warp - (x_seg - c0)) & (kWarps - 1));
-        for (; x < end; x += kWarps) {
+        for (int x = x_seg; x < end; ++x) {
             ++used;
             if (alive) {
                 alive = __all_sync(0xffffffffu, mbar_wait(&full[warp][slot], phase, a.c.status));
                 if (!alive)   // the copies behind it are given another bounded while before anyone leaves
-                    for (int k = used, sl = slot, ph = phase; k < issued; ++k) {
+                    for (int k = used, sl = slot, ph = phase; k < copy; ++k) {
                         if (++sl == L.stages) sl = 0, ph ^= 1;
                         mbar_wait(&full[warp][sl], ph, nullptr);
                     }
@@ -287,17 +339,9 @@ __global__ void __launch_bounds__(FrameShape<DH>::THREADS, 1)
                         if (!seen(i / S::CH))
                             *reinterpret_cast<uint4*>(Vs + S::at(i / S::CH, i % S::CH)) = make_uint4(0u, 0u, 0u, 0u);
                     __syncwarp();
-                    if (newest && seen(p - t0) && lane < S::CH) {   // the new row, to its page and into the block
-                        const uint4 kv = *reinterpret_cast<const uint4*>(a.kn + (size_t)row * a.k_ld + at0.j * DH + lane * 8);
-                        const uint4 vv = *reinterpret_cast<const uint4*>(a.vn + (size_t)row * a.v_ld + at0.j * DH + lane * 8);
-                        const int e = page_of(a.c, me.s, p >> a.c.page_shift);
-                        if (e >= 0) {
-                            const size_t to = (((size_t)e * Hk + at0.j) * a.c.page + (p & (a.c.page - 1))) * DH + lane * 8;
-                            *reinterpret_cast<uint4*>(a.c.k + to) = kv;
-                            *reinterpret_cast<uint4*>(a.c.v + to) = vv;
-                        }
-                        *reinterpret_cast<uint4*>(Ks + S::at(p - t0, lane)) = kv;
-                        *reinterpret_cast<uint4*>(Vs + S::at(p - t0, lane)) = vv;
+                    if (newest && new_page >= 0) {   // the new row, into the block
+                        *reinterpret_cast<uint4*>(Ks + S::at(p - t0, lane)) = new_k;
+                        *reinterpret_cast<uint4*>(Vs + S::at(p - t0, lane)) = new_v;
                     }
                     __syncwarp();
                 }
@@ -380,15 +424,21 @@ __global__ void __launch_bounds__(FrameShape<DH>::THREADS, 1)
                 }
                 if (!whole || newest) fence_proxy_async();   // stores to the slot come before the next copy into it
                 __syncwarp();
-                issue(next_row);
-                next_row = look_up();
+                issue();
+                if (newest && new_page >= 0) {   // and to its page
+                    const size_t to = (((size_t)new_page * Hk + at0.j) * a.c.page + (p & (a.c.page - 1))) * DH + lane * 8;
+                    *reinterpret_cast<uint4*>(a.c.k + to) = new_k;
+                    *reinterpret_cast<uint4*>(a.c.v + to) = new_v;
+                }
             }
             if (++slot == L.stages) {
                 slot = 0;
                 phase ^= 1;
             }
         }
-        // ---- the warps' parts of this (session, KV head) ----
+        // ---- the end of the (session, KV head), or of the range ----
+        const bool ends_here = s0 >= c0 && s1 <= c1;
+        float* rec = x_seg == c0 ? rec_a(warp) : rec_b(warp);   // the ring is free where the range ends
 #pragma unroll
         for (int h = 0; h < NH; ++h)
 #pragma unroll
@@ -398,107 +448,138 @@ __global__ void __launch_bounds__(FrameShape<DH>::THREADS, 1)
                 sum += __shfl_xor_sync(0xffffffffu, sum, 8);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 16);
                 const int r = 8 * h + 2 * tq + e;
-                if (r < G) {
-                    float* rec = comb + (size_t)(warp * G + r) * CS;
-                    if (sum != 0.0f)
+                if (r >= G) continue;
+                if (ends_here) {
+                    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                    uint16_t* to = out_at(row, at0.j, r, g);
 #pragma unroll
-                        for (int mt = 0; mt < MT; ++mt) {
-                            rec[16 * mt + g] = acc[mt][h][e];
-                            rec[16 * mt + g + 8] = acc[mt][h][2 + e];
-                        }
-                    if (g == 0) {
-                        float* ml = comb + (size_t)kWarps * G * CS + (size_t)(warp * G + r) * 2;
-                        ml[0] = m[h][e];
-                        ml[1] = sum;
+                    for (int mt = 0; mt < MT; ++mt) {
+                        const uint32_t v = pack16<F16>(acc[mt][h][e] * inv, acc[mt][h][2 + e] * inv);
+                        to[16 * mt] = (uint16_t)v;
+                        to[16 * mt + 8] = (uint16_t)(v >> 16);
                     }
+                } else {
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        rec[r * CS + 16 * mt + g] = acc[mt][h][e];
+                        rec[r * CS + 16 * mt + g + 8] = acc[mt][h][2 + e];
+                    }
+                    if (g == 0) *reinterpret_cast<float2*>(rec + G * CS + 2 * r) = make_float2(m[h][e], sum);
                 }
             }
-        __syncthreads();
-        const bool shared_seg = s0 < c0 || s1 > c1;
-        const int rec_floats = (G * (DH + 2) + 3) & ~3;   // 16-byte aligned records
-        float* rec = a.partial + (size_t)(2 * blockIdx.x + (s0 <= c0 ? 0 : 1)) * rec_floats;
-        const float* ml = comb + (size_t)kWarps * G * CS;
-        auto out_at = [&](int r, int d) { return a.out + (size_t)row * a.out_ld + (size_t)(at0.j * G + r) * DH + d; };
-        for (int i = tid; i < G * (DH / 4); i += kThreads) {
-            const int r = i / (DH / 4), d = 4 * (i % (DH / 4));
-            float top = -INFINITY;
+        if (!ends_here) {
+            seg_last = make_int4(s0, s1, row, at0.j);
+            if (x_seg == c0) seg_first = seg_last;
+        }
+        if (end < c1) forward(here, end - x_seg);
+        x_seg = end;
+    }
+    if (whole_heads) return;
+
+    // ---- the CTA's warps: each joins what begins with it (warp 0: also what began before the CTA) ----
+    __syncthreads();
+    const int rec_floats = (G * (DH + 2) + 3) & ~3;   // 16-byte aligned records
+    const int C0 = range_start(range0), C1 = range_start(range0 + kWarps);
+    auto join_warps = [&](const int4& seg) {
+        const int s0 = seg.x, s1 = seg.y, last = owner(min(s1, C1) - 1) - range0;
+        const bool shared = s0 < C0 || s1 > C1;
+        const int which = s0 <= C0 ? 0 : 1;
+        float* rec = a.partial + (size_t)(2 * blockIdx.x + which) * rec_floats;
+        const float* from[kWarps];
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[(w * G + r) * 2]);
-            const float base = top == -INFINITY ? 0.0f : top;
-            float sum = 0.0f, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int w = 0; w < kWarps; ++w)   // a warp's first segment is in its first record
+            from[w] = w < warp || w > last ? nullptr : s0 <= range_start(range0 + w) ? rec_a(w) : rec_b(w);
+        for (int i = lane; i < G * (DH / 4); i += 32) {
+            const int r = i / (DH / 4), d = 4 * (i % (DH / 4));
+            // a part without a key that is seen has maximum -inf, sum 0 and zeros: its factor is 0
+            float top = -INFINITY, f[kWarps], sum = 0.0f, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
-                const float lw = ml[(w * G + r) * 2 + 1];
-                if (lw == 0.0f) continue;
-                const float f = exp2_approx(ml[(w * G + r) * 2] - base);
-                const float4 y = *reinterpret_cast<const float4*>(comb + ((size_t)w * G + r) * CS + d);
-                sum = fmaf(lw, f, sum);
-                v[0] = fmaf(y.x, f, v[0]); v[1] = fmaf(y.y, f, v[1]);
-                v[2] = fmaf(y.z, f, v[2]); v[3] = fmaf(y.w, f, v[3]);
+                f[w] = from[w] ? from[w][G * CS + 2 * r] : -INFINITY;
+                top = fmaxf(top, f[w]);
             }
-            if (!shared_seg) {
+            const float base = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                if (!from[w]) continue;
+                f[w] = exp2_approx(f[w] - base);
+                const float4 y = *reinterpret_cast<const float4*>(from[w] + r * CS + d);
+                sum = fmaf(from[w][G * CS + 2 * r + 1], f[w], sum);
+                v[0] = fmaf(y.x, f[w], v[0]); v[1] = fmaf(y.y, f[w], v[1]);
+                v[2] = fmaf(y.z, f[w], v[2]); v[3] = fmaf(y.w, f[w], v[3]);
+            }
+            if (!shared) {
                 const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-                *reinterpret_cast<uint2*>(out_at(r, d)) =
+                *reinterpret_cast<uint2*>(out_at(seg.z, seg.w, r, d)) =
                     make_uint2(pack16<F16>(v[0] * inv, v[1] * inv), pack16<F16>(v[2] * inv, v[3] * inv));
             } else {
                 __stcg(reinterpret_cast<float4*>(rec + r * DH + d), make_float4(v[0], v[1], v[2], v[3]));
                 if (d == 0) __stcg(reinterpret_cast<float2*>(rec + G * DH + 2 * r), make_float2(top, sum));
             }
         }
-        if (shared_seg) {
+        if (shared && lane == 0) open_seg[which] = seg;
+    };
+    if (warp == 0 && seg_first.y > seg_first.x) join_warps(seg_first);
+    if (seg_last.y > c1 && seg_last.x >= c0 && !(warp == 0 && seg_last.x <= c0)) join_warps(seg_last);
+
+    // ---- the CTAs ----
+    __syncthreads();
+    if (tid < 2) {
+        const int4 seg = open_seg[tid];
+        int is_last = 0;
+        if (seg.y > seg.x) {
+            __threadfence();   // the CTA's records, ordered by the barrier, before its arrival
+            const int f = owner(seg.x) / kWarps, n = owner(seg.y - 1) / kWarps - f + 1;
+            is_last = atomicAdd(a.merge + f, 1) == n - 1;
+            if (is_last) a.merge[f] = 0;
             __threadfence();
-            __syncthreads();
-            const int f = owner(s0), n = owner(s1 - 1) - f + 1;
-            if (tid == 0) {
-                last_flag = atomicAdd(a.merge + f, 1) == n - 1;
-                if (last_flag) a.merge[f] = 0;
+        }
+        open_last[tid] = is_last;
+    }
+    __syncthreads();
+    for (int which = 0; which < 2; ++which) {
+        if (!open_last[which]) continue;
+        const int4 seg = open_seg[which];
+        const int f = owner(seg.x) / kWarps, n = owner(seg.y - 1) / kWarps - f + 1;
+        // wts[k][r]: the k-th contributor's (maximum, sum), then its factor; its record is that of its range's start
+        // if the segment began there or before
+        int* rec_at = reinterpret_cast<int*>(wts + 2 * n * G);
+        for (int k = tid; k < n; k += kThreads)
+            rec_at[k] = (2 * (f + k) + (seg.x <= range_start((f + k) * kWarps) ? 0 : 1)) * rec_floats;
+        __syncthreads();
+        for (int i = tid; i < n * G; i += kThreads)
+            reinterpret_cast<float2*>(wts)[i] =
+                __ldcg(reinterpret_cast<const float2*>(a.partial + rec_at[i / G] + G * DH + 2 * (i % G)));
+        __syncthreads();
+        for (int r = warp; r < G; r += kWarps) {
+            float top = -INFINITY, sum = 0.0f;
+            for (int k = lane; k < n; k += 32) top = fmaxf(top, wts[2 * (k * G + r)]);
+            top = warp_max(top);
+            if (top == -INFINITY) top = 0.0f;
+            for (int k = lane; k < n; k += 32) {
+                float* w = wts + 2 * (k * G + r);
+                const float f2 = exp2_approx(w[0] - top);
+                sum = fmaf(w[1], f2, sum);
+                w[0] = f2;
             }
-            __syncthreads();
-            if (last_flag) {
-                __threadfence();
-                // wts[k][r]: the k-th contributor's (maximum, sum), then its factor; its record is that of its first
-                // segment if this one began at or before its range
-                int* rec_at = reinterpret_cast<int*>(wts + 2 * n * G);
-                for (int k = tid; k < n; k += kThreads)
-                    rec_at[k] = (2 * (f + k) + (s0 <= range_start(f + k) ? 0 : 1)) * rec_floats;
-                __syncthreads();
-                for (int i = tid; i < n * G; i += kThreads)
-                    reinterpret_cast<float2*>(wts)[i] =
-                        __ldcg(reinterpret_cast<const float2*>(a.partial + rec_at[i / G] + G * DH + 2 * (i % G)));
-                __syncthreads();
-                for (int r = warp; r < G; r += kWarps) {
-                    float top = -INFINITY, sum = 0.0f;
-                    for (int k = lane; k < n; k += 32) top = fmaxf(top, wts[2 * (k * G + r)]);
-                    top = warp_max(top);
-                    if (top == -INFINITY) top = 0.0f;
-                    for (int k = lane; k < n; k += 32) {
-                        float* w = wts + 2 * (k * G + r);
-                        const float f2 = exp2_approx(w[0] - top);
-                        if (w[1] != 0.0f) sum = fmaf(w[1], f2, sum);   // 0: a part without a key that is seen
-                        w[0] = f2;
-                    }
-                    sum = warp_sum(sum);
-                    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-                    for (int k = lane; k < n; k += 32) wts[2 * (k * G + r)] *= inv;
-                }
-                __syncthreads();
-                for (int i = tid; i < G * (DH / 4); i += kThreads) {
-                    const int r = i / (DH / 4), d = 4 * (i % (DH / 4));
-                    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 8
-                    for (int k = 0; k < n; ++k) {
-                        const float4 y = __ldcg(reinterpret_cast<const float4*>(a.partial + rec_at[k] + r * DH + d));
-                        const float w = wts[2 * (k * G + r)];
-                        v[0] = fmaf(y.x, w, v[0]); v[1] = fmaf(y.y, w, v[1]);
-                        v[2] = fmaf(y.z, w, v[2]); v[3] = fmaf(y.w, w, v[3]);
-                    }
-                    *reinterpret_cast<uint2*>(out_at(r, d)) = make_uint2(pack16<F16>(v[0], v[1]), pack16<F16>(v[2], v[3]));
-                }
-            }
+            sum = warp_sum(sum);
+            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+            for (int k = lane; k < n; k += 32) wts[2 * (k * G + r)] *= inv;
         }
         __syncthreads();
-        if (end < c1) forward(here, end - x_seg);
-        x_seg = end;
+        for (int i = tid; i < G * (DH / 4); i += kThreads) {
+            const int r = i / (DH / 4), d = 4 * (i % (DH / 4));
+            float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
+            for (int k = 0; k < n; ++k) {
+                const float4 y = __ldcg(reinterpret_cast<const float4*>(a.partial + rec_at[k] + r * DH + d));
+                const float w = wts[2 * (k * G + r)];
+                v[0] = fmaf(y.x, w, v[0]); v[1] = fmaf(y.y, w, v[1]);
+                v[2] = fmaf(y.z, w, v[2]); v[3] = fmaf(y.w, w, v[3]);
+            }
+            *reinterpret_cast<uint2*>(out_at(seg.z, seg.w, r, d)) = make_uint2(pack16<F16>(v[0], v[1]), pack16<F16>(v[2], v[3]));
+        }
+        __syncthreads();   // the factors' room is used again
     }
 }
 
@@ -517,8 +598,17 @@ static cudaError_t launch_frames_t(const PagedAttnArgs& a, cudaStream_t s) {
     auto kern = a.c.Hq / a.c.Hk <= 8 ? paged_frame_kernel<DH, F16, 1> : paged_frame_kernel<DH, F16, 2>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L.total);
     if (e != cudaSuccess) return e;
-    kern<<<grid, S::THREADS, L.total, s>>>(mk, mv, a, L);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(S::THREADS);
+    cfg.dynamicSmemBytes = L.total;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, mk, mv, a, L);
 }
 
 cudaError_t launch_paged_frames(const PagedAttnArgs& a, cudaStream_t s) {
