@@ -53,6 +53,8 @@ struct PagedAttnArgs {
 
 cudaError_t launch_paged_append(const PagedAttnArgs& a, cudaStream_t s);
 cudaError_t launch_paged_tiles(const PagedAttnArgs& a, cudaStream_t s);
+// the tensor-core form for many rows; cudaErrorNotSupported: the shape is not covered
+cudaError_t launch_paged_prompts(const PagedAttnArgs& a, cudaStream_t s);
 // one row per session, appended and attended in one launch; cudaErrorNotSupported: the shape is not covered
 cudaError_t launch_paged_frames(const PagedAttnArgs& a, cudaStream_t s);
 

@@ -150,6 +150,11 @@ extern "C" vc_status vc_paged_attend(const vc_paged_kv* kv, int layer, const vc_
         if (e != cudaErrorNotSupported) return record_cuda_failure(e, __func__);
     }
     if (a.kn) CKP(launch_paged_append(a, s));
+    if (a.cu_rows) {
+        const cudaError_t e = launch_paged_prompts(a, s);
+        if (e == cudaSuccess) return VC_OK;
+        if (e != cudaErrorNotSupported) return record_cuda_failure(e, __func__);
+    }
     CKP(launch_paged_tiles(a, s));
     return VC_OK;
 }

@@ -16,6 +16,7 @@ namespace vc {
 // read and written per row).
 // ------------------------------------------------------------------------------------------
 __global__ void __launch_bounds__(256) paged_append_kernel(const PagedAttnArgs a) {
+    pdl_trigger();
     const int width = a.c.Hk * a.c.Dh / 8;   // 16-byte chunks per row
     const long long idx = (long long)blockIdx.x * blockDim.x + threadIdx.x;
     const int row = (int)(idx / width), chunk = (int)(idx % width);
@@ -55,31 +56,6 @@ cudaError_t launch_paged_append(const PagedAttnArgs& a, cudaStream_t s) {
 // them in split order.
 // ------------------------------------------------------------------------------------------
 static constexpr int kTR = 64, kTK = 64, kTThreads = 128;
-
-// the session and the tile within it of the launch's `tile`-th tile; false behind the last (a whole warp calls)
-VC_DEV bool find_tile(const PagedAttnArgs& a, int group, int tile_rows, int tile, int& session, int& t) {
-    const int lane = threadIdx.x & 31;
-    long long before = 0;
-    for (int b0 = 0; b0 < a.batch; b0 += 32) {
-        const int b = b0 + lane;
-        const long long mine = b < a.batch ? ((long long)session_rows(a, b) * group + tile_rows - 1) / tile_rows : 0;
-        long long incl = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long u = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += u;
-        }
-        const unsigned hit = __ballot_sync(0xffffffffu, before + incl > tile);
-        if (hit) {
-            const int l = __ffs(hit) - 1;
-            session = b0 + l;
-            t = (int)(tile - (before + __shfl_sync(0xffffffffu, incl - mine, l)));
-            return true;
-        }
-        before += __shfl_sync(0xffffffffu, incl, 31);
-    }
-    return false;
-}
 
 template <int DH>
 static constexpr size_t tile_smem_bytes() { return (size_t)5 * 64 * (DH + 8) * 2; }

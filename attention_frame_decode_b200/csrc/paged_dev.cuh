@@ -120,4 +120,29 @@ VC_DEV KeyBlocks key_blocks(int window, int sinks, int p_lo, int p_hi) {
     return k;
 }
 
+// the session and the tile within it of the launch's `tile`-th tile; false behind the last (a whole warp calls)
+VC_DEV bool find_tile(const PagedAttnArgs& a, int group, int tile_rows, int tile, int& session, int& t) {
+    const int lane = threadIdx.x & 31;
+    long long before = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += 32) {
+        const int b = b0 + lane;
+        const long long mine = b < a.batch ? ((long long)session_rows(a, b) * group + tile_rows - 1) / tile_rows : 0;
+        long long incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long u = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += u;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, before + incl > tile);
+        if (hit) {
+            const int l = __ffs(hit) - 1;
+            session = b0 + l;
+            t = (int)(tile - (before + __shfl_sync(0xffffffffu, incl - mine, l)));
+            return true;
+        }
+        before += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    return false;
+}
+
 }  // namespace vc

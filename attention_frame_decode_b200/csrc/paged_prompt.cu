@@ -1,0 +1,471 @@
+// paged_prompt.cu -- windowed attention over the paged KV cache for prompts, on tcgen05 tensor cores.
+//
+// The packed rows of a session and KV head (paged_attn.cu) are cut into tiles of 256 = two MMA tiles of 128 rows;
+// one CTA per SM takes a tile and walks the blocks of 128 keys that its rows can see.  Per block and MMA tile i:
+//     S_i = Q_i K^T (tcgen05.mma into tensor memory, fp32)
+//     P_i = exp2(scale S_i - m_i), one thread per row, written back to tensor memory as the 16-bit A operand
+//     O_i += P_i V (tcgen05.mma, A from tensor memory)
+// The two tiles alternate: while the threads of one form its weights, the tensor core works on the other's
+// products.  The running maximum moves only when it grew by more than 2^8 (weights up to 2^8 lose no precision in
+// fp32 or the 16-bit formats), so O_i is rarely read back to be rescaled.
+// Bound: the tensor core (4 Dh flops per visible pair) and, as much, the exponentials: a block costs each SM about
+// 2 x 1024 cycles of either.
+// Warps: 0 copies K and V page by page (TMA, 128-byte swizzle) into a ring; 1 issues the MMAs; 2 and 3 clean the
+// values of edge blocks; 4-7 and 8-11 are the rows of the two tiles.
+#include "paged_dev.cuh"
+#include "tc.cuh"
+
+namespace vc {
+
+static constexpr int kPRows = 256, kPKeys = 128, kPThreads = 384;
+
+template <int DH>
+struct PromptShape {
+    static constexpr int HALVES = DH / 64;                    // 64-wide column parts
+    static constexpr int TILE = kPKeys * DH * 2;              // bytes of a K or V block, or of an MMA tile's rows of Q
+    static constexpr int STAGES = DH == 128 ? 5 : 8;          // K and V blocks in turn
+    static constexpr int BYTES = 2 * TILE + STAGES * TILE + 1024;
+    // tensor memory columns: S of each tile, O of each tile; P shares S's columns where all 512 are needed (the MMAs
+    // of one shape run in order, so S of the next block is written after P of this one is read)
+    static constexpr uint32_t S0 = 0, O0 = 256, P0 = DH == 128 ? 0 : 384, P_STEP = DH == 128 ? 128 : 64;
+};
+
+VC_DEV void tc_mma_ta(uint32_t tmem, uint32_t atmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(
+            tmem),
+        "r"(atmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// 16 32-bit values of each lane to 16 consecutive columns
+VC_DEV void tc_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+VC_DEV void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// the low n bits (all for n >= 32, none for n <= 0)
+VC_DEV uint32_t low_bits(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
+
+// what a thread knows of its row
+struct PromptRow {
+    int p, window, sinks;
+    // bit c: whether key t0 + c is seen (c < 32); groups: bit u, whether the 16 keys from t0 + 16 u on have a page
+    VC_DEV uint32_t seen(int t0, uint32_t groups) const {
+        uint32_t v = low_bits(p - t0 + 1);
+        if (window > 0) v &= ~low_bits(p - window + 1 - t0) | low_bits(sinks - t0);
+        return v & (((groups & 1u) ? 0xffffu : 0u) | ((groups & 2u) ? 0xffff0000u : 0u));
+    }
+};
+
+template <int DH, bool F16>
+__global__ void __launch_bounds__(kPThreads, 1)
+    paged_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                        const PagedAttnArgs a, int splits) {
+    using S = PromptShape<DH>;
+    constexpr int ST = S::STAGES;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* Qs = smem;                     // [2 tiles][halves][128 rows][128 B]
+    uint8_t* ring = smem + 2 * S::TILE;     // [stages][halves][128 keys][128 B]
+    __shared__ uint64_t full[ST], empty[ST], clean[4], q_ready, s_full[2], p_ready[2], o_full[2], drained;
+    __shared__ uint32_t tmem_base, block_mapped[16];
+    __shared__ int odd_values, last_flag;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int G = a.c.Hq / a.c.Hk, j = blockIdx.y, split = blockIdx.z;
+    pdl_trigger();
+    if (tid == 0) {
+        tma_prefetch_map(&tmK);
+        tma_prefetch_map(&tmV);
+        for (int s = 0; s < ST; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int s = 0; s < 4; ++s) mbar_init(&clean[s], 64);   // values of block n at n % 4: no more are in the ring
+        mbar_init(&q_ready, 256);
+        mbar_init(&drained, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_ready[i], 128);
+            mbar_init(&o_full[i], 1);
+        }
+        odd_values = 0;
+        fence_mbar_init();
+    }
+    pdl_wait();
+    if (blockIdx.x == 0 && j == 0 && split == 0)   // reports every session whose indices do not fit
+        for (int i = tid; i < a.batch; i += kPThreads) {
+            AttnSession o;
+            attn_session(a, i, o);
+        }
+    int session, tile;
+    if (!find_tile(a, G, kPRows, (int)(gridDim.x - 1 - blockIdx.x), session, tile)) return;   // the longest rows first
+    AttnSession o;
+    if (!attn_session(a, session, o)) return;
+    const int n_rows = o.n * G, r0 = tile * kPRows;
+    const int p_lo = o.p0 + r0 / G, p_hi = o.p0 + (min(r0 + kPRows, n_rows) - 1) / G;
+    const KeyBlocks kb = key_blocks<kPKeys>(a.c.window, a.c.sinks, p_lo, p_hi);
+    const int b0 = (int)((long long)kb.total * split / splits), b1 = (int)((long long)kb.total * (split + 1) / splits);
+    const int nb = b1 - b0;
+
+    if (warp == 1) tmem_alloc(&tmem_base, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base;
+    const int box_rows = min(a.c.page, kPKeys), boxes = kPKeys / box_rows;
+    bool ok = true;
+
+    if (warp == 0) {
+        // ---- copies: K of block 0, V of block 0, K of block 1, ... in ring order ----
+        int entry = -1, issued = 0;
+        auto look_up = [&](int b) {   // lane q < boxes: the table entry of the block's q-th box
+            entry = -1;
+            const int t = b < b1 ? kb.block(b) * kPKeys + lane * box_rows : INT32_MAX;
+            if (lane < boxes && t <= p_hi) entry = page_of(a.c, o.s, t >> a.c.page_shift);
+        };
+        look_up(b0);
+        for (int n = 0; n < nb && ok; ++n) {
+            const int t = kb.block(b0 + n) * kPKeys + lane * box_rows;
+            const bool there = entry >= 0;
+            const unsigned mapped = __ballot_sync(0xffffffffu, there);
+            const int pool_row = (entry * a.c.Hk + j) * a.c.page + (t & (a.c.page - 1));
+            look_up(b0 + n + 1);
+            if (lane == 0) {   // a bit for each 16 keys
+                uint32_t groups = 0;
+                for (int u = 0; u < kPKeys / 16; ++u) groups |= ((mapped >> (16 * u / box_rows)) & 1u) << u;
+                block_mapped[n & 15] = groups;
+            }
+            for (int kv = 0; kv < 2 && ok; ++kv, ++issued) {
+                const int s = issued % ST;
+                if (issued >= ST) ok = __all_sync(0xffffffffu, mbar_wait(&empty[s], (uint32_t)((issued / ST - 1) & 1), a.c.status));
+                if (!ok) break;
+                if (lane == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)(__popc(mapped) * box_rows * DH * 2));
+                __syncwarp();
+                if (there)
+#pragma unroll
+                    for (int h = 0; h < S::HALVES; ++h)
+                        tma_load_2d(ring + s * S::TILE + h * (kPKeys * 128) + lane * box_rows * 128, kv ? &tmV : &tmK, h * 64,
+                                    pool_row, &full[s]);
+            }
+        }
+        // no copy outlives the CTA: after a wait that gave up, each gets another bounded while
+        if (!ok)
+            for (int k = max(0, issued - ST); k < issued; ++k) mbar_wait(&full[k % ST], (uint32_t)((k / ST) & 1), nullptr);
+    } else if (warp == 1) {
+        // ---- products ----
+        if (lane == 0) {
+            constexpr uint32_t ID_S = umma_idesc(!F16, false, 128, kPKeys), ID_O = umma_idesc(!F16, true, 128, DH);
+            auto mma_s = [&](int i, int s) {   // S_i = Q_i K^T
+                const uint32_t q = smem_u32(Qs + i * S::TILE), k = smem_u32(ring + s * S::TILE);
+#pragma unroll
+                for (int c = 0; c < DH / 16; ++c) {
+                    const uint32_t off = (uint32_t)((c >> 2) * (128 * 128) + (c & 3) * 32);
+                    tc_mma(tmem + S::S0 + (uint32_t)(i * 128), desc_sw128(q + off), desc_sw128(k + off), ID_S, c != 0);
+                }
+            };
+            auto mma_o = [&](int i, int s, bool first) {   // O_i += P_i V
+                const uint32_t v = smem_u32(ring + s * S::TILE);
+#pragma unroll
+                for (int c = 0; c < kPKeys / 16; ++c)
+                    tc_mma_ta(tmem + S::O0 + (uint32_t)(i * DH), tmem + S::P0 + (uint32_t)(i * S::P_STEP + c * 8),
+                              umma_desc(v + (uint32_t)(c * 2048), kPKeys * 128, 1024, UMMA_SW128), ID_O, !(first && c == 0));
+            };
+            if (nb > 0) {
+                ok = mbar_wait(&q_ready, 0, a.c.status) && mbar_wait(&full[0], 0, a.c.status);
+                tc_fence_after();
+                if (ok)
+                    for (int i = 0; i < 2; ++i) {
+                        mma_s(i, 0);
+                        tc_commit(&s_full[i]);
+                    }
+                if (ok) tc_commit(&empty[0]);
+            }
+            for (int n = 0; n < nb && ok; ++n) {
+                const int kv = 2 * n + 1, kk = 2 * n + 2, sv = kv % ST, sk = kk % ST;
+                ok = mbar_wait(&full[sv], (uint32_t)((kv / ST) & 1), a.c.status) &&
+                     mbar_wait(&clean[n & 3], (uint32_t)((n >> 2) & 1), a.c.status);
+                if (ok && n + 1 < nb) ok = mbar_wait(&full[sk], (uint32_t)((kk / ST) & 1), a.c.status);
+                for (int i = 0; i < 2 && ok; ++i) {
+                    ok = mbar_wait(&p_ready[i], (uint32_t)(n & 1), a.c.status);
+                    if (!ok) break;
+                    tc_fence_after();
+                    mma_o(i, sv, n == 0);
+                    if (n + 1 < nb) {
+                        mma_s(i, sk);
+                        tc_commit(&s_full[i]);
+                    } else {
+                        tc_commit(&o_full[i]);
+                    }
+                }
+                if (ok) {
+                    tc_commit(&empty[sv]);
+                    if (n + 1 < nb) tc_commit(&empty[sk]);
+                }
+            }
+            if (!ok) {   // no product outlives the tensor memory
+                tc_commit(&drained);
+                mbar_wait(&drained, 0, nullptr);
+            }
+        }
+    } else if (warp < 4) {
+        // ---- values that not every row of the CTA sees: those that no row sees become 0, and so do infinities and
+        // NaN (the rows that see them get them at the end), so that a weight of 0 takes nothing in ----
+        const int t64 = tid - 64;
+        for (int n = 0; n < nb && ok; ++n) {
+            const int kv = 2 * n + 1, s = kv % ST, t0 = kb.block(b0 + n) * kPKeys;
+            ok = __all_sync(0xffffffffu, mbar_wait(&full[s], (uint32_t)((kv / ST) & 1), a.c.status));
+            if (!ok) break;
+            const uint32_t groups = block_mapped[n & 15];
+            const bool whole = groups == 0xffu && t0 + kPKeys - 1 <= p_lo &&
+                               (a.c.window == 0 || t0 > p_hi - a.c.window || t0 + kPKeys - 1 < a.c.sinks);
+            if (!whole) {
+                uint8_t* Vs = ring + s * S::TILE;
+                bool odd = false;
+                for (int i = t64; i < kPKeys * S::HALVES * 8; i += 64) {
+                    const int r = (i >> 3) & (kPKeys - 1), t = t0 + r;
+                    const bool any = ((groups >> (r >> 4)) & 1u) && t <= p_hi &&
+                                     (a.c.window == 0 || t < a.c.sinks || t > p_lo - a.c.window);
+                    uint4* at = reinterpret_cast<uint4*>(Vs + (i >> 10) * (kPKeys * 128) + r * 128 + (i & 7) * 16);
+                    if (!any) {
+                        *at = make_uint4(0u, 0u, 0u, 0u);
+                    } else {
+                        const uint4 v = *at;
+                        if (nonfinite2<F16>(v.x) || nonfinite2<F16>(v.y) || nonfinite2<F16>(v.z) || nonfinite2<F16>(v.w)) {
+                            odd = true;
+                            uint16_t* e = reinterpret_cast<uint16_t*>(at);
+                            for (int u = 0; u < 8; ++u)
+                                if ((e[u] & exponent_mask<F16>()) == exponent_mask<F16>()) e[u] = 0;
+                        }
+                    }
+                }
+                if (odd) odd_values = 1;
+                fence_proxy_async();
+            }
+            mbar_arrive(&clean[n & 3]);
+        }
+    } else {
+        // ---- rows ----
+        const int i = (warp - 4) >> 2, quarter = warp & 3;
+        const int r = r0 + i * 128 + quarter * 32 + lane;
+        const bool in = r < n_rows;
+        const int token = o.row0 + (in ? r / G : 0), head = j * G + (in ? r % G : 0);
+        {
+            const uint16_t* q = a.q + (size_t)token * a.q_ld + (size_t)head * DH;
+            const int rr = quarter * 32 + lane;
+#pragma unroll
+            for (int c = 0; c < DH / 8; ++c) {
+                const uint4 v = in ? *reinterpret_cast<const uint4*>(q + c * 8) : make_uint4(0u, 0u, 0u, 0u);
+                *reinterpret_cast<uint4*>(Qs + i * S::TILE + (c >> 3) * (128 * 128) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = v;
+            }
+        }
+        fence_proxy_async();
+        mbar_arrive(&q_ready);
+        const PromptRow me{o.p0 + r / G, a.c.window, a.c.sinks};
+        const int w_lo = o.p0 + (r - lane) / G, w_hi = o.p0 + (r - lane + 31) / G;   // the warp's rows
+        const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+        const uint32_t tS = tmem + lanes + S::S0 + (uint32_t)(i * 128), tO = tmem + lanes + S::O0 + (uint32_t)(i * DH),
+                       tP = tmem + lanes + S::P0 + (uint32_t)(i * S::P_STEP);
+        float m = -INFINITY, l = 0.0f;
+        for (int n = 0; n < nb && ok; ++n) {
+            const int t0 = kb.block(b0 + n) * kPKeys;
+            ok = __all_sync(0xffffffffu, mbar_wait(&s_full[i], (uint32_t)(n & 1), a.c.status));
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t groups = block_mapped[n & 15];
+            const bool whole = groups == 0xffu && t0 + kPKeys - 1 <= w_lo &&
+                               (a.c.window == 0 || t0 > w_hi - a.c.window || t0 + kPKeys - 1 < a.c.sinks);
+            float top = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < kPKeys; c += 32) {
+                float v[32];
+                tc_ld32(tS + (uint32_t)c, v);
+                if (!whole) {
+                    const uint32_t seen = me.seen(t0 + c, groups >> (c >> 4));
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] = (seen >> e) & 1u ? v[e] : -INFINITY;
+                }
+#pragma unroll
+                for (int e = 0; e < 32; ++e) top = fmaxf(top, v[e]);
+            }
+            top *= a.scale_log2;   // above 0
+            // the maximum moves where it grew by more than 2^8, or was none (then every weight so far was 0)
+            const float m_new = m == -INFINITY || top > m + 8.0f ? top : m;
+            const float f = m == -INFINITY || m_new == m ? 1.0f : exp2_approx(m - m_new);
+            m = m_new;
+            l *= f;
+            if (n > 0 && __any_sync(0xffffffffu, f != 1.0f)) {
+                // O_i stands at the block before: its products were committed with S_i's
+#pragma unroll 1
+                for (int c = 0; c < DH; c += 32) {
+                    float v[32];
+                    tc_ld32(tO + (uint32_t)c, v);
+                    uint32_t u[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(v[e] * f);
+                    tc_st16(tO + (uint32_t)c, u);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(v[16 + e] * f);
+                    tc_st16(tO + (uint32_t)(c + 16), u);
+                }
+            }
+            const float base = m == -INFINITY ? 0.0f : m;
+            float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int c = 0; c < kPKeys; c += 32) {
+                float v[32];
+                tc_ld32(tS + (uint32_t)c, v);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] = exp2_approx(fmaf(v[e], a.scale_log2, -base));
+                if (!whole) {
+                    const uint32_t seen = me.seen(t0 + c, groups >> (c >> 4));
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] = (seen >> e) & 1u ? v[e] : 0.0f;
+                }
+                // P in 16 bits, as the tensor core takes it: 2^-9 (bf16) or 2^-12 (fp16) of each weight
+                uint32_t u[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    part[e & 3] += v[2 * e] + v[2 * e + 1];
+                    u[e] = pack16<F16>(v[2 * e], v[2 * e + 1]);
+                }
+                tc_st16(tP + (uint32_t)(c / 2), u);   // over columns of S that were read already
+            }
+            l += (part[0] + part[1]) + (part[2] + part[3]);
+            tc_wait_st();
+            tc_fence_before();
+            mbar_arrive(&p_ready[i]);
+        }
+        if (ok && nb > 0) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&o_full[i], 0, a.c.status));
+            tc_fence_after();
+        }
+        // ---- out, or a split's record: [256][DH] sums, [256] maxima, [256] sums of weights ----
+        const bool odd = odd_values != 0;
+        const float inv = splits > 1 ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
+        const int unit = blockIdx.x * gridDim.y + j, rr = i * 128 + quarter * 32 + lane;
+        float* rec = a.partial + ((size_t)unit * splits + split) * (kPRows * (DH + 2));
+        uint16_t* to = a.out + (size_t)token * a.out_ld + (size_t)head * DH;
+#pragma unroll 1
+        for (int c = 0; c < DH && ok; c += 32) {
+            float v[32];
+            if (nb > 0) tc_ld32(tO + (uint32_t)c, v);
+            else
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] = 0.0f;
+            if (!in) continue;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] *= inv;
+            if (odd)   // the infinities and NaN that were taken out of the values, to the rows that see them
+                for (int n = 0; n < nb; ++n)
+                    for (int u = 0; u < kPKeys; ++u) {
+                        const int t = kb.block(b0 + n) * kPKeys + u;
+                        if (t > me.p || !(a.c.window == 0 || t < a.c.sinks || t > me.p - a.c.window)) continue;
+                        const int e = page_of(a.c, o.s, t >> a.c.page_shift);
+                        if (e < 0) continue;
+                        const uint16_t* x = a.c.v + (((size_t)e * a.c.Hk + j) * a.c.page + (t & (a.c.page - 1))) * DH + c;
+#pragma unroll
+                        for (int q = 0; q < 32; ++q)
+                            if ((x[q] & exponent_mask<F16>()) == exponent_mask<F16>()) v[q] += unpack16<F16>(x[q]);
+                    }
+            if (splits == 1) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 8)
+                    *reinterpret_cast<uint4*>(to + c + e) =
+                        make_uint4(pack16<F16>(v[e], v[e + 1]), pack16<F16>(v[e + 2], v[e + 3]), pack16<F16>(v[e + 4], v[e + 5]),
+                                   pack16<F16>(v[e + 6], v[e + 7]));
+            } else {
+#pragma unroll
+                for (int e = 0; e < 32; e += 4)
+                    __stcg(reinterpret_cast<float4*>(rec + rr * DH + c + e), make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]));
+            }
+        }
+        if (splits > 1) {
+            __stcg(rec + kPRows * DH + rr, m);
+            __stcg(rec + kPRows * DH + kPRows + rr, l);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+    if (splits == 1) return;
+
+    // ---- the last split of the tile to arrive joins them in order ----
+    const int unit = blockIdx.x * gridDim.y + j;
+    if (tid == 0) {
+        __threadfence();   // the CTA's record, ordered by the barrier, before its arrival
+        last_flag = atomicAdd(a.merge + unit, 1) == splits - 1;
+        if (last_flag) a.merge[unit] = 0;
+        __threadfence();
+    }
+    __syncthreads();
+    if (!last_flag) return;
+    constexpr int REC = kPRows * (DH + 2);
+    const float* all = a.partial + (size_t)unit * splits * REC;
+    for (int idx = tid; idx < min(kPRows, n_rows - r0) * (DH / 4); idx += kPThreads) {
+        const int r = idx / (DH / 4), d = 4 * (idx % (DH / 4));
+        float top = -INFINITY;
+        for (int sp = 0; sp < splits; ++sp) top = fmaxf(top, __ldcg(all + (size_t)sp * REC + kPRows * DH + r));
+        if (top == -INFINITY) top = 0.0f;
+        float sum = 0.0f, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+        for (int sp = 0; sp < splits; ++sp) {   // a split that saw nothing: maximum -inf, factor 0, sums 0
+            const float* p = all + (size_t)sp * REC;
+            const float w = exp2_approx(__ldcg(p + kPRows * DH + r) - top);
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(p + r * DH + d));
+            sum = fmaf(__ldcg(p + kPRows * DH + kPRows + r), w, sum);
+            v[0] = fmaf(x.x, w, v[0]); v[1] = fmaf(x.y, w, v[1]);
+            v[2] = fmaf(x.z, w, v[2]); v[3] = fmaf(x.w, w, v[3]);
+        }
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        uint16_t* to = a.out + (size_t)(o.row0 + (r0 + r) / G) * a.out_ld + (size_t)(j * G + (r0 + r) % G) * DH + d;
+        *reinterpret_cast<uint2*>(to) = make_uint2(pack16<F16>(v[0] * inv, v[1] * inv), pack16<F16>(v[2] * inv, v[3] * inv));
+    }
+}
+
+template <int DH, bool F16>
+static cudaError_t launch_prompts_t(const PagedAttnArgs& a, cudaStream_t s) {
+    using S = PromptShape<DH>;
+    const long long G = a.c.Hq / a.c.Hk;
+    // at most: every session's last tile may be part-filled
+    const long long tiles = (a.rows * G + kPRows - 1) / kPRows + a.batch;
+    if (tiles > INT32_MAX || a.c.Hk > 65535) return cudaErrorNotSupported;
+    const long long units = tiles * a.c.Hk;
+    const int splits = units < a.num_sms ? (int)(a.num_sms / units) : 1;
+    CUtensorMap mk, mv;
+    const int rows = a.c.pages * a.c.Hk * a.c.page, box = a.c.page < kPKeys ? a.c.page : kPKeys;
+    if (!tma_map_2d(&mk, a.c.k, rows, DH, DH, 64, box, F16, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !tma_map_2d(&mv, a.c.v, rows, DH, DH, 64, box, F16, CU_TENSOR_MAP_SWIZZLE_128B))
+        return cudaErrorInvalidValue;
+    auto kern = paged_prompt_kernel<DH, F16>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::BYTES);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)tiles, (unsigned)a.c.Hk, (unsigned)splits);
+    cfg.blockDim = dim3(kPThreads);
+    cfg.dynamicSmemBytes = S::BYTES;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, mk, mv, a, splits);
+}
+
+cudaError_t launch_paged_prompts(const PagedAttnArgs& a, cudaStream_t s) {
+    if (!(a.scale_log2 > 0.0f)) return cudaErrorNotSupported;   // the row maximum is taken before the scale
+    if (a.c.Dh == 128) return a.f16 ? launch_prompts_t<128, true>(a, s) : launch_prompts_t<128, false>(a, s);
+    if (a.c.Dh == 64) return a.f16 ? launch_prompts_t<64, true>(a, s) : launch_prompts_t<64, false>(a, s);
+    return cudaErrorNotSupported;
+}
+
+}  // namespace vc
