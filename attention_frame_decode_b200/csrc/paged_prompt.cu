@@ -25,9 +25,9 @@ struct PromptShape {
     static constexpr int TILE = kPKeys * DH * 2;              // bytes of a K or V block, or of an MMA tile's rows of Q
     static constexpr int STAGES = DH == 128 ? 5 : 8;          // K and V blocks in turn
     static constexpr int BYTES = 2 * TILE + STAGES * TILE + 1024;
-    // tensor memory columns: S of each tile, O of each tile; P shares S's columns where all 512 are needed (the MMAs
+    // tensor memory columns: S of each tile, O of each tile; P shares S's upper columns where all 512 are needed (the MMAs
     // of one shape run in order, so S of the next block is written after P of this one is read)
-    static constexpr uint32_t S0 = 0, O0 = 256, P0 = DH == 128 ? 0 : 384, P_STEP = DH == 128 ? 128 : 64;
+    static constexpr uint32_t S0 = 0, O0 = 256, P0 = DH == 128 ? 64 : 384, P_STEP = DH == 128 ? 128 : 64;
 };
 
 VC_DEV void tc_mma_ta(uint32_t tmem, uint32_t atmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
@@ -47,6 +47,28 @@ VC_DEV void tc_st16(uint32_t taddr, const uint32_t (&r)[16]) {
 }
 VC_DEV void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// maximum of three
+VC_DEV float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+// two fp32 operations in one instruction
+VC_DEV float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n .reg .b64 x, y, z, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
+        " fma.rn.f32x2 w, x, y, z;\n mov.b64 {%0, %1}, w;\n}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+VC_DEV float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n .reg .b64 x, y, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n add.rn.f32x2 w, x, y;\n mov.b64 {%0, %1}, w;\n}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
 // the low n bits (all for n >= 32, none for n <= 0)
 VC_DEV uint32_t low_bits(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
 
@@ -279,19 +301,30 @@ __global__ void __launch_bounds__(kPThreads, 1)
             const uint32_t groups = block_mapped[n & 15];
             const bool whole = groups == 0xffu && t0 + kPKeys - 1 <= w_lo &&
                                (a.c.window == 0 || t0 > w_hi - a.c.window || t0 + kPKeys - 1 < a.c.sinks);
-            float top = -INFINITY;
+            // a row's 128 scores: the first 64 are read for the maximum and again for the weights, the others stay
+            float v[64];
+            auto take = [&](int c0) {
+                tc_ld64(tS + (uint32_t)c0, v);
+                if (!whole)
 #pragma unroll
-            for (int c = 0; c < kPKeys; c += 32) {
-                float v[32];
-                tc_ld32(tS + (uint32_t)c, v);
-                if (!whole) {
-                    const uint32_t seen = me.seen(t0 + c, groups >> (c >> 4));
+                    for (int c = 0; c < 64; c += 32) {
+                        const uint32_t seen = me.seen(t0 + c0 + c, groups >> ((c0 + c) >> 4));
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) v[e] = (seen >> e) & 1u ? v[e] : -INFINITY;
-                }
+                        for (int e = 0; e < 32; ++e) v[c + e] = (seen >> e) & 1u ? v[c + e] : -INFINITY;
+                    }
+            };
+            float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            auto highest = [&]() {
 #pragma unroll
-                for (int e = 0; e < 32; ++e) top = fmaxf(top, v[e]);
-            }
+                for (int e = 0; e < 64; e += 8)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) t4[u] = max3(t4[u], v[e + u], v[e + 4 + u]);
+            };
+            take(0);
+            highest();
+            take(64);
+            highest();
+            float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
             top *= a.scale_log2;   // above 0
             // the maximum moves where it grew by more than 2^8, or was none (then every weight so far was 0)
             const float m_new = m == -INFINITY || top > m + 8.0f ? top : m;
@@ -301,41 +334,37 @@ __global__ void __launch_bounds__(kPThreads, 1)
             if (n > 0 && __any_sync(0xffffffffu, f != 1.0f)) {
                 // O_i stands at the block before: its products were committed with S_i's
 #pragma unroll 1
-                for (int c = 0; c < DH; c += 32) {
-                    float v[32];
-                    tc_ld32(tO + (uint32_t)c, v);
+                for (int c = 0; c < DH; c += 16) {
+                    float x[16];
+                    tc_ld16(tO + (uint32_t)c, x);
                     uint32_t u[16];
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(v[e] * f);
+                    for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(x[e] * f);
                     tc_st16(tO + (uint32_t)c, u);
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(v[16 + e] * f);
-                    tc_st16(tO + (uint32_t)(c + 16), u);
                 }
             }
             const float base = m == -INFINITY ? 0.0f : m;
-            float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            const float2 by = make_float2(a.scale_log2, a.scale_log2), off = make_float2(-base, -base);
+            float2 part[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+            auto weigh = [&](int c0) {   // P in 16 bits, as the tensor core takes it: 2^-9 (bf16) or 2^-12 (fp16) of each
 #pragma unroll
-            for (int c = 0; c < kPKeys; c += 32) {
-                float v[32];
-                tc_ld32(tS + (uint32_t)c, v);
+                for (int c = 0; c < 64; c += 32) {
+                    uint32_t u[16];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] = exp2_approx(fmaf(v[e], a.scale_log2, -base));
-                if (!whole) {
-                    const uint32_t seen = me.seen(t0 + c, groups >> (c >> 4));
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) v[e] = (seen >> e) & 1u ? v[e] : 0.0f;
+                    for (int e = 0; e < 16; ++e) {
+                        float2 z = fma2(make_float2(v[c + 2 * e], v[c + 2 * e + 1]), by, off);   // -inf where not seen
+                        z.x = exp2_approx(z.x);
+                        z.y = exp2_approx(z.y);
+                        part[e & 1] = add2(part[e & 1], z);
+                        u[e] = pack16<F16>(z.x, z.y);
+                    }
+                    tc_st16(tP + (uint32_t)((c0 + c) / 2), u);
                 }
-                // P in 16 bits, as the tensor core takes it: 2^-9 (bf16) or 2^-12 (fp16) of each weight
-                uint32_t u[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    part[e & 3] += v[2 * e] + v[2 * e + 1];
-                    u[e] = pack16<F16>(v[2 * e], v[2 * e + 1]);
-                }
-                tc_st16(tP + (uint32_t)(c / 2), u);   // over columns of S that were read already
-            }
-            l += (part[0] + part[1]) + (part[2] + part[3]);
+            };
+            weigh(64);   // to columns behind the first 64 scores
+            take(0);
+            weigh(0);
+            l += (part[0].x + part[0].y) + (part[1].x + part[1].y);
             tc_wait_st();
             tc_fence_before();
             mbar_arrive(&p_ready[i]);
