@@ -30,11 +30,41 @@ struct PromptShape {
     static constexpr uint32_t S0 = 0, O0 = 256, P0 = DH == 128 ? 64 : 384, P_STEP = DH == 128 ? 128 : 64;
 };
 
-VC_DEV void tc_mma_ta(uint32_t tmem, uint32_t atmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+// a wait for an mbarrier's phase of at most `limit` polls, without a branch that the compiler sees; 1: it came
+VC_DEV uint32_t mbar_poll(uint64_t* bar, uint32_t parity, uint32_t limit) {
+    uint32_t done;
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(
-            tmem),
-        "r"(atmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        "{\n .reg .pred p;\n .reg .u32 i;\n mov.u32 i, %3;\n mov.u32 %0, 0;\n"
+        "again:\n setp.eq.u32 p, i, 0;\n @p bra over;\n sub.u32 i, i, 1;\n"
+        " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @!p bra again;\n mov.u32 %0, 1;\n"
+        "over:\n}\n"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(limit)
+        : "memory");
+    return done;
+}
+// The MMA warp's control flow and operands are the same in all its lanes and known to be (values from memory are
+// broadcast): the operands so live in uniform registers, as the instruction wants them, and are not moved there one
+// by one for every product.  The predicate `lead`, true in one lane, issues.  D (tensor memory) (+)= A B^T, A from shared or from tensor memory.
+VC_DEV void tc_mma_lead(uint32_t lead, uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead)
+        : "memory");
+}
+VC_DEV void tc_mma_lead_ta(uint32_t lead, uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead)
+        : "memory");
+}
+VC_DEV void tc_commit_lead(uint32_t lead, uint64_t* bar) {
+    asm volatile(
+        "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar)),
+        "r"(lead)
         : "memory");
 }
 // 16 32-bit values of each lane to 16 consecutive columns
@@ -97,7 +127,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     __shared__ uint32_t tmem_base, block_mapped[16];
     __shared__ int odd_values, last_flag;
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int G = a.c.Hq / a.c.Hk, j = blockIdx.y, split = blockIdx.z;
     pdl_trigger();
     if (tid == 0) {
@@ -180,59 +210,76 @@ __global__ void __launch_bounds__(kPThreads, 1)
             for (int k = max(0, issued - ST); k < issued; ++k) mbar_wait(&full[k % ST], (uint32_t)((k / ST) & 1), nullptr);
     } else if (warp == 1) {
         // ---- products ----
-        if (lane == 0) {
-            constexpr uint32_t ID_S = umma_idesc(!F16, false, 128, kPKeys), ID_O = umma_idesc(!F16, true, 128, DH);
-            auto mma_s = [&](int i, int s) {   // S_i = Q_i K^T
-                const uint32_t q = smem_u32(Qs + i * S::TILE), k = smem_u32(ring + s * S::TILE);
+        constexpr uint32_t ID_S = umma_idesc(!F16, false, 128, kPKeys), ID_O = umma_idesc(!F16, true, 128, DH);
+        const int nb_u = __shfl_sync(0xffffffffu, nb, 0);
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        uint32_t lead = lane == 0, fine = 1;
+        const uint64_t q_desc = desc_sw128(smem_u32(Qs)), k_desc = desc_sw128(smem_u32(ring)),
+                       v_desc = umma_desc(smem_u32(ring), kPKeys * 128, 1024, UMMA_SW128);   // addresses count 16 bytes
+        auto mma_s = [&](int i, int s) {   // S_i = Q_i K^T
 #pragma unroll
-                for (int c = 0; c < DH / 16; ++c) {
-                    const uint32_t off = (uint32_t)((c >> 2) * (128 * 128) + (c & 3) * 32);
-                    tc_mma(tmem + S::S0 + (uint32_t)(i * 128), desc_sw128(q + off), desc_sw128(k + off), ID_S, c != 0);
-                }
-            };
-            auto mma_o = [&](int i, int s, bool first) {   // O_i += P_i V
-                const uint32_t v = smem_u32(ring + s * S::TILE);
+            for (int c = 0; c < DH / 16; ++c) {
+                const uint32_t off = (uint32_t)((c >> 2) * (128 * 128) + (c & 3) * 32) / 16;
+                tc_mma_lead(lead, tm + S::S0 + (uint32_t)(i * 128), q_desc + (uint32_t)(i * (S::TILE / 16)) + off,
+                            k_desc + (uint32_t)s * (S::TILE / 16) + off, ID_S, c != 0);
+            }
+        };
+        auto mma_o = [&](int i, int s, bool first) {   // O_i += P_i V
 #pragma unroll
-                for (int c = 0; c < kPKeys / 16; ++c)
-                    tc_mma_ta(tmem + S::O0 + (uint32_t)(i * DH), tmem + S::P0 + (uint32_t)(i * S::P_STEP + c * 8),
-                              umma_desc(v + (uint32_t)(c * 2048), kPKeys * 128, 1024, UMMA_SW128), ID_O, !(first && c == 0));
-            };
-            if (nb > 0) {
-                ok = mbar_wait(&q_ready, 0, a.c.status) && mbar_wait(&full[0], 0, a.c.status);
+            for (int c = 0; c < kPKeys / 16; ++c)
+                tc_mma_lead_ta(lead, tm + S::O0 + (uint32_t)(i * DH), tm + S::P0 + (uint32_t)(i * S::P_STEP + c * 8),
+                               v_desc + (uint32_t)s * (S::TILE / 16) + (uint32_t)(c * 2048 / 16), ID_O, c != 0 || !first);
+        };
+        auto wait = [&](uint64_t* bar, uint32_t parity) {   // after one that gave up: nothing more is issued
+            fine &= mbar_poll(bar, parity, fine ? (uint32_t)kWaitLimit : 0u);
+            lead &= fine;
+            __syncwarp();
+        };
+        if (nb_u > 0) {
+            wait(&q_ready, 0);
+            wait(&full[0], 0);
+            tc_fence_after();
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                mma_s(i, 0);
+                tc_commit_lead(lead, &s_full[i]);
+            }
+            tc_commit_lead(lead, &empty[0]);
+        }
+        int sv = 1, sk = 2, pk = 0;   // ring slots of block n's values and block n + 1's keys, the keys' phase
+        for (int n = 0; n < nb_u - 1; ++n) {
+            wait(&clean[n & 3], (uint32_t)((n >> 2) & 1));   // the values are there and clean
+            wait(&full[sk], (uint32_t)pk);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                wait(&p_ready[i], (uint32_t)(n & 1));
                 tc_fence_after();
-                if (ok)
-                    for (int i = 0; i < 2; ++i) {
-                        mma_s(i, 0);
-                        tc_commit(&s_full[i]);
-                    }
-                if (ok) tc_commit(&empty[0]);
+                mma_o(i, sv, n == 0);
+                mma_s(i, sk);
+                tc_commit_lead(lead, &s_full[i]);
             }
-            for (int n = 0; n < nb && ok; ++n) {
-                const int kv = 2 * n + 1, kk = 2 * n + 2, sv = kv % ST, sk = kk % ST;
-                ok = mbar_wait(&full[sv], (uint32_t)((kv / ST) & 1), a.c.status) &&
-                     mbar_wait(&clean[n & 3], (uint32_t)((n >> 2) & 1), a.c.status);
-                if (ok && n + 1 < nb) ok = mbar_wait(&full[sk], (uint32_t)((kk / ST) & 1), a.c.status);
-                for (int i = 0; i < 2 && ok; ++i) {
-                    ok = mbar_wait(&p_ready[i], (uint32_t)(n & 1), a.c.status);
-                    if (!ok) break;
-                    tc_fence_after();
-                    mma_o(i, sv, n == 0);
-                    if (n + 1 < nb) {
-                        mma_s(i, sk);
-                        tc_commit(&s_full[i]);
-                    } else {
-                        tc_commit(&o_full[i]);
-                    }
-                }
-                if (ok) {
-                    tc_commit(&empty[sv]);
-                    if (n + 1 < nb) tc_commit(&empty[sk]);
-                }
+            tc_commit_lead(lead, &empty[sv]);
+            tc_commit_lead(lead, &empty[sk]);
+            if ((sv += 2) >= ST) sv -= ST;
+            if ((sk += 2) >= ST) sk -= ST, pk ^= 1;
+        }
+        if (nb_u > 0) {
+            const int n = nb_u - 1;
+            wait(&clean[n & 3], (uint32_t)((n >> 2) & 1));
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                wait(&p_ready[i], (uint32_t)(n & 1));
+                tc_fence_after();
+                mma_o(i, sv, n == 0);
+                tc_commit_lead(lead, &o_full[i]);
             }
-            if (!ok) {   // no product outlives the tensor memory
+        }
+        if (!fine) {   // no product outlives the tensor memory
+            if (lane == 0) {
+                atomicOr(a.c.status, VC_DEV_TIMEOUT);
                 tc_commit(&drained);
-                mbar_wait(&drained, 0, nullptr);
             }
+            mbar_wait(&drained, 0, nullptr);
         }
     } else if (warp < 4) {
         // ---- values that not every row of the CTA sees: those that no row sees become 0, and so do infinities and
