@@ -25,9 +25,10 @@ struct PromptShape {
     static constexpr int TILE = kPKeys * DH * 2;              // bytes of a K or V block, or of an MMA tile's rows of Q
     static constexpr int STAGES = DH == 128 ? 5 : 8;          // K and V blocks in turn
     static constexpr int BYTES = 2 * TILE + STAGES * TILE + 1024;
+    static constexpr bool P_APART = DH < 128;
     // tensor memory columns: S of each tile, O of each tile; P shares S's upper columns where all 512 are needed (the MMAs
     // of one shape run in order, so S of the next block is written after P of this one is read)
-    static constexpr uint32_t S0 = 0, O0 = 256, P0 = DH == 128 ? 64 : 384, P_STEP = DH == 128 ? 128 : 64;
+    static constexpr uint32_t S0 = 0, O0 = 256, P0 = P_APART ? 384 : 64, P_STEP = P_APART ? 64 : 128;
 };
 
 // a wait for an mbarrier's phase of at most `limit` polls, without a branch that the compiler sees; 1: it came
@@ -43,28 +44,18 @@ VC_DEV uint32_t mbar_poll(uint64_t* bar, uint32_t parity, uint32_t limit) {
         : "memory");
     return done;
 }
-// The MMA warp's control flow and operands are the same in all its lanes and known to be (values from memory are
-// broadcast): the operands so live in uniform registers, as the instruction wants them, and are not moved there one
-// by one for every product.  The predicate `lead`, true in one lane, issues.  D (tensor memory) (+)= A B^T, A from shared or from tensor memory.
-VC_DEV void tc_mma_lead(uint32_t lead, uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
-        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead)
-        : "memory");
+// one lane of a converged warp.  What that lane alone does needs no proof that its operands are the same in all
+// lanes: the products' descriptors go to uniform registers without a loop over the lanes.
+VC_DEV bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
+    return one != 0;
 }
-VC_DEV void tc_mma_lead_ta(uint32_t lead, uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+// D (tensor memory) (+)= A B^T, A from tensor memory
+VC_DEV void tc_mma_ta(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
-        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-        "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead)
-        : "memory");
-}
-VC_DEV void tc_commit_lead(uint32_t lead, uint64_t* bar) {
-    asm volatile(
-        "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
-        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar)),
-        "r"(lead)
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 // 16 32-bit values of each lane to 16 consecutive columns
@@ -75,12 +66,35 @@ VC_DEV void tc_st16(uint32_t taddr, const uint32_t (&r)[16]) {
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
+// 32 consecutive columns, started (the registers are not there before tc_arrived)
+VC_DEV void tc_start32(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+          "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+          "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+          "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+// the loads started before are there: r depends on it
+VC_DEV void tc_arrived(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                   "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                   "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                   "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
+}
 VC_DEV void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// maximum of three
+// maximum of three; NaN if one is
 VC_DEV float max3(float a, float b, float c) {
     float d;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
 // two fp32 operations in one instruction
@@ -123,7 +137,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* Qs = smem;                     // [2 tiles][halves][128 rows][128 B]
     uint8_t* ring = smem + 2 * S::TILE;     // [stages][halves][128 keys][128 B]
-    __shared__ uint64_t full[ST], empty[ST], clean[4], q_ready, s_full[2], p_ready[2], o_full[2], drained;
+    __shared__ uint64_t full[ST], empty[ST], clean[4], q_ready, s_full[2], p_ready[2], o_done[2], drained;
     __shared__ uint32_t tmem_base, block_mapped[16];
     __shared__ int odd_values, last_flag;
 
@@ -143,7 +157,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&p_ready[i], 128);
-            mbar_init(&o_full[i], 1);
+            mbar_init(&o_done[i], 1);
         }
         odd_values = 0;
         fence_mbar_init();
@@ -213,38 +227,41 @@ __global__ void __launch_bounds__(kPThreads, 1)
         constexpr uint32_t ID_S = umma_idesc(!F16, false, 128, kPKeys), ID_O = umma_idesc(!F16, true, 128, DH);
         const int nb_u = __shfl_sync(0xffffffffu, nb, 0);
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-        uint32_t lead = lane == 0, fine = 1;
+        uint32_t fine = 1;
         const uint64_t q_desc = desc_sw128(smem_u32(Qs)), k_desc = desc_sw128(smem_u32(ring)),
                        v_desc = umma_desc(smem_u32(ring), kPKeys * 128, 1024, UMMA_SW128);   // addresses count 16 bytes
         auto mma_s = [&](int i, int s) {   // S_i = Q_i K^T
 #pragma unroll
             for (int c = 0; c < DH / 16; ++c) {
                 const uint32_t off = (uint32_t)((c >> 2) * (128 * 128) + (c & 3) * 32) / 16;
-                tc_mma_lead(lead, tm + S::S0 + (uint32_t)(i * 128), q_desc + (uint32_t)(i * (S::TILE / 16)) + off,
-                            k_desc + (uint32_t)s * (S::TILE / 16) + off, ID_S, c != 0);
+                tc_mma(tm + S::S0 + (uint32_t)(i * 128), q_desc + (uint32_t)(i * (S::TILE / 16)) + off,
+                       k_desc + (uint32_t)s * (S::TILE / 16) + off, ID_S, c != 0);
             }
+            tc_commit(&s_full[i]);
         };
         auto mma_o = [&](int i, int s, bool first) {   // O_i += P_i V
 #pragma unroll
             for (int c = 0; c < kPKeys / 16; ++c)
-                tc_mma_lead_ta(lead, tm + S::O0 + (uint32_t)(i * DH), tm + S::P0 + (uint32_t)(i * S::P_STEP + c * 8),
-                               v_desc + (uint32_t)s * (S::TILE / 16) + (uint32_t)(c * 2048 / 16), ID_O, c != 0 || !first);
+                tc_mma_ta(tm + S::O0 + (uint32_t)(i * DH), tm + S::P0 + (uint32_t)(i * S::P_STEP + c * 8),
+                          v_desc + (uint32_t)s * (S::TILE / 16) + (uint32_t)(c * 2048 / 16), ID_O, c != 0 || !first);
+            tc_commit(&o_done[i]);
         };
-        auto wait = [&](uint64_t* bar, uint32_t parity) {   // after one that gave up: nothing more is issued
-            fine &= mbar_poll(bar, parity, fine ? (uint32_t)kWaitLimit : 0u);
-            lead &= fine;
+        auto wait = [&](uint64_t* bar, uint32_t parity) {   // after one that gave up the others are short, and what is computed is not used
+            fine &= mbar_poll(bar, parity, fine ? (uint32_t)kWaitLimit : 1u);
             __syncwarp();
         };
         if (nb_u > 0) {
             wait(&q_ready, 0);
             wait(&full[0], 0);
             tc_fence_after();
+            if (elect_one()) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                mma_s(i, 0);
-                tc_commit_lead(lead, &s_full[i]);
+                for (int i = 0; i < 2; ++i) {
+                    mma_s(i, 0);
+                }
+                tc_commit(&empty[0]);
             }
-            tc_commit_lead(lead, &empty[0]);
+            __syncwarp();
         }
         int sv = 1, sk = 2, pk = 0;   // ring slots of block n's values and block n + 1's keys, the keys' phase
         for (int n = 0; n < nb_u - 1; ++n) {
@@ -254,12 +271,17 @@ __global__ void __launch_bounds__(kPThreads, 1)
             for (int i = 0; i < 2; ++i) {
                 wait(&p_ready[i], (uint32_t)(n & 1));
                 tc_fence_after();
-                mma_o(i, sv, n == 0);
-                mma_s(i, sk);
-                tc_commit_lead(lead, &s_full[i]);
+                if (elect_one()) {
+                    if constexpr (S::P_APART) mma_s(i, sk);
+                    mma_o(i, sv, n == 0);
+                    if constexpr (!S::P_APART) mma_s(i, sk);
+                    if (i == 1) {
+                        tc_commit(&empty[sv]);
+                        tc_commit(&empty[sk]);
+                    }
+                }
+                __syncwarp();
             }
-            tc_commit_lead(lead, &empty[sv]);
-            tc_commit_lead(lead, &empty[sk]);
             if ((sv += 2) >= ST) sv -= ST;
             if ((sk += 2) >= ST) sk -= ST, pk ^= 1;
         }
@@ -270,8 +292,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
             for (int i = 0; i < 2; ++i) {
                 wait(&p_ready[i], (uint32_t)(n & 1));
                 tc_fence_after();
-                mma_o(i, sv, n == 0);
-                tc_commit_lead(lead, &o_full[i]);
+                if (elect_one()) {
+                    mma_o(i, sv, n == 0);
+                }
+                __syncwarp();
             }
         }
         if (!fine) {   // no product outlives the tensor memory
@@ -323,14 +347,18 @@ __global__ void __launch_bounds__(kPThreads, 1)
         const int r = r0 + i * 128 + quarter * 32 + lane;
         const bool in = r < n_rows;
         const int token = o.row0 + (in ? r / G : 0), head = j * G + (in ? r % G : 0);
-        {
-            const uint16_t* q = a.q + (size_t)token * a.q_ld + (size_t)head * DH;
-            const int rr = quarter * 32 + lane;
+        {   // the warp's 32 rows of Q, DH / 8 lanes to a row
+            constexpr int CH = DH / 8;
+            const long long mine = in ? (long long)token * a.q_ld + (long long)head * DH : -1;
 #pragma unroll
-            for (int c = 0; c < DH / 8; ++c) {
-                const uint4 v = in ? *reinterpret_cast<const uint4*>(q + c * 8) : make_uint4(0u, 0u, 0u, 0u);
-                *reinterpret_cast<uint4*>(Qs + i * S::TILE + (c >> 3) * (128 * 128) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = v;
+            for (int it = 0; it < CH; ++it) {
+                const int rr = it * (32 / CH) + lane / CH, c = lane % CH, row = quarter * 32 + rr;
+                const long long from = __shfl_sync(0xffffffffu, mine, rr);
+                cp_async16(Qs + i * S::TILE + (c >> 3) * (128 * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4),
+                           a.q + (from < 0 ? 0 : from) + c * 8, from >= 0);
             }
+            cp_async_commit();
+            cp_async_wait<0>();
         }
         fence_proxy_async();
         mbar_arrive(&q_ready);
@@ -348,76 +376,113 @@ __global__ void __launch_bounds__(kPThreads, 1)
             const uint32_t groups = block_mapped[n & 15];
             const bool whole = groups == 0xffu && t0 + kPKeys - 1 <= w_lo &&
                                (a.c.window == 0 || t0 > w_hi - a.c.window || t0 + kPKeys - 1 < a.c.sinks);
-            // a row's 128 scores: the first 64 are read for the maximum and again for the weights, the others stay
-            float v[64];
-            auto take = [&](int c0) {
-                tc_ld64(tS + (uint32_t)c0, v);
-                if (!whole)
-#pragma unroll
-                    for (int c = 0; c < 64; c += 32) {
-                        const uint32_t seen = me.seen(t0 + c0 + c, groups >> ((c0 + c) >> 4));
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) v[c + e] = (seen >> e) & 1u ? v[c + e] : -INFINITY;
-                    }
+            const float2 by = make_float2(a.scale_log2, a.scale_log2);
+            // z -> 2^(z scale - base) of two scores, added to the sum, and rounded to 16 bits as the tensor core takes it
+            // (2^-9 of a weight in bf16, 2^-12 in fp16); -inf, a key that is not seen, gives 0
+            float2 part[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+            auto weigh = [&](float x, float y, float2 off, int e) {
+                float2 z = fma2(make_float2(x, y), by, off);
+                z.x = exp2_approx(z.x);
+                z.y = exp2_approx(z.y);
+                part[e & 1] = add2(part[e & 1], z);
+                return pack16<F16>(z.x, z.y);
             };
-            float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-            auto highest = [&]() {
+            auto hide = [&](float (&v)[32], int c) {   // scores of columns c .. c + 31 that are not seen: -inf
+                if (whole) return;
+                const uint32_t seen = me.seen(t0 + c, groups >> (c >> 4));
 #pragma unroll
-                for (int e = 0; e < 64; e += 8)
+                for (int e = 0; e < 32; ++e) v[e] = (seen >> e) & 1u ? v[e] : -INFINITY;
+            };
+            uint32_t pk[kPKeys / 2], raw[2][32];
+            float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            auto highest = [&](const float (&v)[32]) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 8)
 #pragma unroll
                     for (int u = 0; u < 4; ++u) t4[u] = max3(t4[u], v[e + u], v[e + 4 + u]);
             };
-            take(0);
-            highest();
-            take(64);
-            highest();
-            float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
-            top *= a.scale_log2;   // above 0
-            // the maximum moves where it grew by more than 2^8, or was none (then every weight so far was 0)
-            const float m_new = m == -INFINITY || top > m + 8.0f ? top : m;
-            const float f = m == -INFINITY || m_new == m ? 1.0f : exp2_approx(m - m_new);
-            m = m_new;
-            l *= f;
-            if (n > 0 && __any_sync(0xffffffffu, f != 1.0f)) {
-                // O_i stands at the block before: its products were committed with S_i's
-#pragma unroll 1
-                for (int c = 0; c < DH; c += 16) {
-                    float x[16];
-                    tc_ld16(tO + (uint32_t)c, x);
-                    uint32_t u[16];
+            // the weights under the maximum that stands, which holds nearly always: one pass over the scores
+            bool done = false;
+            if (__all_sync(0xffffffffu, m != -INFINITY)) {
+                const float2 off = make_float2(-m, -m);
+                tc_start32(tS, raw[0]);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(x[e] * f);
-                    tc_st16(tO + (uint32_t)c, u);
+                for (int c = 0; c < kPKeys; c += 32) {
+                    uint32_t (&cur)[32] = raw[(c >> 5) & 1];
+                    tc_arrived(cur);
+                    if (c + 32 < kPKeys) tc_start32(tS + (uint32_t)(c + 32), raw[((c >> 5) + 1) & 1]);
+                    float v[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(cur[e]);
+                    hide(v, c);
+                    highest(v);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) pk[c / 2 + e] = weigh(v[2 * e], v[2 * e + 1], off, e);
+                }
+                const float top = max3(t4[0], max3(t4[1], t4[2], t4[3]), t4[3]) * a.scale_log2;   // scale above 0
+                done = __all_sync(0xffffffffu, top <= m + 8.0f);   // not where a score is not a number
+            }
+            if (!done) {
+                // the maximum moves: it is found first
+                part[0] = part[1] = make_float2(0.0f, 0.0f);
+                t4[0] = t4[1] = t4[2] = t4[3] = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < kPKeys; c += 32) {
+                    float v[32];
+                    tc_ld32(tS + (uint32_t)c, v);
+                    hide(v, c);
+                    highest(v);
+                }
+                const float top = max3(t4[0], max3(t4[1], t4[2], t4[3]), t4[3]) * a.scale_log2;
+                // it moves where it grew by more than 8 (a factor of 2^8), or was none (then every weight so far was 0)
+                const float m_new = top <= m + 8.0f ? m : top;   // NaN moves it too, and makes the row's sum NaN
+                const float f = m == -INFINITY || m_new == m ? 1.0f : exp2_approx(m - m_new);
+                m = m_new;
+                l *= f;
+                if (n > 0 && __any_sync(0xffffffffu, f != 1.0f)) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(&o_done[i], (uint32_t)((n - 1) & 1), a.c.status));
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < DH; c += 16) {
+                        float x[16];
+                        tc_ld16(tO + (uint32_t)c, x);
+                        uint32_t u[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(x[e] * f);
+                        tc_st16(tO + (uint32_t)c, u);
+                    }
+                }
+                const float base = m == -INFINITY ? 0.0f : m;
+                const float2 off = make_float2(-base, -base);
+#pragma unroll
+                for (int c = 0; c < kPKeys; c += 32) {
+                    float v[32];
+                    tc_ld32(tS + (uint32_t)c, v);
+                    hide(v, c);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) pk[c / 2 + e] = weigh(v[2 * e], v[2 * e + 1], off, e);
                 }
             }
-            const float base = m == -INFINITY ? 0.0f : m;
-            const float2 by = make_float2(a.scale_log2, a.scale_log2), off = make_float2(-base, -base);
-            float2 part[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-            auto weigh = [&](int c0) {   // P in 16 bits, as the tensor core takes it: 2^-9 (bf16) or 2^-12 (fp16) of each
-#pragma unroll
-                for (int c = 0; c < 64; c += 32) {
-                    uint32_t u[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        float2 z = fma2(make_float2(v[c + 2 * e], v[c + 2 * e + 1]), by, off);   // -inf where not seen
-                        z.x = exp2_approx(z.x);
-                        z.y = exp2_approx(z.y);
-                        part[e & 1] = add2(part[e & 1], z);
-                        u[e] = pack16<F16>(z.x, z.y);
-                    }
-                    tc_st16(tP + (uint32_t)((c0 + c) / 2), u);
-                }
-            };
-            weigh(64);   // to columns behind the first 64 scores
-            take(0);
-            weigh(0);
             l += (part[0].x + part[0].y) + (part[1].x + part[1].y);
+            if (S::P_APART && n > 0) {   // the products with the weights before are complete (elsewhere: they were before S)
+                ok = __all_sync(0xffffffffu, mbar_wait(&o_done[i], (uint32_t)((n - 1) & 1), a.c.status));
+                if (!ok) break;
+                tc_fence_after();
+            }
+#pragma unroll
+            for (int c = 0; c < kPKeys / 2; c += 16) {
+                uint32_t u[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) u[e] = pk[c + e];
+                tc_st16(tP + (uint32_t)c, u);
+            }
             tc_wait_st();
             tc_fence_before();
             mbar_arrive(&p_ready[i]);
         }
         if (ok && nb > 0) {
-            ok = __all_sync(0xffffffffu, mbar_wait(&o_full[i], 0, a.c.status));
+            ok = __all_sync(0xffffffffu, mbar_wait(&o_done[i], (uint32_t)((nb - 1) & 1), a.c.status));
             tc_fence_after();
         }
         // ---- out, or a split's record: [256][DH] sums, [256] maxima, [256] sums of weights ----
