@@ -56,6 +56,19 @@ VC_DEV bool nonfinite2(uint32_t u) {
     return (u & m) == m || ((u >> 16) & m) == m;
 }
 
+// whether one of eight 16-bit values is an infinity or NaN: the exponent's carry reaches the sign bit of its half
+template <bool F16>
+VC_DEV bool any_nonfinite(const uint4& x) {
+    constexpr uint32_t one = F16 ? 0x04000400u : 0x00800080u, rest = 0x7FFF7FFFu;
+    return ((((x.x & rest) + one) | ((x.y & rest) + one) | ((x.z & rest) + one) | ((x.w & rest) + one)) & 0x80008000u) != 0;
+}
+// the pair with 0 in the place of each
+template <bool F16>
+VC_DEV uint32_t finite2(uint32_t u) {
+    constexpr uint32_t m = exponent_mask<F16>();
+    return ((u & m) == m ? 0u : u & 0xffffu) | (((u >> 16) & m) == m ? 0u : u & 0xffff0000u);
+}
+
 VC_DEV void tma_prefetch_map(const void* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }

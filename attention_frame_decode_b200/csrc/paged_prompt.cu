@@ -11,13 +11,13 @@
 // Bound: the tensor core (4 Dh flops per visible pair) and, as much, the exponentials: a block costs each SM about
 // 2 x 1024 cycles of either.
 // Warps: 0 copies K and V page by page (TMA, 128-byte swizzle) into a ring; 1 issues the MMAs; 2 and 3 clean the
-// values of edge blocks; 4-7 and 8-11 are the rows of the two tiles.
+// values of edge blocks; 4-11 and 12-19 are the rows of the two tiles.
 #include "paged_dev.cuh"
 #include "tc.cuh"
 
 namespace vc {
 
-static constexpr int kPRows = 256, kPKeys = 128, kPThreads = 384;
+static constexpr int kPRows = 256, kPKeys = 128, kPThreads = 640;
 
 template <int DH>
 struct PromptShape {
@@ -26,9 +26,11 @@ struct PromptShape {
     static constexpr int STAGES = DH == 128 ? 5 : 8;          // K and V blocks in turn
     static constexpr int BYTES = 2 * TILE + STAGES * TILE + 1024;
     static constexpr bool P_APART = DH < 128;
-    // tensor memory columns: S of each tile, O of each tile; P shares S's upper columns where all 512 are needed (the MMAs
+    // columns from the first 64 keys' weights to the others' (over the scores that they came from, or side by side)
+    static constexpr uint32_t P_HALF = P_APART ? 32 : 64;
+    // tensor memory columns: S of each tile, O of each tile; P shares S's columns where all 512 are needed (the MMAs
     // of one shape run in order, so S of the next block is written after P of this one is read)
-    static constexpr uint32_t S0 = 0, O0 = 256, P0 = P_APART ? 384 : 64, P_STEP = P_APART ? 64 : 128;
+    static constexpr uint32_t S0 = 0, O0 = 256, P0 = P_APART ? 384 : 0, P_STEP = P_APART ? 64 : 128;
 };
 
 // a wait for an mbarrier's phase of at most `limit` polls, without a branch that the compiler sees; 1: it came
@@ -66,29 +68,6 @@ VC_DEV void tc_st16(uint32_t taddr, const uint32_t (&r)[16]) {
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
-// 32 consecutive columns, started (the registers are not there before tc_arrived)
-VC_DEV void tc_start32(uint32_t taddr, uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
-          "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
-          "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
-          "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr));
-}
-// the loads started before are there: r depends on it
-VC_DEV void tc_arrived(uint32_t (&r)[32]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
-                   "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
-                   "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
-                   "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
-                 :
-                 : "memory");
-}
 VC_DEV void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // maximum of three; NaN if one is
@@ -113,6 +92,18 @@ VC_DEV float2 add2(float2 a, float2 b) {
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return d;
 }
+// the two warps (64 threads) of a row: whether any of their threads has p; a barrier
+VC_DEV bool any_of_pair(int id, bool p) {
+    uint32_t any;
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %2, 0;\n barrier.cta.red.or.pred q, %1, 64, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+        : "=r"(any)
+        : "r"(id), "r"((uint32_t)p)
+        : "memory");
+    return any != 0;
+}
+VC_DEV void sync_pair(int id) { asm volatile("barrier.cta.sync %0, 64;" ::"r"(id) : "memory"); }
+
 // the low n bits (all for n >= 32, none for n <= 0)
 VC_DEV uint32_t low_bits(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
 
@@ -140,6 +131,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     __shared__ uint64_t full[ST], empty[ST], clean[4], q_ready, s_full[2], p_ready[2], o_done[2], drained;
     __shared__ uint32_t tmem_base, block_mapped[16];
     __shared__ int odd_values, last_flag;
+    __shared__ float top_x[2][128];   // a row's highest score, between its two threads
 
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int G = a.c.Hq / a.c.Hk, j = blockIdx.y, split = blockIdx.z;
@@ -152,11 +144,11 @@ __global__ void __launch_bounds__(kPThreads, 1)
             mbar_init(&empty[s], 1);
         }
         for (int s = 0; s < 4; ++s) mbar_init(&clean[s], 64);   // values of block n at n % 4: no more are in the ring
-        mbar_init(&q_ready, 256);
+        mbar_init(&q_ready, 512);
         mbar_init(&drained, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
-            mbar_init(&p_ready[i], 128);
+            mbar_init(&p_ready[i], 256);
             mbar_init(&o_done[i], 1);
         }
         odd_values = 0;
@@ -242,7 +234,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         auto mma_o = [&](int i, int s, bool first) {   // O_i += P_i V
 #pragma unroll
             for (int c = 0; c < kPKeys / 16; ++c)
-                tc_mma_ta(tm + S::O0 + (uint32_t)(i * DH), tm + S::P0 + (uint32_t)(i * S::P_STEP + c * 8),
+                tc_mma_ta(tm + S::O0 + (uint32_t)(i * DH), tm + S::P0 + (uint32_t)(i * S::P_STEP + (c >> 2) * S::P_HALF + (c & 3) * 8),
                           v_desc + (uint32_t)s * (S::TILE / 16) + (uint32_t)(c * 2048 / 16), ID_O, c != 0 || !first);
             tc_commit(&o_done[i]);
         };
@@ -318,23 +310,38 @@ __global__ void __launch_bounds__(kPThreads, 1)
                                (a.c.window == 0 || t0 > p_hi - a.c.window || t0 + kPKeys - 1 < a.c.sinks);
             if (!whole) {
                 uint8_t* Vs = ring + s * S::TILE;
+                constexpr int ROW = S::HALVES * 8;   // 16-byte chunks of a row
+                auto chunk_at = [&](int r, int c) {
+                    return reinterpret_cast<uint4*>(Vs + (c >> 3) * (kPKeys * 128) + r * 128 + (c & 7) * 16);   // any order of a row's
+                };
                 bool odd = false;
-                for (int i = t64; i < kPKeys * S::HALVES * 8; i += 64) {
-                    const int r = (i >> 3) & (kPKeys - 1), t = t0 + r;
-                    const bool any = ((groups >> (r >> 4)) & 1u) && t <= p_hi &&
-                                     (a.c.window == 0 || t < a.c.sinks || t > p_lo - a.c.window);
-                    uint4* at = reinterpret_cast<uint4*>(Vs + (i >> 10) * (kPKeys * 128) + r * 128 + (i & 7) * 16);
-                    if (!any) {
-                        *at = make_uint4(0u, 0u, 0u, 0u);
-                    } else {
-                        const uint4 v = *at;
-                        if (nonfinite2<F16>(v.x) || nonfinite2<F16>(v.y) || nonfinite2<F16>(v.z) || nonfinite2<F16>(v.w)) {
-                            odd = true;
-                            uint16_t* e = reinterpret_cast<uint16_t*>(at);
-                            for (int u = 0; u < 8; ++u)
-                                if ((e[u] & exponent_mask<F16>()) == exponent_mask<F16>()) e[u] = 0;
+                // rows r0 .. r1 - 1 of the block: seen by none (`none`), or by some
+                auto sweep = [&](int first, int last, bool none) {
+                    const int n_chunks = max(last - first, 0) * ROW;
+#pragma unroll 4
+                    for (int k = t64; k < n_chunks; k += 64) {
+                        uint4* at = chunk_at(first + k / ROW, k % ROW);
+                        if (none) {
+                            *at = make_uint4(0u, 0u, 0u, 0u);
+                        } else {
+                            const uint4 x = *at;
+                            if (any_nonfinite<F16>(x)) {
+                                odd = true;
+                                *at = make_uint4(finite2<F16>(x.x), finite2<F16>(x.y), finite2<F16>(x.z), finite2<F16>(x.w));
+                            }
                         }
                     }
+                };
+                auto clip = [&](long long t) { return (int)(t < t0 ? 0 : t > t0 + kPKeys ? kPKeys : t - t0); };
+                // no page: whatever an earlier block left there
+                for (int u = 0; u < kPKeys / 16; ++u)
+                    if (!((groups >> u) & 1u)) sweep(16 * u, 16 * u + 16, true);
+                sweep(clip(p_lo + 1LL), clip(p_hi + 1LL), false);     // the first row sees up to p_lo, the last up to p_hi
+                sweep(clip(p_hi + 1LL), kPKeys, true);
+                if (a.c.window > 0) {                                  // and from p_lo - window + 1 on, behind the sinks
+                    const long long from = p_lo - (long long)a.c.window + 1, to = p_hi - (long long)a.c.window + 1;
+                    sweep(clip(a.c.sinks), clip(from), true);
+                    sweep(clip(from > a.c.sinks ? from : a.c.sinks), clip(to), false);
                 }
                 if (odd) odd_values = 1;
                 fence_proxy_async();
@@ -342,19 +349,20 @@ __global__ void __launch_bounds__(kPThreads, 1)
             mbar_arrive(&clean[n & 3]);
         }
     } else {
-        // ---- rows ----
-        const int i = (warp - 4) >> 2, quarter = warp & 3;
-        const int r = r0 + i * 128 + quarter * 32 + lane;
+        // ---- rows: a row's scores of a block belong to two threads, a half each, whose warps (and those of the other
+        // tile) share the special function units of an SM quarter ----
+        const int i = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1, quarter = warp & 3, rr = quarter * 32 + lane;
+        const int r = r0 + i * 128 + rr;
         const bool in = r < n_rows;
         const int token = o.row0 + (in ? r / G : 0), head = j * G + (in ? r % G : 0);
-        {   // the warp's 32 rows of Q, DH / 8 lanes to a row
+        {   // every second group of the warp's 32 rows of Q, DH / 8 lanes to a row
             constexpr int CH = DH / 8;
             const long long mine = in ? (long long)token * a.q_ld + (long long)head * DH : -1;
 #pragma unroll
-            for (int it = 0; it < CH; ++it) {
-                const int rr = it * (32 / CH) + lane / CH, c = lane % CH, row = quarter * 32 + rr;
-                const long long from = __shfl_sync(0xffffffffu, mine, rr);
-                cp_async16(Qs + i * S::TILE + (c >> 3) * (128 * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4),
+            for (int it = 0; it < CH / 2; ++it) {
+                const int row = (2 * it + half) * (32 / CH) + lane / CH, c = lane % CH, at = quarter * 32 + row;
+                const long long from = __shfl_sync(0xffffffffu, mine, row);
+                cp_async16(Qs + i * S::TILE + (c >> 3) * (128 * 128) + at * 128 + (((c & 7) ^ (at & 7)) << 4),
                            a.q + (from < 0 ? 0 : from) + c * 8, from >= 0);
             }
             cp_async_commit();
@@ -365,86 +373,78 @@ __global__ void __launch_bounds__(kPThreads, 1)
         const PromptRow me{o.p0 + r / G, a.c.window, a.c.sinks};
         const int w_lo = o.p0 + (r - lane) / G, w_hi = o.p0 + (r - lane + 31) / G;   // the warp's rows
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-        const uint32_t tS = tmem + lanes + S::S0 + (uint32_t)(i * 128), tO = tmem + lanes + S::O0 + (uint32_t)(i * DH),
-                       tP = tmem + lanes + S::P0 + (uint32_t)(i * S::P_STEP);
+        const uint32_t tS = tmem + lanes + S::S0 + (uint32_t)(i * 128 + half * 64), tO = tmem + lanes + S::O0 + (uint32_t)(i * DH),
+                       tP = tmem + lanes + S::P0 + (uint32_t)(i * S::P_STEP + half * S::P_HALF);
+        auto wait = [&](uint64_t* bar, int phase) {   // after one that gave up none waits, and what is computed is not used
+            ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, (uint32_t)(phase & 1), a.c.status));
+        };
+        const int pair = 1 + i * 4 + quarter;   // the barrier of the rows' two warps
+        // m: the maximum under which the row's weights stand (its threads agree on it); l: the sum of this thread's
         float m = -INFINITY, l = 0.0f;
-        for (int n = 0; n < nb && ok; ++n) {
-            const int t0 = kb.block(b0 + n) * kPKeys;
-            ok = __all_sync(0xffffffffu, mbar_wait(&s_full[i], (uint32_t)(n & 1), a.c.status));
-            if (!ok) break;
+        const float2 by = make_float2(a.scale_log2, a.scale_log2);
+        for (int n = 0; n < nb; ++n) {
+            const int t0 = kb.block(b0 + n) * kPKeys + half * 64;
+            wait(&s_full[i], n);
             tc_fence_after();
-            const uint32_t groups = block_mapped[n & 15];
-            const bool whole = groups == 0xffu && t0 + kPKeys - 1 <= w_lo &&
-                               (a.c.window == 0 || t0 > w_hi - a.c.window || t0 + kPKeys - 1 < a.c.sinks);
-            const float2 by = make_float2(a.scale_log2, a.scale_log2);
-            // z -> 2^(z scale - base) of two scores, added to the sum, and rounded to 16 bits as the tensor core takes it
-            // (2^-9 of a weight in bf16, 2^-12 in fp16); -inf, a key that is not seen, gives 0
-            float2 part[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-            auto weigh = [&](float x, float y, float2 off, int e) {
-                float2 z = fma2(make_float2(x, y), by, off);
-                z.x = exp2_approx(z.x);
-                z.y = exp2_approx(z.y);
-                part[e & 1] = add2(part[e & 1], z);
-                return pack16<F16>(z.x, z.y);
-            };
-            auto hide = [&](float (&v)[32], int c) {   // scores of columns c .. c + 31 that are not seen: -inf
-                if (whole) return;
-                const uint32_t seen = me.seen(t0 + c, groups >> (c >> 4));
+            const uint32_t groups = block_mapped[n & 15] >> (4 * half);
+            const bool whole = (groups & 0xfu) == 0xfu && t0 + 63 <= w_lo &&
+                               (a.c.window == 0 || t0 > w_hi - a.c.window || t0 + 63 < a.c.sinks);
+            float t4[4], v[32];
+            float2 part[2];
+            uint32_t pk[2][16];
+            auto take = [&](int c) {   // scores of columns c .. c + 31, -inf where not seen, and their maximum
+                tc_ld32(tS + (uint32_t)c, v);
+                if (!whole) {
+                    const uint32_t seen = me.seen(t0 + c, groups >> (c >> 4));
 #pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] = (seen >> e) & 1u ? v[e] : -INFINITY;
-            };
-            uint32_t pk[kPKeys / 2], raw[2][32];
-            float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-            auto highest = [&](const float (&v)[32]) {
+                    for (int e = 0; e < 32; ++e) v[e] = (seen >> e) & 1u ? v[e] : -INFINITY;
+                }
 #pragma unroll
                 for (int e = 0; e < 32; e += 8)
 #pragma unroll
                     for (int u = 0; u < 4; ++u) t4[u] = max3(t4[u], v[e + u], v[e + 4 + u]);
             };
-            // the weights under the maximum that stands, which holds nearly always: one pass over the scores
-            bool done = false;
-            if (__all_sync(0xffffffffu, m != -INFINITY)) {
-                const float2 off = make_float2(-m, -m);
-                tc_start32(tS, raw[0]);
+            // the weights 2^(z scale - base): added to the sum, and rounded to 16 bits as the tensor core takes them (2^-9
+            // of a weight in bf16, 2^-12 in fp16); 0 where not seen
+            auto weigh = [&](uint32_t (&u)[16], float2 off) {
 #pragma unroll
-                for (int c = 0; c < kPKeys; c += 32) {
-                    uint32_t (&cur)[32] = raw[(c >> 5) & 1];
-                    tc_arrived(cur);
-                    if (c + 32 < kPKeys) tc_start32(tS + (uint32_t)(c + 32), raw[((c >> 5) + 1) & 1]);
-                    float v[32];
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(cur[e]);
-                    hide(v, c);
-                    highest(v);
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) pk[c / 2 + e] = weigh(v[2 * e], v[2 * e + 1], off, e);
+                for (int e = 0; e < 16; ++e) {
+                    float2 z = fma2(make_float2(v[2 * e], v[2 * e + 1]), by, off);
+                    z.x = exp2_approx(z.x);
+                    z.y = exp2_approx(z.y);
+                    part[e & 1] = add2(part[e & 1], z);
+                    u[e] = pack16<F16>(z.x, z.y);
                 }
-                const float top = max3(t4[0], max3(t4[1], t4[2], t4[3]), t4[3]) * a.scale_log2;   // scale above 0
-                done = __all_sync(0xffffffffu, top <= m + 8.0f);   // not where a score is not a number
-            }
-            if (!done) {
-                // the maximum moves: it is found first
+            };
+            auto clear = [&]() {
                 part[0] = part[1] = make_float2(0.0f, 0.0f);
                 t4[0] = t4[1] = t4[2] = t4[3] = -INFINITY;
-#pragma unroll
-                for (int c = 0; c < kPKeys; c += 32) {
-                    float v[32];
-                    tc_ld32(tS + (uint32_t)c, v);
-                    hide(v, c);
-                    highest(v);
-                }
-                const float top = max3(t4[0], max3(t4[1], t4[2], t4[3]), t4[3]) * a.scale_log2;
-                // it moves where it grew by more than 8 (a factor of 2^8), or was none (then every weight so far was 0)
-                const float m_new = top <= m + 8.0f ? m : top;   // NaN moves it too, and makes the row's sum NaN
+            };
+            auto top = [&]() { return max3(t4[0], max3(t4[1], t4[2], t4[3]), t4[3]) * a.scale_log2; };   // scale above 0
+            // the weights under the maximum that stands, which holds nearly always: the scores are passed over once
+            clear();
+            const float2 off = make_float2(-m, -m);
+            take(0);
+            weigh(pk[0], off);
+            take(32);
+            weigh(pk[1], off);
+            if (any_of_pair(pair, !(top() <= m + 8.0f) || m == -INFINITY)) {   // (not where a score is not a number)
+                // it moves where it grew by more than 8 (a factor of 2^8), or was none (then all weights so far were 0)
+                float tp = top();
+                if (half == 0) top_x[i][rr] = tp;
+                sync_pair(pair);
+                if (half == 1) top_x[i][rr] = max3(tp, top_x[i][rr], tp);
+                sync_pair(pair);
+                tp = top_x[i][rr];
+                const float m_new = tp <= m + 8.0f ? m : tp;   // NaN moves it too, and makes the row's sum NaN
                 const float f = m == -INFINITY || m_new == m ? 1.0f : exp2_approx(m - m_new);
                 m = m_new;
                 l *= f;
-                if (n > 0 && __any_sync(0xffffffffu, f != 1.0f)) {
-                    ok = __all_sync(0xffffffffu, mbar_wait(&o_done[i], (uint32_t)((n - 1) & 1), a.c.status));
-                    if (!ok) break;
+                if (n > 0 && __any_sync(0xffffffffu, f != 1.0f)) {   // the products so far are in O_i; a half of it each
+                    wait(&o_done[i], n - 1);
                     tc_fence_after();
 #pragma unroll 1
-                    for (int c = 0; c < DH; c += 16) {
+                    for (int c = half * (DH / 2); c < (half + 1) * (DH / 2); c += 16) {
                         float x[16];
                         tc_ld16(tO + (uint32_t)c, x);
                         uint32_t u[16];
@@ -454,45 +454,41 @@ __global__ void __launch_bounds__(kPThreads, 1)
                     }
                 }
                 const float base = m == -INFINITY ? 0.0f : m;
-                const float2 off = make_float2(-base, -base);
-#pragma unroll
-                for (int c = 0; c < kPKeys; c += 32) {
-                    float v[32];
-                    tc_ld32(tS + (uint32_t)c, v);
-                    hide(v, c);
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) pk[c / 2 + e] = weigh(v[2 * e], v[2 * e + 1], off, e);
-                }
+                const float2 off_new = make_float2(-base, -base);
+                clear();
+                take(0);
+                weigh(pk[0], off_new);
+                take(32);
+                weigh(pk[1], off_new);
             }
             l += (part[0].x + part[0].y) + (part[1].x + part[1].y);
             if (S::P_APART && n > 0) {   // the products with the weights before are complete (elsewhere: they were before S)
-                ok = __all_sync(0xffffffffu, mbar_wait(&o_done[i], (uint32_t)((n - 1) & 1), a.c.status));
-                if (!ok) break;
+                wait(&o_done[i], n - 1);
                 tc_fence_after();
             }
-#pragma unroll
-            for (int c = 0; c < kPKeys / 2; c += 16) {
-                uint32_t u[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) u[e] = pk[c + e];
-                tc_st16(tP + (uint32_t)c, u);
-            }
+            tc_st16(tP, pk[0]);
+            tc_st16(tP + 16, pk[1]);
             tc_wait_st();
             tc_fence_before();
             mbar_arrive(&p_ready[i]);
         }
-        if (ok && nb > 0) {
-            ok = __all_sync(0xffffffffu, mbar_wait(&o_done[i], (uint32_t)((nb - 1) & 1), a.c.status));
+        if (nb > 0) {
+            wait(&o_done[i], nb - 1);
             tc_fence_after();
         }
+        // the row's sum, by way of the room of Q (its last products are complete)
+        float* l_part = reinterpret_cast<float*>(Qs + i * S::TILE);
+        l_part[half * 128 + rr] = l;
+        sync_pair(pair);
+        l = l_part[rr] + l_part[128 + rr];
         // ---- out, or a split's record: [256][DH] sums, [256] maxima, [256] sums of weights ----
         const bool odd = odd_values != 0;
         const float inv = splits > 1 ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
-        const int unit = blockIdx.x * gridDim.y + j, rr = i * 128 + quarter * 32 + lane;
+        const int unit = blockIdx.x * gridDim.y + j, at = i * 128 + rr;
         float* rec = a.partial + ((size_t)unit * splits + split) * (kPRows * (DH + 2));
         uint16_t* to = a.out + (size_t)token * a.out_ld + (size_t)head * DH;
 #pragma unroll 1
-        for (int c = 0; c < DH && ok; c += 32) {
+        for (int c = half * (DH / 2); c < (half + 1) * (DH / 2) && ok; c += 32) {   // a half each
             float v[32];
             if (nb > 0) tc_ld32(tO + (uint32_t)c, v);
             else
@@ -522,12 +518,12 @@ __global__ void __launch_bounds__(kPThreads, 1)
             } else {
 #pragma unroll
                 for (int e = 0; e < 32; e += 4)
-                    __stcg(reinterpret_cast<float4*>(rec + rr * DH + c + e), make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]));
+                    __stcg(reinterpret_cast<float4*>(rec + at * DH + c + e), make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]));
             }
         }
-        if (splits > 1) {
-            __stcg(rec + kPRows * DH + rr, m);
-            __stcg(rec + kPRows * DH + kPRows + rr, l);
+        if (splits > 1 && half == 0) {
+            __stcg(rec + kPRows * DH + at, m);
+            __stcg(rec + kPRows * DH + kPRows + at, l);
         }
     }
     tc_fence_before();
