@@ -16,7 +16,8 @@ struct PagedKv {
 };
 
 struct PagedWorkspace {
-    int* head;        // [0] copies listed by a resize or fork
+    int* head;        // [0] copies listed by a resize or fork, [1], [2] a compaction's moves and live pages
+    int* ticket;      // work handed out by attention (zero between calls)
     int* merge;       // arrival counters of split attention work [kMergeCounters] (zero between calls)
     int* copies;      // [seqs][3]: source page, destination page, positions to copy
     int* ok;          // [seqs]: rows of a fork that are done
@@ -48,6 +49,7 @@ struct PagedAttnArgs {
     int batch, rows, f16, num_sms;
     float scale_log2;            // scale * log2(e)
     int* merge;
+    int* ticket;                 // counts the pieces handed out (zero between calls)
     float* partial;
 };
 

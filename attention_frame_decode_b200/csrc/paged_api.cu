@@ -34,6 +34,7 @@ PagedWorkspace paged_carve(const vc_paged_kv& c, void* base) {
         return p;
     };
     w.head = (int*)take(256);
+    w.ticket = (int*)take(256);
     w.merge = (int*)take((size_t)kMaxSplitCtas * 4);
     w.copies = (int*)take((size_t)c.seqs * 12);
     w.ok = (int*)take((size_t)c.seqs * 4);
@@ -138,6 +139,7 @@ extern "C" vc_status vc_paged_attend(const vc_paged_kv* kv, int layer, const vc_
     a.scale_log2 = scale * 1.4426950408889634f;
     const PagedWorkspace w = paged_carve(*kv, kv->workspace);
     a.merge = w.merge;
+    a.ticket = w.ticket;
     a.partial = w.partial;
     int dev = 0;
     CKP(cudaGetDevice(&dev));

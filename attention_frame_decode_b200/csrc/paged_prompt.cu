@@ -1,17 +1,19 @@
 // paged_prompt.cu -- windowed attention over the paged KV cache for prompts, on tcgen05 tensor cores.
 //
 // The packed rows of a session and KV head (paged_attn.cu) are cut into tiles of 256 = two MMA tiles of 128 rows;
-// one CTA per SM takes a tile and walks the blocks of 128 keys that its rows can see.  Per block and MMA tile i:
+// one CTA per SM takes tiles in turn and walks the blocks of 128 keys that a tile's rows can see.  Per block and MMA
+// tile i:
 //     S_i = Q_i K^T (tcgen05.mma into tensor memory, fp32)
-//     P_i = exp2(scale S_i - m_i), one thread per row, written back to tensor memory as the 16-bit A operand
+//     P_i = exp2(scale S_i - m_i), two threads per row, written back to tensor memory as the 16-bit A operand
 //     O_i += P_i V (tcgen05.mma, A from tensor memory)
 // The two tiles alternate: while the threads of one form its weights, the tensor core works on the other's
 // products.  The running maximum moves only when it grew by more than 2^8 (weights up to 2^8 lose no precision in
-// fp32 or the 16-bit formats), so O_i is rarely read back to be rescaled.
-// Bound: the tensor core (4 Dh flops per visible pair) and, as much, the exponentials: a block costs each SM about
-// 2 x 1024 cycles of either.
-// Warps: 0 copies K and V page by page (TMA, 128-byte swizzle) into a ring; 1 issues the MMAs; 2 and 3 clean the
-// values of edge blocks; 4-11 and 12-19 are the rows of the two tiles.
+// fp32 or the 16-bit formats), so O_i is rarely read back to be rescaled, and a block's weights are formed in one pass
+// over its scores.
+// Bound: per block and SM about 2 x 1008 cycles of products (M = N = 128: 63 each) and 2 x 1024 of exponentials; what
+// it takes is the chain of one tile, weights then products, since tensor memory has no room for scores ahead.
+// Warps: 0 copies K and V page by page (TMA, 128-byte swizzle) into a ring; 1 issues the MMAs; 2 brings the rows of Q;
+// 3 cleans the values of edge blocks; 4-11 and 12-19 are the rows of the two tiles.
 #include "paged_dev.cuh"
 #include "tc.cuh"
 
@@ -22,9 +24,10 @@ static constexpr int kPRows = 256, kPKeys = 128, kPThreads = 640;
 template <int DH>
 struct PromptShape {
     static constexpr int HALVES = DH / 64;                    // 64-wide column parts
-    static constexpr int TILE = kPKeys * DH * 2;              // bytes of a K or V block, or of an MMA tile's rows of Q
-    static constexpr int STAGES = DH == 128 ? 5 : 8;          // K and V blocks in turn
-    static constexpr int BYTES = 2 * TILE + STAGES * TILE + 1024;
+    static constexpr int TILE = kPKeys * DH * 2;              // bytes of a K or V block
+    static constexpr int QBYTES = 2 * TILE;                   // bytes of the rows of Q, [halves][256 rows][128 B]
+    static constexpr int STAGES = DH == 128 ? 4 : 8;          // K and V blocks in turn (a power of two)
+    static constexpr int BYTES = QBYTES + STAGES * TILE + 1024;
     static constexpr bool P_APART = DH < 128;
     // columns from the first 64 keys' weights to the others' (over the scores that they came from, or side by side)
     static constexpr uint32_t P_HALF = P_APART ? 32 : 64;
@@ -104,6 +107,25 @@ VC_DEV bool any_of_pair(int id, bool p) {
 }
 VC_DEV void sync_pair(int id) { asm volatile("barrier.cta.sync %0, 64;" ::"r"(id) : "memory"); }
 
+// one of the steps of a 4 x 4 transpose over lanes: y of the lanes without the bit for x of those with it
+VC_DEV void swap_lanes(uint4& x, uint4& y, int bit, bool has) {
+    uint4 t = has ? x : y;
+    t.x = __shfl_xor_sync(0xffffffffu, t.x, bit);
+    t.y = __shfl_xor_sync(0xffffffffu, t.y, bit);
+    t.z = __shfl_xor_sync(0xffffffffu, t.z, bit);
+    t.w = __shfl_xor_sync(0xffffffffu, t.w, bit);
+    if (has) x = t;
+    else y = t;
+}
+
+VC_DEV void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+            smem_u32(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+
 // the low n bits (all for n >= 32, none for n <= 0)
 VC_DEV uint32_t low_bits(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
 
@@ -118,106 +140,157 @@ struct PromptRow {
     }
 };
 
+struct PromptMaps {
+    CUtensorMap q, k, v;
+};
+
+// one piece of work: a tile of a session and KV head, or a split of its key blocks
+struct PromptWork {
+    KeyBlocks kb;            // the tile's key blocks; this piece's are b0 .. b0 + nb - 1
+    int b0, nb;
+    int s, row0, n_rows;     // the session's index and first row; its packed rows
+    int r0, r1, p0;          // the tile's packed rows r0 .. r1 - 1; the position of the session's first row
+    int p_lo, p_hi, j, unit, split;
+};
+
+// piece `item` of the launch (a whole warp calls); nb is 0 where there is nothing to do, and n_rows too where not even
+// an empty record is wanted, and -1 behind the last piece.  A tile holds whole tokens: tile_rows = (256 / G) G rows.
+VC_DEV PromptWork prompt_work(const PagedAttnArgs& a, int tiles, int splits, int item) {
+    PromptWork w{};
+    const int G = a.c.Hq / a.c.Hk, tile_rows = kPRows / G * G;
+    if (item >= tiles * a.c.Hk * splits) {
+        w.nb = -1;
+        return w;
+    }
+    w.split = item % splits;
+    w.unit = item / splits;
+    w.j = w.unit % a.c.Hk;
+    int session, tile;
+    AttnSession o;
+    // the longest rows first
+    if (!find_tile(a, G, tile_rows, tiles - 1 - w.unit / a.c.Hk, session, tile) || !attn_session(a, session, o)) return w;
+    w.s = o.s;
+    w.row0 = o.row0;
+    w.n_rows = o.n * G;
+    w.r0 = tile * tile_rows;
+    w.p0 = o.p0;
+    w.p_lo = o.p0 + w.r0 / G;
+    w.r1 = min(w.r0 + tile_rows, w.n_rows);
+    w.p_hi = o.p0 + (w.r1 - 1) / G;
+    w.kb = key_blocks<kPKeys>(a.c.window, a.c.sinks, w.p_lo, w.p_hi);
+    w.b0 = (int)((long long)w.kb.total * w.split / splits);
+    w.nb = (int)((long long)w.kb.total * (w.split + 1) / splits) - w.b0;
+    return w;
+}
+
 template <int DH, bool F16>
 __global__ void __launch_bounds__(kPThreads, 1)
-    paged_prompt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                        const PagedAttnArgs a, int splits) {
+    paged_prompt_kernel(const __grid_constant__ PromptMaps maps, const PagedAttnArgs a, int tiles, int splits) {
     using S = PromptShape<DH>;
     constexpr int ST = S::STAGES;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t* Qs = smem;                     // [2 tiles][halves][128 rows][128 B]
-    uint8_t* ring = smem + 2 * S::TILE;     // [stages][halves][128 keys][128 B]
-    __shared__ uint64_t full[ST], empty[ST], clean[4], q_ready, s_full[2], p_ready[2], o_done[2], drained;
+    uint8_t* Qs = smem;                     // [halves][256 rows][128 B]
+    uint8_t* ring = smem + S::QBYTES;       // [stages][halves][128 keys][128 B]
+    __shared__ uint64_t full[ST], empty[ST], clean[4], work_ready[2], q_ready[2], q_free, s_full[2], p_ready[2], o_done[2], o_free[2], drained;
     __shared__ uint32_t tmem_base, block_mapped[16];
-    __shared__ int odd_values, last_flag;
-    __shared__ float top_x[2][128];   // a row's highest score, between its two threads
+    __shared__ int odd_values[4], last_flag;
+    __shared__ PromptWork work[4];       // piece t at t % 4: written again when the rows are done with it
+    __shared__ float top_x[2][128], l_part[2][2][128];   // a row's highest score, between its two threads; their sums
 
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-    const int G = a.c.Hq / a.c.Hk, j = blockIdx.y, split = blockIdx.z;
+    const int G = a.c.Hq / a.c.Hk, items = tiles * a.c.Hk * splits;   // pieces
     pdl_trigger();
     if (tid == 0) {
-        tma_prefetch_map(&tmK);
-        tma_prefetch_map(&tmV);
+        tma_prefetch_map(&maps.q);
+        tma_prefetch_map(&maps.k);
+        tma_prefetch_map(&maps.v);
         for (int s = 0; s < ST; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
-        for (int s = 0; s < 4; ++s) mbar_init(&clean[s], 64);   // values of block n at n % 4: no more are in the ring
-        mbar_init(&q_ready, 512);
+        for (int s = 0; s < 4; ++s) mbar_init(&clean[s], 32);   // values of block g at g % 4: no more are in the ring
+        mbar_init(&q_free, 1);
         mbar_init(&drained, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&p_ready[i], 256);
             mbar_init(&o_done[i], 1);
+            mbar_init(&work_ready[i], 1);
+            mbar_init(&q_ready[i], 1);
+            mbar_init(&o_free[i], 512 + 32);
         }
-        odd_values = 0;
         fence_mbar_init();
     }
-    pdl_wait();
-    if (blockIdx.x == 0 && j == 0 && split == 0)   // reports every session whose indices do not fit
-        for (int i = tid; i < a.batch; i += kPThreads) {
-            AttnSession o;
-            attn_session(a, i, o);
-        }
-    int session, tile;
-    if (!find_tile(a, G, kPRows, (int)(gridDim.x - 1 - blockIdx.x), session, tile)) return;   // the longest rows first
-    AttnSession o;
-    if (!attn_session(a, session, o)) return;
-    const int n_rows = o.n * G, r0 = tile * kPRows;
-    const int p_lo = o.p0 + r0 / G, p_hi = o.p0 + (min(r0 + kPRows, n_rows) - 1) / G;
-    const KeyBlocks kb = key_blocks<kPKeys>(a.c.window, a.c.sinks, p_lo, p_hi);
-    const int b0 = (int)((long long)kb.total * split / splits), b1 = (int)((long long)kb.total * (split + 1) / splits);
-    const int nb = b1 - b0;
-
     if (warp == 1) tmem_alloc(&tmem_base, 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_base;
-    const int box_rows = min(a.c.page, kPKeys), boxes = kPKeys / box_rows;
-    bool ok = true;
+    pdl_wait();
+    if (blockIdx.x == 0)   // reports every session whose indices do not fit
+        for (int i = tid; i < a.batch; i += kPThreads) {
+            AttnSession o;
+            attn_session(a, i, o);
+        }
+    bool ok = true;   // false after a wait that gave up: no other waits any more, and what is computed is not used
+    auto wait = [&](uint64_t* bar, int phase) {
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, (uint32_t)(phase & 1), a.c.status));
+    };
+    // Every role goes through the CTA's pieces in turn (t counts them, g the key blocks since the launch) and is held
+    // up by barriers alone: the copies, the rows of Q and the first scores of a piece come while the one before ends.
+    // No barrier completes twice before all that wait for it have seen it once: q_ready and o_free alternate (the
+    // products of piece t + 1 begin after o_free of t, and q_ready of t + 2 after those), the others are held back by
+    // the arrivals of the same threads.
 
     if (warp == 0) {
-        // ---- copies: K of block 0, V of block 0, K of block 1, ... in ring order ----
-        int entry = -1, issued = 0;
-        auto look_up = [&](int b) {   // lane q < boxes: the table entry of the block's q-th box
-            entry = -1;
-            const int t = b < b1 ? kb.block(b) * kPKeys + lane * box_rows : INT32_MAX;
-            if (lane < boxes && t <= p_hi) entry = page_of(a.c, o.s, t >> a.c.page_shift);
-        };
-        look_up(b0);
-        for (int n = 0; n < nb && ok; ++n) {
-            const int t = kb.block(b0 + n) * kPKeys + lane * box_rows;
-            const bool there = entry >= 0;
-            const unsigned mapped = __ballot_sync(0xffffffffu, there);
-            const int pool_row = (entry * a.c.Hk + j) * a.c.page + (t & (a.c.page - 1));
-            look_up(b0 + n + 1);
-            if (lane == 0) {   // a bit for each 16 keys
-                uint32_t groups = 0;
-                for (int u = 0; u < kPKeys / 16; ++u) groups |= ((mapped >> (16 * u / box_rows)) & 1u) << u;
-                block_mapped[n & 15] = groups;
-            }
-            for (int kv = 0; kv < 2 && ok; ++kv, ++issued) {
-                const int s = issued % ST;
-                if (issued >= ST) ok = __all_sync(0xffffffffu, mbar_wait(&empty[s], (uint32_t)((issued / ST - 1) & 1), a.c.status));
-                if (!ok) break;
-                if (lane == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)(__popc(mapped) * box_rows * DH * 2));
-                __syncwarp();
-                if (there)
+        // ---- copies: K of a block, V of the block, K of the next, ... in ring order ----
+        const int box_rows = min(a.c.page, kPKeys), boxes = kPKeys / box_rows;
+        int issued = 0;
+        for (int t = 0; t <= items && ok; ++t) {
+            wait(&work_ready[t & 1], t >> 1);
+            const PromptWork w = work[t & 3];
+            if (w.nb < 0) break;
+            int entry = -1;
+            auto look_up = [&](int n) {   // lane q < boxes: the table entry of block n's q-th box
+                entry = -1;
+                const int t = n < w.nb ? w.kb.block(w.b0 + n) * kPKeys + lane * box_rows : INT32_MAX;
+                if (lane < boxes && t <= w.p_hi) entry = page_of(a.c, w.s, t >> a.c.page_shift);
+            };
+            look_up(0);
+            for (int n = 0; n < w.nb && ok; ++n) {
+                const int t = w.kb.block(w.b0 + n) * kPKeys + lane * box_rows;
+                const bool there = entry >= 0;
+                const unsigned mapped = __ballot_sync(0xffffffffu, there);
+                const int pool_row = (entry * a.c.Hk + w.j) * a.c.page + (t & (a.c.page - 1));
+                look_up(n + 1);
+                for (int kv = 0; kv < 2; ++kv, ++issued) {
+                    const int s = issued & (ST - 1);
+                    if (issued >= ST) wait(&empty[s], issued / ST - 1);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        if (kv == 0) {   // a bit for each 16 keys
+                            uint32_t groups = 0;
+                            for (int u = 0; u < kPKeys / 16; ++u) groups |= ((mapped >> (16 * u / box_rows)) & 1u) << u;
+                            block_mapped[(issued >> 1) & 15] = groups;
+                        }
+                        mbar_arrive_expect_tx(&full[s], (uint32_t)(__popc(mapped) * box_rows * DH * 2));
+                    }
+                    __syncwarp();
+                    if (there)
 #pragma unroll
-                    for (int h = 0; h < S::HALVES; ++h)
-                        tma_load_2d(ring + s * S::TILE + h * (kPKeys * 128) + lane * box_rows * 128, kv ? &tmV : &tmK, h * 64,
-                                    pool_row, &full[s]);
+                        for (int h = 0; h < S::HALVES; ++h)
+                            tma_load_2d(ring + s * S::TILE + h * (kPKeys * 128) + lane * box_rows * 128, kv ? &maps.v : &maps.k,
+                                        h * 64, pool_row, &full[s]);
+                }
             }
         }
         // no copy outlives the CTA: after a wait that gave up, each gets another bounded while
         if (!ok)
-            for (int k = max(0, issued - ST); k < issued; ++k) mbar_wait(&full[k % ST], (uint32_t)((k / ST) & 1), nullptr);
+            for (int k = max(0, issued - ST); k < issued; ++k) mbar_wait(&full[k & (ST - 1)], (uint32_t)((k / ST) & 1), nullptr);
     } else if (warp == 1) {
         // ---- products ----
         constexpr uint32_t ID_S = umma_idesc(!F16, false, 128, kPKeys), ID_O = umma_idesc(!F16, true, 128, DH);
-        const int nb_u = __shfl_sync(0xffffffffu, nb, 0);
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
         uint32_t fine = 1;
         const uint64_t q_desc = desc_sw128(smem_u32(Qs)), k_desc = desc_sw128(smem_u32(ring)),
@@ -225,9 +298,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
         auto mma_s = [&](int i, int s) {   // S_i = Q_i K^T
 #pragma unroll
             for (int c = 0; c < DH / 16; ++c) {
-                const uint32_t off = (uint32_t)((c >> 2) * (128 * 128) + (c & 3) * 32) / 16;
-                tc_mma(tm + S::S0 + (uint32_t)(i * 128), q_desc + (uint32_t)(i * (S::TILE / 16)) + off,
-                       k_desc + (uint32_t)s * (S::TILE / 16) + off, ID_S, c != 0);
+                tc_mma(tm + S::S0 + (uint32_t)(i * 128),
+                       q_desc + (uint32_t)((i * (128 * 128) + (c >> 2) * (256 * 128) + (c & 3) * 32) / 16),
+                       k_desc + (uint32_t)s * (S::TILE / 16) + (uint32_t)(((c >> 2) * (128 * 128) + (c & 3) * 32) / 16), ID_S, c != 0);
             }
             tc_commit(&s_full[i]);
         };
@@ -238,56 +311,56 @@ __global__ void __launch_bounds__(kPThreads, 1)
                           v_desc + (uint32_t)s * (S::TILE / 16) + (uint32_t)(c * 2048 / 16), ID_O, c != 0 || !first);
             tc_commit(&o_done[i]);
         };
-        auto wait = [&](uint64_t* bar, uint32_t parity) {   // after one that gave up the others are short, and what is computed is not used
-            fine &= mbar_poll(bar, parity, fine ? (uint32_t)kWaitLimit : 1u);
+        auto hold = [&](uint64_t* bar, int phase) {   // as wait(), with control flow that is the same in all lanes
+            fine &= mbar_poll(bar, (uint32_t)(phase & 1), fine ? (uint32_t)kWaitLimit : 1u);
             __syncwarp();
         };
-        if (nb_u > 0) {
-            wait(&q_ready, 0);
-            wait(&full[0], 0);
-            tc_fence_after();
-            if (elect_one()) {
+        auto slot = [](int k) { return k & (ST - 1); };
+        int g = 0;
+        for (int t = 0; t <= items; ++t) {
+            hold(&q_ready[t & 1], t >> 1);
+            const int nb = __shfl_sync(0xffffffffu, work[t & 3].nb, 0);
+            if (nb < 0) break;
+            if (nb > 0) {
+                hold(&full[slot(2 * g)], 2 * g / ST);
+                tc_fence_after();
+                if (elect_one()) {
+                    mma_s(0, slot(2 * g));
+                    mma_s(1, slot(2 * g));
+                    tc_commit(&empty[slot(2 * g)]);
+                }
+                __syncwarp();
+                if (t > 0) hold(&o_free[(t - 1) & 1], (t - 1) >> 1);   // the outputs of the piece before were read
+                if (nb == 1) {
+                    if (elect_one()) tc_commit(&q_free);
+                    __syncwarp();
+                }
+            } else {
+                if (t > 0) hold(&o_free[(t - 1) & 1], (t - 1) >> 1);
+                if (lane == 0) mbar_arrive(&q_free);
+                __syncwarp();
+            }
+            for (int n = 0; n < nb; ++n, ++g) {
+                const bool more = n + 1 < nb;
+                const int sv = slot(2 * g + 1), sk = slot(2 * g + 2);
+                hold(&clean[g & 3], g >> 2);   // the values are there and clean
+                if (more) hold(&full[sk], (2 * g + 2) / ST);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    mma_s(i, 0);
-                }
-                tc_commit(&empty[0]);
-            }
-            __syncwarp();
-        }
-        int sv = 1, sk = 2, pk = 0;   // ring slots of block n's values and block n + 1's keys, the keys' phase
-        for (int n = 0; n < nb_u - 1; ++n) {
-            wait(&clean[n & 3], (uint32_t)((n >> 2) & 1));   // the values are there and clean
-            wait(&full[sk], (uint32_t)pk);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                wait(&p_ready[i], (uint32_t)(n & 1));
-                tc_fence_after();
-                if (elect_one()) {
-                    if constexpr (S::P_APART) mma_s(i, sk);
-                    mma_o(i, sv, n == 0);
-                    if constexpr (!S::P_APART) mma_s(i, sk);
-                    if (i == 1) {
-                        tc_commit(&empty[sv]);
-                        tc_commit(&empty[sk]);
+                    hold(&p_ready[i], g);
+                    tc_fence_after();
+                    if (elect_one()) {
+                        if (S::P_APART && more) mma_s(i, sk);
+                        mma_o(i, sv, n == 0);
+                        if (!S::P_APART && more) mma_s(i, sk);
+                        if (i == 1) {
+                            tc_commit(&empty[sv]);
+                            if (more) tc_commit(&empty[sk]);
+                            if (n + 2 == nb) tc_commit(&q_free);
+                        }
                     }
+                    __syncwarp();
                 }
-                __syncwarp();
-            }
-            if ((sv += 2) >= ST) sv -= ST;
-            if ((sk += 2) >= ST) sk -= ST, pk ^= 1;
-        }
-        if (nb_u > 0) {
-            const int n = nb_u - 1;
-            wait(&clean[n & 3], (uint32_t)((n >> 2) & 1));
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                wait(&p_ready[i], (uint32_t)(n & 1));
-                tc_fence_after();
-                if (elect_one()) {
-                    mma_o(i, sv, n == 0);
-                }
-                __syncwarp();
             }
         }
         if (!fine) {   // no product outlives the tensor memory
@@ -297,233 +370,270 @@ __global__ void __launch_bounds__(kPThreads, 1)
             }
             mbar_wait(&drained, 0, nullptr);
         }
-    } else if (warp < 4) {
-        // ---- values that not every row of the CTA sees: those that no row sees become 0, and so do infinities and
+    } else if (warp == 2) {
+        // ---- the pieces, handed out as CTAs come for them (the first by index), and their rows of Q ----
+        for (int t = 0; t <= items; ++t) {
+            int item = blockIdx.x;
+            if (t > 0) {
+                if (lane == 0) {
+                    const int k = atomicAdd(a.ticket, 1);   // each CTA takes one behind the last piece: `items` in all
+                    if (k == items - 1) *a.ticket = 0;
+                    item = (int)gridDim.x + k;
+                }
+                item = __shfl_sync(0xffffffffu, item, 0);
+            }
+            const PromptWork w = prompt_work(a, tiles, splits, item);
+            if (lane == 0) {
+                work[t & 3] = w;
+                odd_values[t & 3] = 0;
+                mbar_arrive(&work_ready[t & 1]);
+            }
+            if (t > 0) wait(&q_free, t - 1);   // the scores of the piece before are complete
+            if (lane == 0) {
+                if (w.nb > 0 && ok) {
+                    mbar_arrive_expect_tx(&q_ready[t & 1], (uint32_t)(kPRows / G * G * DH * 2));
+                    for (int h = 0; h < S::HALVES; ++h)
+                        tma_load_3d(Qs + h * (256 * 128), &maps.q, h * 64, w.j * G, w.row0 + w.r0 / G, &q_ready[t & 1]);
+                } else {
+                    mbar_arrive(&q_ready[t & 1]);
+                }
+            }
+            __syncwarp();
+            if (w.nb < 0) break;
+        }
+    } else if (warp == 3) {
+        // ---- values that not every row of the tile sees: those that no row sees become 0, and so do infinities and
         // NaN (the rows that see them get them at the end), so that a weight of 0 takes nothing in ----
-        const int t64 = tid - 64;
-        for (int n = 0; n < nb && ok; ++n) {
-            const int kv = 2 * n + 1, s = kv % ST, t0 = kb.block(b0 + n) * kPKeys;
-            ok = __all_sync(0xffffffffu, mbar_wait(&full[s], (uint32_t)((kv / ST) & 1), a.c.status));
-            if (!ok) break;
-            const uint32_t groups = block_mapped[n & 15];
-            const bool whole = groups == 0xffu && t0 + kPKeys - 1 <= p_lo &&
-                               (a.c.window == 0 || t0 > p_hi - a.c.window || t0 + kPKeys - 1 < a.c.sinks);
-            if (!whole) {
-                uint8_t* Vs = ring + s * S::TILE;
-                constexpr int ROW = S::HALVES * 8;   // 16-byte chunks of a row
-                auto chunk_at = [&](int r, int c) {
-                    return reinterpret_cast<uint4*>(Vs + (c >> 3) * (kPKeys * 128) + r * 128 + (c & 7) * 16);   // any order of a row's
-                };
-                bool odd = false;
-                // rows r0 .. r1 - 1 of the block: seen by none (`none`), or by some
-                auto sweep = [&](int first, int last, bool none) {
-                    const int n_chunks = max(last - first, 0) * ROW;
+        int g = 0;
+        for (int t = 0; t <= items; ++t) {
+            wait(&q_ready[t & 1], t >> 1);
+            const PromptWork w = work[t & 3];
+            if (w.nb < 0) break;
+            for (int n = 0; n < w.nb; ++n, ++g) {
+                const int s = (2 * g + 1) & (ST - 1), t0 = w.kb.block(w.b0 + n) * kPKeys;
+                wait(&full[s], (2 * g + 1) / ST);
+                const uint32_t groups = block_mapped[g & 15];
+                const bool whole = groups == 0xffu && t0 + kPKeys - 1 <= w.p_lo &&
+                                   (a.c.window == 0 || t0 > w.p_hi - a.c.window || t0 + kPKeys - 1 < a.c.sinks);
+                if (!whole && ok) {
+                    uint8_t* Vs = ring + s * S::TILE;
+                    constexpr int ROW = S::HALVES * 8;   // 16-byte chunks of a row (their order does not matter)
+                    bool odd = false;
+                    // rows first .. last - 1 of the block: seen by none, or by some
+                    auto sweep = [&](int first, int last, bool none) {
+                        const int n_chunks = max(last - first, 0) * ROW;
 #pragma unroll 4
-                    for (int k = t64; k < n_chunks; k += 64) {
-                        uint4* at = chunk_at(first + k / ROW, k % ROW);
-                        if (none) {
-                            *at = make_uint4(0u, 0u, 0u, 0u);
-                        } else {
-                            const uint4 x = *at;
-                            if (any_nonfinite<F16>(x)) {
-                                odd = true;
-                                *at = make_uint4(finite2<F16>(x.x), finite2<F16>(x.y), finite2<F16>(x.z), finite2<F16>(x.w));
+                        for (int k = lane; k < n_chunks; k += 32) {
+                            const int c = k % ROW;
+                            uint4* at = reinterpret_cast<uint4*>(Vs + (c >> 3) * (kPKeys * 128) + (first + k / ROW) * 128 + (c & 7) * 16);
+                            if (none) {
+                                *at = make_uint4(0u, 0u, 0u, 0u);
+                            } else {
+                                const uint4 x = *at;
+                                if (any_nonfinite<F16>(x)) {
+                                    odd = true;
+                                    *at = make_uint4(finite2<F16>(x.x), finite2<F16>(x.y), finite2<F16>(x.z), finite2<F16>(x.w));
+                                }
                             }
                         }
+                        __syncwarp();
+                    };
+                    auto clip = [&](long long at) { return (int)(at < t0 ? 0 : at > t0 + kPKeys ? kPKeys : at - t0); };
+                    // no page: whatever an earlier block left there
+                    for (int u = 0; u < kPKeys / 16; ++u)
+                        if (!((groups >> u) & 1u)) sweep(16 * u, 16 * u + 16, true);
+                    sweep(clip(w.p_lo + 1LL), clip(w.p_hi + 1LL), false);   // the first row sees up to p_lo, the last to p_hi
+                    sweep(clip(w.p_hi + 1LL), kPKeys, true);
+                    if (a.c.window > 0) {                                    // and from p_lo - window + 1 on, behind the sinks
+                        const long long from = w.p_lo - (long long)a.c.window + 1, to = w.p_hi - (long long)a.c.window + 1;
+                        sweep(clip(a.c.sinks), clip(from), true);
+                        sweep(clip(from > a.c.sinks ? from : a.c.sinks), clip(to), false);
                     }
-                };
-                auto clip = [&](long long t) { return (int)(t < t0 ? 0 : t > t0 + kPKeys ? kPKeys : t - t0); };
-                // no page: whatever an earlier block left there
-                for (int u = 0; u < kPKeys / 16; ++u)
-                    if (!((groups >> u) & 1u)) sweep(16 * u, 16 * u + 16, true);
-                sweep(clip(p_lo + 1LL), clip(p_hi + 1LL), false);     // the first row sees up to p_lo, the last up to p_hi
-                sweep(clip(p_hi + 1LL), kPKeys, true);
-                if (a.c.window > 0) {                                  // and from p_lo - window + 1 on, behind the sinks
-                    const long long from = p_lo - (long long)a.c.window + 1, to = p_hi - (long long)a.c.window + 1;
-                    sweep(clip(a.c.sinks), clip(from), true);
-                    sweep(clip(from > a.c.sinks ? from : a.c.sinks), clip(to), false);
+                    if (odd) odd_values[t & 3] = 1;
+                    fence_proxy_async();
                 }
-                if (odd) odd_values = 1;
-                fence_proxy_async();
+                mbar_arrive(&clean[g & 3]);
             }
-            mbar_arrive(&clean[n & 3]);
+            mbar_arrive(&o_free[t & 1]);   // this role is done with the piece, too
         }
     } else {
         // ---- rows: a row's scores of a block belong to two threads, a half each, whose warps (and those of the other
         // tile) share the special function units of an SM quarter ----
         const int i = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1, quarter = warp & 3, rr = quarter * 32 + lane;
-        const int r = r0 + i * 128 + rr;
-        const bool in = r < n_rows;
-        const int token = o.row0 + (in ? r / G : 0), head = j * G + (in ? r % G : 0);
-        {   // every second group of the warp's 32 rows of Q, DH / 8 lanes to a row
-            constexpr int CH = DH / 8;
-            const long long mine = in ? (long long)token * a.q_ld + (long long)head * DH : -1;
-#pragma unroll
-            for (int it = 0; it < CH / 2; ++it) {
-                const int row = (2 * it + half) * (32 / CH) + lane / CH, c = lane % CH, at = quarter * 32 + row;
-                const long long from = __shfl_sync(0xffffffffu, mine, row);
-                cp_async16(Qs + i * S::TILE + (c >> 3) * (128 * 128) + at * 128 + (((c & 7) ^ (at & 7)) << 4),
-                           a.q + (from < 0 ? 0 : from) + c * 8, from >= 0);
-            }
-            cp_async_commit();
-            cp_async_wait<0>();
-        }
-        fence_proxy_async();
-        mbar_arrive(&q_ready);
-        const PromptRow me{o.p0 + r / G, a.c.window, a.c.sinks};
-        const int w_lo = o.p0 + (r - lane) / G, w_hi = o.p0 + (r - lane + 31) / G;   // the warp's rows
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         const uint32_t tS = tmem + lanes + S::S0 + (uint32_t)(i * 128 + half * 64), tO = tmem + lanes + S::O0 + (uint32_t)(i * DH),
                        tP = tmem + lanes + S::P0 + (uint32_t)(i * S::P_STEP + half * S::P_HALF);
-        auto wait = [&](uint64_t* bar, int phase) {   // after one that gave up none waits, and what is computed is not used
-            ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, (uint32_t)(phase & 1), a.c.status));
-        };
         const int pair = 1 + i * 4 + quarter;   // the barrier of the rows' two warps
-        // m: the maximum under which the row's weights stand (its threads agree on it); l: the sum of this thread's
-        float m = -INFINITY, l = 0.0f;
         const float2 by = make_float2(a.scale_log2, a.scale_log2);
-        for (int n = 0; n < nb; ++n) {
-            const int t0 = kb.block(b0 + n) * kPKeys + half * 64;
-            wait(&s_full[i], n);
-            tc_fence_after();
-            const uint32_t groups = block_mapped[n & 15] >> (4 * half);
-            const bool whole = (groups & 0xfu) == 0xfu && t0 + 63 <= w_lo &&
-                               (a.c.window == 0 || t0 > w_hi - a.c.window || t0 + 63 < a.c.sinks);
-            float t4[4], v[32];
-            float2 part[2];
-            uint32_t pk[2][16];
-            auto take = [&](int c) {   // scores of columns c .. c + 31, -inf where not seen, and their maximum
-                tc_ld32(tS + (uint32_t)c, v);
-                if (!whole) {
-                    const uint32_t seen = me.seen(t0 + c, groups >> (c >> 4));
+        int g = 0;
+        for (int t = 0; t <= items; ++t) {
+            wait(&q_ready[t & 1], t >> 1);
+            const PromptWork& w = work[t & 3];
+            const int nb = w.nb, r = w.r0 + i * 128 + rr;
+            if (nb < 0) break;
+            const bool in = r < w.r1;   // rows behind the tile's last decide nothing (whatever their Q is)
+            const PromptRow me{w.p0 + r / G, a.c.window, a.c.sinks};
+            const int w_lo = w.p0 + (r - lane) / G, w_hi = w.p0 + (r - lane + 31) / G;   // the warp's rows
+            // m: the maximum under which the row's weights stand (its threads agree on it); l: the sum of this thread's
+            float m = -INFINITY, l = 0.0f;
+            for (int n = 0; n < nb; ++n, ++g) {
+                const int t0 = w.kb.block(w.b0 + n) * kPKeys + half * 64;
+                wait(&s_full[i], g);
+                tc_fence_after();
+                const uint32_t groups = block_mapped[g & 15] >> (4 * half);
+                const bool whole = (groups & 0xfu) == 0xfu && t0 + 63 <= w_lo &&
+                                   (a.c.window == 0 || t0 > w_hi - a.c.window || t0 + 63 < a.c.sinks);
+                float t4[4], v[32];
+                float2 part[2];
+                uint32_t pk[2][16];
+                auto take = [&](int c) {   // scores of columns c .. c + 31, -inf where not seen, and their maximum
+                    tc_ld32(tS + (uint32_t)c, v);
+                    if (!whole) {
+                        const uint32_t seen = me.seen(t0 + c, groups >> (c >> 4));
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) v[e] = (seen >> e) & 1u ? v[e] : -INFINITY;
-                }
-#pragma unroll
-                for (int e = 0; e < 32; e += 8)
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) t4[u] = max3(t4[u], v[e + u], v[e + 4 + u]);
-            };
-            // the weights 2^(z scale - base): added to the sum, and rounded to 16 bits as the tensor core takes them (2^-9
-            // of a weight in bf16, 2^-12 in fp16); 0 where not seen
-            auto weigh = [&](uint32_t (&u)[16], float2 off) {
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    float2 z = fma2(make_float2(v[2 * e], v[2 * e + 1]), by, off);
-                    z.x = exp2_approx(z.x);
-                    z.y = exp2_approx(z.y);
-                    part[e & 1] = add2(part[e & 1], z);
-                    u[e] = pack16<F16>(z.x, z.y);
-                }
-            };
-            auto clear = [&]() {
-                part[0] = part[1] = make_float2(0.0f, 0.0f);
-                t4[0] = t4[1] = t4[2] = t4[3] = -INFINITY;
-            };
-            auto top = [&]() { return max3(t4[0], max3(t4[1], t4[2], t4[3]), t4[3]) * a.scale_log2; };   // scale above 0
-            // the weights under the maximum that stands, which holds nearly always: the scores are passed over once
-            clear();
-            const float2 off = make_float2(-m, -m);
-            take(0);
-            weigh(pk[0], off);
-            take(32);
-            weigh(pk[1], off);
-            if (any_of_pair(pair, !(top() <= m + 8.0f) || m == -INFINITY)) {   // (not where a score is not a number)
-                // it moves where it grew by more than 8 (a factor of 2^8), or was none (then all weights so far were 0)
-                float tp = top();
-                if (half == 0) top_x[i][rr] = tp;
-                sync_pair(pair);
-                if (half == 1) top_x[i][rr] = max3(tp, top_x[i][rr], tp);
-                sync_pair(pair);
-                tp = top_x[i][rr];
-                const float m_new = tp <= m + 8.0f ? m : tp;   // NaN moves it too, and makes the row's sum NaN
-                const float f = m == -INFINITY || m_new == m ? 1.0f : exp2_approx(m - m_new);
-                m = m_new;
-                l *= f;
-                if (n > 0 && __any_sync(0xffffffffu, f != 1.0f)) {   // the products so far are in O_i; a half of it each
-                    wait(&o_done[i], n - 1);
-                    tc_fence_after();
-#pragma unroll 1
-                    for (int c = half * (DH / 2); c < (half + 1) * (DH / 2); c += 16) {
-                        float x[16];
-                        tc_ld16(tO + (uint32_t)c, x);
-                        uint32_t u[16];
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(x[e] * f);
-                        tc_st16(tO + (uint32_t)c, u);
+                        for (int e = 0; e < 32; ++e) v[e] = (seen >> e) & 1u ? v[e] : -INFINITY;
                     }
-                }
-                const float base = m == -INFINITY ? 0.0f : m;
-                const float2 off_new = make_float2(-base, -base);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8)
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) t4[u] = max3(t4[u], v[e + u], v[e + 4 + u]);
+                };
+                // the weights 2^(z scale - base): added to the sum, and rounded to 16 bits as the tensor core takes them
+                // (2^-9 of a weight in bf16, 2^-12 in fp16); 0 where not seen
+                auto weigh = [&](uint32_t (&u)[16], float2 off) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        float2 z = fma2(make_float2(v[2 * e], v[2 * e + 1]), by, off);
+                        z.x = exp2_approx(z.x);
+                        z.y = exp2_approx(z.y);
+                        part[e & 1] = add2(part[e & 1], z);
+                        u[e] = pack16<F16>(z.x, z.y);
+                    }
+                };
+                auto clear = [&]() {
+                    part[0] = part[1] = make_float2(0.0f, 0.0f);
+                    t4[0] = t4[1] = t4[2] = t4[3] = -INFINITY;
+                };
+                auto top = [&]() { return max3(t4[0], max3(t4[1], t4[2], t4[3]), t4[3]) * a.scale_log2; };   // scale above 0
+                // the weights under the maximum that stands, which holds nearly always: the scores are passed over once
                 clear();
+                const bool standing = __all_sync(0xffffffffu, m != -INFINITY || !in);   // of the same rows in both warps
                 take(0);
-                weigh(pk[0], off_new);
+                if (standing) weigh(pk[0], make_float2(-m, -m));
                 take(32);
-                weigh(pk[1], off_new);
+                if (standing) weigh(pk[1], make_float2(-m, -m));
+                if (!standing || any_of_pair(pair, in && !(top() <= m + 8.0f))) {   // (not where a score is not a number)
+                    // it moves where it grew by more than 8 (a factor of 2^8), or was none (then all weights so far were 0)
+                    float tp = top();
+                    if (half == 0) top_x[i][rr] = tp;
+                    sync_pair(pair);
+                    if (half == 1) top_x[i][rr] = max3(tp, top_x[i][rr], tp);
+                    sync_pair(pair);
+                    tp = top_x[i][rr];
+                    const float m_new = tp <= m + 8.0f ? m : tp;   // NaN moves it too, and makes the row's sum NaN
+                    const float f = !in || m == -INFINITY || m_new == m ? 1.0f : exp2_approx(m - m_new);
+                    m = m_new;
+                    l *= f;
+                    if (n > 0 && __any_sync(0xffffffffu, f != 1.0f)) {   // the products so far are in O_i; a half of it each
+                        wait(&o_done[i], g - 1);
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c = half * (DH / 2); c < (half + 1) * (DH / 2); c += 16) {
+                            float x[16];
+                            tc_ld16(tO + (uint32_t)c, x);
+                            uint32_t u[16];
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(x[e] * f);
+                            tc_st16(tO + (uint32_t)c, u);
+                        }
+                    }
+                    const float base = m == -INFINITY ? 0.0f : m;
+                    const float2 off_new = make_float2(-base, -base);
+                    clear();
+                    take(0);
+                    weigh(pk[0], off_new);
+                    take(32);
+                    weigh(pk[1], off_new);
+                }
+                l += (part[0].x + part[0].y) + (part[1].x + part[1].y);
+                if (S::P_APART && g > 0) {   // the products with the weights before are complete (elsewhere: they were before S)
+                    wait(&o_done[i], g - 1);
+                    tc_fence_after();
+                }
+                tc_st16(tP, pk[0]);
+                tc_st16(tP + 16, pk[1]);
+                tc_wait_st();
+                tc_fence_before();
+                mbar_arrive(&p_ready[i]);
             }
-            l += (part[0].x + part[0].y) + (part[1].x + part[1].y);
-            if (S::P_APART && n > 0) {   // the products with the weights before are complete (elsewhere: they were before S)
-                wait(&o_done[i], n - 1);
+            // ---- out, or a split's record: [256][DH] sums, [256] maxima, [256] sums of weights ----
+            if (nb > 0) {
+                l_part[i][half][rr] = l;
+                sync_pair(pair);
+                l = l_part[i][0][rr] + l_part[i][1][rr];
+            }
+            const int at = i * 128 + rr;
+            const long long mine = in ? (long long)(w.row0 + r / G) * a.out_ld + (long long)(w.j * G + r % G) * DH : -1;
+            long long to[4];   // where the rows of the thread's group of four go
+#pragma unroll
+            for (int u = 0; u < 4; ++u) to[u] = __shfl_sync(0xffffffffu, mine, (lane & ~3) + u);
+            const float inv = splits > 1 ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
+            float* rec = a.partial + ((size_t)w.unit * splits + w.split) * (kPRows * (DH + 2));
+            if (nb > 0) {
+                wait(&o_done[i], g - 1);
                 tc_fence_after();
             }
-            tc_st16(tP, pk[0]);
-            tc_st16(tP + 16, pk[1]);
-            tc_wait_st();
-            tc_fence_before();
-            mbar_arrive(&p_ready[i]);
-        }
-        if (nb > 0) {
-            wait(&o_done[i], nb - 1);
-            tc_fence_after();
-        }
-        // the row's sum, by way of the room of Q (its last products are complete)
-        float* l_part = reinterpret_cast<float*>(Qs + i * S::TILE);
-        l_part[half * 128 + rr] = l;
-        sync_pair(pair);
-        l = l_part[rr] + l_part[128 + rr];
-        // ---- out, or a split's record: [256][DH] sums, [256] maxima, [256] sums of weights ----
-        const bool odd = odd_values != 0;
-        const float inv = splits > 1 ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
-        const int unit = blockIdx.x * gridDim.y + j, at = i * 128 + rr;
-        float* rec = a.partial + ((size_t)unit * splits + split) * (kPRows * (DH + 2));
-        uint16_t* to = a.out + (size_t)token * a.out_ld + (size_t)head * DH;
+            const bool odd = odd_values[t & 3] != 0;
 #pragma unroll 1
-        for (int c = half * (DH / 2); c < (half + 1) * (DH / 2) && ok; c += 32) {   // a half each
-            float v[32];
-            if (nb > 0) tc_ld32(tO + (uint32_t)c, v);
-            else
+            for (int c = half * (DH / 2); c < (half + 1) * (DH / 2); c += 32) {   // a half each
+                float v[32];
+                if (nb > 0) tc_ld32(tO + (uint32_t)c, v);
+                else
 #pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] = 0.0f;
-            if (!in) continue;
+                    for (int e = 0; e < 32; ++e) v[e] = 0.0f;
+                if (c + 32 == (half + 1) * (DH / 2)) {   // O_i may be written again
+                    tc_fence_before();
+                    mbar_arrive(&o_free[t & 1]);
+                }
+                if (!ok) continue;
 #pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] *= inv;
-            if (odd)   // the infinities and NaN that were taken out of the values, to the rows that see them
-                for (int n = 0; n < nb; ++n)
-                    for (int u = 0; u < kPKeys; ++u) {
-                        const int t = kb.block(b0 + n) * kPKeys + u;
-                        if (t > me.p || !(a.c.window == 0 || t < a.c.sinks || t > me.p - a.c.window)) continue;
-                        const int e = page_of(a.c, o.s, t >> a.c.page_shift);
-                        if (e < 0) continue;
-                        const uint16_t* x = a.c.v + (((size_t)e * a.c.Hk + j) * a.c.page + (t & (a.c.page - 1))) * DH + c;
+                for (int e = 0; e < 32; ++e) v[e] *= inv;
+                if (odd && in)   // the infinities and NaN that were taken out of the values, to the rows that see them
+                    for (int n = 0; n < nb; ++n)
+                        for (int u = 0; u < kPKeys; ++u) {
+                            const int p = w.kb.block(w.b0 + n) * kPKeys + u;
+                            if (p > me.p || !(a.c.window == 0 || p < a.c.sinks || p > me.p - a.c.window)) continue;
+                            const int e = page_of(a.c, w.s, p >> a.c.page_shift);
+                            if (e < 0) continue;
+                            const uint16_t* x = a.c.v + (((size_t)e * a.c.Hk + w.j) * a.c.page + (p & (a.c.page - 1))) * DH + c;
 #pragma unroll
-                        for (int q = 0; q < 32; ++q)
-                            if ((x[q] & exponent_mask<F16>()) == exponent_mask<F16>()) v[q] += unpack16<F16>(x[q]);
-                    }
-            if (splits == 1) {
+                            for (int q = 0; q < 32; ++q)
+                                if ((x[q] & exponent_mask<F16>()) == exponent_mask<F16>()) v[q] += unpack16<F16>(x[q]);
+                        }
+                if (splits == 1) {
+                    // four lanes exchange the 16-byte pieces of their rows, so that each writes 64 bytes of a row together
+                    uint4 x[4];
 #pragma unroll
-                for (int e = 0; e < 32; e += 8)
-                    *reinterpret_cast<uint4*>(to + c + e) =
-                        make_uint4(pack16<F16>(v[e], v[e + 1]), pack16<F16>(v[e + 2], v[e + 3]), pack16<F16>(v[e + 4], v[e + 5]),
-                                   pack16<F16>(v[e + 6], v[e + 7]));
-            } else {
+                    for (int u = 0; u < 4; ++u)
+                        x[u] = make_uint4(pack16<F16>(v[8 * u], v[8 * u + 1]), pack16<F16>(v[8 * u + 2], v[8 * u + 3]),
+                                          pack16<F16>(v[8 * u + 4], v[8 * u + 5]), pack16<F16>(v[8 * u + 6], v[8 * u + 7]));
+                    swap_lanes(x[0], x[1], 1, lane & 1);
+                    swap_lanes(x[2], x[3], 1, lane & 1);
+                    swap_lanes(x[0], x[2], 2, lane & 2);
+                    swap_lanes(x[1], x[3], 2, lane & 2);
 #pragma unroll
-                for (int e = 0; e < 32; e += 4)
-                    __stcg(reinterpret_cast<float4*>(rec + at * DH + c + e), make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]));
+                    for (int u = 0; u < 4; ++u)
+                        if (to[u] >= 0) *reinterpret_cast<uint4*>(a.out + to[u] + c + (lane & 3) * 8) = x[u];
+                } else if (in) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        __stcg(reinterpret_cast<float4*>(rec + at * DH + c + e), make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]));
+                }
             }
-        }
-        if (splits > 1 && half == 0) {
-            __stcg(rec + kPRows * DH + at, m);
-            __stcg(rec + kPRows * DH + kPRows + at, l);
+            if (splits > 1 && half == 0 && in) {
+                __stcg(rec + kPRows * DH + at, m);
+                __stcg(rec + kPRows * DH + kPRows + at, l);
+            }
         }
     }
     tc_fence_before();
@@ -535,19 +645,20 @@ __global__ void __launch_bounds__(kPThreads, 1)
     }
     if (splits == 1) return;
 
-    // ---- the last split of the tile to arrive joins them in order ----
-    const int unit = blockIdx.x * gridDim.y + j;
+    // ---- the last split of the tile to arrive joins them in order (a CTA has one piece where tiles are split) ----
+    const PromptWork& w = work[0];
+    if (w.n_rows == 0) return;
     if (tid == 0) {
         __threadfence();   // the CTA's record, ordered by the barrier, before its arrival
-        last_flag = atomicAdd(a.merge + unit, 1) == splits - 1;
-        if (last_flag) a.merge[unit] = 0;
+        last_flag = atomicAdd(a.merge + w.unit, 1) == splits - 1;
+        if (last_flag) a.merge[w.unit] = 0;
         __threadfence();
     }
     __syncthreads();
     if (!last_flag) return;
     constexpr int REC = kPRows * (DH + 2);
-    const float* all = a.partial + (size_t)unit * splits * REC;
-    for (int idx = tid; idx < min(kPRows, n_rows - r0) * (DH / 4); idx += kPThreads) {
+    const float* all = a.partial + (size_t)w.unit * splits * REC;
+    for (int idx = tid; idx < (w.r1 - w.r0) * (DH / 4); idx += kPThreads) {
         const int r = idx / (DH / 4), d = 4 * (idx % (DH / 4));
         float top = -INFINITY;
         for (int sp = 0; sp < splits; ++sp) top = fmaxf(top, __ldcg(all + (size_t)sp * REC + kPRows * DH + r));
@@ -556,14 +667,14 @@ __global__ void __launch_bounds__(kPThreads, 1)
 #pragma unroll 4
         for (int sp = 0; sp < splits; ++sp) {   // a split that saw nothing: maximum -inf, factor 0, sums 0
             const float* p = all + (size_t)sp * REC;
-            const float w = exp2_approx(__ldcg(p + kPRows * DH + r) - top);
+            const float f = exp2_approx(__ldcg(p + kPRows * DH + r) - top);
             const float4 x = __ldcg(reinterpret_cast<const float4*>(p + r * DH + d));
-            sum = fmaf(__ldcg(p + kPRows * DH + kPRows + r), w, sum);
-            v[0] = fmaf(x.x, w, v[0]); v[1] = fmaf(x.y, w, v[1]);
-            v[2] = fmaf(x.z, w, v[2]); v[3] = fmaf(x.w, w, v[3]);
+            sum = fmaf(__ldcg(p + kPRows * DH + kPRows + r), f, sum);
+            v[0] = fmaf(x.x, f, v[0]); v[1] = fmaf(x.y, f, v[1]);
+            v[2] = fmaf(x.z, f, v[2]); v[3] = fmaf(x.w, f, v[3]);
         }
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-        uint16_t* to = a.out + (size_t)(o.row0 + (r0 + r) / G) * a.out_ld + (size_t)(j * G + (r0 + r) % G) * DH + d;
+        uint16_t* to = a.out + (size_t)(w.row0 + (w.r0 + r) / G) * a.out_ld + (size_t)(w.j * G + (w.r0 + r) % G) * DH + d;
         *reinterpret_cast<uint2*>(to) = make_uint2(pack16<F16>(v[0] * inv, v[1] * inv), pack16<F16>(v[2] * inv, v[3] * inv));
     }
 }
@@ -572,21 +683,31 @@ template <int DH, bool F16>
 static cudaError_t launch_prompts_t(const PagedAttnArgs& a, cudaStream_t s) {
     using S = PromptShape<DH>;
     const long long G = a.c.Hq / a.c.Hk;
+    if (G > kPRows) return cudaErrorNotSupported;
     // at most: every session's last tile may be part-filled
-    const long long tiles = (a.rows * G + kPRows - 1) / kPRows + a.batch;
-    if (tiles > INT32_MAX || a.c.Hk > 65535) return cudaErrorNotSupported;
-    const long long units = tiles * a.c.Hk;
+    const long long tile_rows = kPRows / G * G, tiles = (a.rows * G + tile_rows - 1) / tile_rows + a.batch,
+                    units = tiles * a.c.Hk;
+    if (units > INT32_MAX) return cudaErrorNotSupported;
     const int splits = units < a.num_sms ? (int)(a.num_sms / units) : 1;
-    CUtensorMap mk, mv;
+    PromptMaps maps;
     const int rows = a.c.pages * a.c.Hk * a.c.page, box = a.c.page < kPKeys ? a.c.page : kPKeys;
-    if (!tma_map_2d(&mk, a.c.k, rows, DH, DH, 64, box, F16, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !tma_map_2d(&mv, a.c.v, rows, DH, DH, 64, box, F16, CU_TENSOR_MAP_SWIZZLE_128B))
+    EncodeTiledFn encode = tma_encode_fn();
+    // a tile's rows of Q: whole tokens, the heads of one KV head of each, packed as they come
+    const cuuint64_t dims[3] = {(cuuint64_t)DH, (cuuint64_t)a.c.Hq, (cuuint64_t)a.rows};
+    const cuuint64_t strides[2] = {(cuuint64_t)DH * 2, (cuuint64_t)a.q_ld * 2};
+    const cuuint32_t q_box[3] = {64, (cuuint32_t)G, (cuuint32_t)(kPRows / G)}, unit[3] = {1, 1, 1};
+    if (!encode ||
+        encode(&maps.q, F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(a.q),
+               dims, strides, q_box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS ||
+        !tma_map_2d(&maps.k, a.c.k, rows, DH, DH, 64, box, F16, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !tma_map_2d(&maps.v, a.c.v, rows, DH, DH, 64, box, F16, CU_TENSOR_MAP_SWIZZLE_128B))
         return cudaErrorInvalidValue;
     auto kern = paged_prompt_kernel<DH, F16>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::BYTES);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)tiles, (unsigned)a.c.Hk, (unsigned)splits);
+    cfg.gridDim = dim3((unsigned)(units * splits < a.num_sms ? units * splits : a.num_sms));
     cfg.blockDim = dim3(kPThreads);
     cfg.dynamicSmemBytes = S::BYTES;
     cfg.stream = s;
@@ -595,7 +716,7 @@ static cudaError_t launch_prompts_t(const PagedAttnArgs& a, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, mk, mv, a, splits);
+    return cudaLaunchKernelEx(&cfg, kern, maps, a, (int)tiles, splits);
 }
 
 cudaError_t launch_paged_prompts(const PagedAttnArgs& a, cudaStream_t s) {
