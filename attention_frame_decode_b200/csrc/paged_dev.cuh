@@ -69,6 +69,22 @@ VC_DEV uint32_t finite2(uint32_t u) {
     return ((u & m) == m ? 0u : u & 0xffffu) | (((u >> 16) & m) == m ? 0u : u & 0xffff0000u);
 }
 
+// A wait for an mbarrier's phase of at most `limit` polls, without a branch that the compiler sees; 1: it came.  A poll
+// sleeps until the phase completes or up to 10 us: a waiting warp leaves the issue slots to the others.
+static constexpr uint32_t kPollLimit = 1u << 18;
+VC_DEV uint32_t mbar_poll(uint64_t* bar, uint32_t parity, uint32_t limit) {
+    uint32_t done;
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .u32 i;\n mov.u32 i, %3;\n mov.u32 %0, 0;\n"
+        "again:\n setp.eq.u32 p, i, 0;\n @p bra over;\n sub.u32 i, i, 1;\n"
+        " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 10000;\n @!p bra again;\n mov.u32 %0, 1;\n"
+        "over:\n}\n"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(limit)
+        : "memory");
+    return done;
+}
+
 VC_DEV void tma_prefetch_map(const void* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }

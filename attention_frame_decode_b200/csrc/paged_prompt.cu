@@ -36,19 +36,6 @@ struct PromptShape {
     static constexpr uint32_t S0 = 0, O0 = 256, P0 = P_APART ? 384 : 0, P_STEP = P_APART ? 64 : 128;
 };
 
-// a wait for an mbarrier's phase of at most `limit` polls, without a branch that the compiler sees; 1: it came
-VC_DEV uint32_t mbar_poll(uint64_t* bar, uint32_t parity, uint32_t limit) {
-    uint32_t done;
-    asm volatile(
-        "{\n .reg .pred p;\n .reg .u32 i;\n mov.u32 i, %3;\n mov.u32 %0, 0;\n"
-        "again:\n setp.eq.u32 p, i, 0;\n @p bra over;\n sub.u32 i, i, 1;\n"
-        " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @!p bra again;\n mov.u32 %0, 1;\n"
-        "over:\n}\n"
-        : "=r"(done)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(limit)
-        : "memory");
-    return done;
-}
 // one lane of a converged warp.  What that lane alone does needs no proof that its operands are the same in all
 // lanes: the products' descriptors go to uniform registers without a loop over the lanes.
 VC_DEV bool elect_one() {
@@ -235,7 +222,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
         }
     bool ok = true;   // false after a wait that gave up: no other waits any more, and what is computed is not used
     auto wait = [&](uint64_t* bar, int phase) {
-        ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, (uint32_t)(phase & 1), a.c.status));
+        if (!ok) return;
+        ok = __all_sync(0xffffffffu, mbar_poll(bar, (uint32_t)(phase & 1), kPollLimit) != 0);
+        if (!ok && lane == 0) atomicOr(a.c.status, VC_DEV_TIMEOUT);
     };
     // Every role goes through the CTA's pieces in turn (t counts them, g the key blocks since the launch) and is held
     // up by barriers alone: the copies, the rows of Q and the first scores of a piece come while the one before ends.
@@ -312,7 +301,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             tc_commit(&o_done[i]);
         };
         auto hold = [&](uint64_t* bar, int phase) {   // as wait(), with control flow that is the same in all lanes
-            fine &= mbar_poll(bar, (uint32_t)(phase & 1), fine ? (uint32_t)kWaitLimit : 1u);
+            fine &= mbar_poll(bar, (uint32_t)(phase & 1), fine ? kPollLimit : 1u);
             __syncwarp();
         };
         auto slot = [](int k) { return k & (ST - 1); };
