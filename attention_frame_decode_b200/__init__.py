@@ -118,6 +118,9 @@ _lib.vc_paged_resize.argtypes = [C.POINTER(VcPagedKv), _i, _p, _p, _i, _p, _p]
 _lib.vc_paged_fork.argtypes = [C.POINTER(VcPagedKv), _i, _p, _p, C.POINTER(VcSessionPart), _i, _p, _p]
 _lib.vc_paged_compact.argtypes = [C.POINTER(VcPagedKv), _p, _p]
 _lib.vc_paged_attend.argtypes = [C.POINTER(VcPagedKv), _i, C.POINTER(VcAttnRows), _p]
+_lib.vc_step_paged.argtypes = [_p, _p, C.POINTER(VcTokenEmbeddings), _i, _p, C.POINTER(VcState), C.POINTER(VcPagedKv),
+                               _p, _p, _p]
+_lib.vc_prefill_paged.argtypes = [_p, _p, _i, _i, C.POINTER(VcState), C.POINTER(VcPagedKv), _p]
 _lib.vc_destroy.argtypes = [_p]
 _lib.vc_destroy.restype = None
 _lib.vc_status_string.argtypes = [_i]
@@ -129,7 +132,7 @@ for _f in ("vc_quantize_weight", "vc_pack_bf16_weight", "vc_pack_weight", "vc_de
            "vc_debug_set_prefill_taps", "vc_debug_set_zx_taps", "vc_debug_mamba_step",
            "vc_debug_gemv", "vc_debug_gemm", "vc_debug_mamba_prefill", "vc_debug_gemv_noalloc",
            "vc_gemv_noalloc_status", "vc_gemv_noalloc_reset", "vc_paged_resize", "vc_paged_fork", "vc_paged_compact",
-           "vc_paged_attend"):
+           "vc_paged_attend", "vc_step_paged", "vc_prefill_paged"):
     getattr(_lib, _f).restype = _i
 
 EXPORTS = ("vc_weight_bytes", "vc_quantize_weight", "vc_pack_bf16_weight", "vc_pack_weight", "vc_debug_dequant",
@@ -140,7 +143,8 @@ EXPORTS = ("vc_weight_bytes", "vc_quantize_weight", "vc_pack_bf16_weight", "vc_p
            "vc_debug_gemv", "vc_debug_gemm", "vc_gemv_noalloc_scratch_bytes", "vc_debug_gemv_noalloc",
            "vc_gemv_noalloc_status", "vc_gemv_noalloc_reset",
            "vc_debug_mamba_prefill_scratch_bytes", "vc_debug_mamba_prefill", "vc_paged_workspace_bytes",
-           "vc_paged_resize", "vc_paged_fork", "vc_paged_compact", "vc_paged_attend", "vc_destroy",
+           "vc_paged_resize", "vc_paged_fork", "vc_paged_compact", "vc_paged_attend", "vc_step_paged",
+           "vc_prefill_paged", "vc_destroy",
            "vc_status_string", "vc_last_cuda_error")
 
 
@@ -404,6 +408,34 @@ class Backbone:
     def prefill(self, x, slot: int, state: State, stream=None):
         T = x.shape[0]
         _check(_lib.vc_prefill(self.h, _ptr(x), T, slot, C.byref(state.c), _stream(stream)), "vc_prefill")
+
+    def _paged(self, cache):
+        if cache.device != self.workspace.device:
+            raise ValueError(f"a cache on {cache.device}; the backbone is on {self.workspace.device}")
+        return C.byref(cache.c)
+
+    def step_paged(self, x, state: State, cache: PagedCache, tok_text, tok_func, slots=None, emb=None, stream=None):
+        """one frame with the attention layers' keys and values in a paged cache (see vc_step_paged); emb: (emb_text,
+        emb_func) to fuse the previous tokens in, as step_fused does"""
+        B = x.shape[0]
+        e = None if emb is None else VcTokenEmbeddings(_ptr(emb[0]), _ptr(emb[1]))
+        self._emb = emb
+        _check(_lib.vc_step_paged(self.h, _ptr(x), None if e is None else C.byref(e), B, _ptr(slots), C.byref(state.c),
+                                  self._paged(cache), _ptr(tok_text), _ptr(tok_func), _stream(stream)), "vc_step_paged")
+
+    def prefill_paged(self, x, slot: int, state: State, cache: PagedCache, stream=None):
+        """prefill into a session of a paged cache (see vc_prefill_paged)"""
+        _check(_lib.vc_prefill_paged(self.h, _ptr(x), x.shape[0], slot, C.byref(state.c), self._paged(cache),
+                                     _stream(stream)), "vc_prefill_paged")
+
+    def new_cache(self, pages: int, page_size: int, columns: int, window: int = 0, sinks: int = 0,
+                  status=None) -> PagedCache:
+        """an empty paged cache of this backbone's attention layers and sessions"""
+        c = self.c
+        return PagedCache.empty(layers=self.cfg.pattern.count("*"), pages=pages, page_size=page_size,
+                                kv_heads=c.attn_kv_heads, head_dim=c.attn_head_dim, seqs=self.n_slots, columns=columns,
+                                q_heads=c.attn_q_heads, window=window, sinks=sinks, device=self.workspace.device,
+                                status=status)
 
     def close(self):
         if getattr(self, "h", None):

@@ -1,6 +1,8 @@
 // api.cu -- the C ABI of libvc (include/vc.h): weight preparation, backbone handle, the
 // per-frame step as one CUDA graph of ~145 kernels chained with programmatic dependent launch.
 #include <cuda_runtime.h>
+#include <limits.h>
+#include <stddef.h>
 #include <stdio.h>
 #include <string.h>
 
@@ -19,6 +21,7 @@
 #include "gemv.cuh"
 #include "gemv_core.cuh"
 #include "layout.cuh"
+#include "paged.cuh"
 #include "prefill.cuh"
 
 using namespace vc;
@@ -114,6 +117,8 @@ struct Workspace {
     size_t prefill_bytes;
     FrameProgram* prog;  // the frame kernel's program (device copy)
     int* fk_sync;        // [0] barrier arrivals, [1] abort flag of the frame kernel
+    uint16_t* qkv;       // a step's queries, keys and values for a paged cache
+    int *pos, *pf_pos;   // positions that a paged cache granted: a step's rows; a prefill (kPagedPrefillInts)
 };
 
 struct GraphKey {
@@ -127,6 +132,8 @@ struct GraphKey {
     const float* tz;
     const void* et;   // token embeddings of the fused-input variant (null: plain inputs)
     const void* ef;
+    PagedKv kv;       // the paged cache and its workspace (zero: the state's own rows)
+    const void* kv_ws;
     bool operator<(const GraphKey& o) const {
         return memcmp(this, &o, sizeof(GraphKey)) < 0;
     }
@@ -244,6 +251,8 @@ extern "C" size_t vc_workspace_bytes(const vc_config* cfg) {
     add(accum_floats(cfg, D) * 4);            // split-unit accumulators
     add(sizeof(FrameProgram));                // the frame kernel's program
     add(256);                                 // its barrier and abort words
+    add((size_t)B * D.qkv_rows * 2 + 16);     // a paged step's queries, keys and values
+    add((16 + kPagedPrefillInts) * 4);        // positions of a paged cache
     return align_up(total, 256);
 }
 
@@ -285,6 +294,9 @@ static void carve(vc_backbone* h, uint8_t* base) {
     W.accum = (float*)take(accum_floats(&h->cfg, D) * 4);
     W.prog = (FrameProgram*)take(sizeof(FrameProgram));
     W.fk_sync = (int*)take(256);
+    W.qkv = (uint16_t*)take((size_t)B * D.qkv_rows * 2 + 16);
+    W.pos = (int*)take((16 + kPagedPrefillInts) * 4);
+    W.pf_pos = W.pos + 16;
 }
 
 static bool qmat_ok(const vc_qmat& m, int fmt, int group, int N, int K) {
@@ -407,6 +419,7 @@ struct StepSink {
     virtual cudaError_t gemv(const GemvLaunch& l, const GemvArgs& a) = 0;
     virtual cudaError_t mamba(const MambaStepArgs& a) = 0;
     virtual cudaError_t attn(const AttnArgs& a) = 0;
+    virtual cudaError_t paged_attn(const vc_paged_kv& kv, int layer, const PagedAttnArgs& a) = 0;
     virtual ~StepSink() = default;
 };
 
@@ -418,6 +431,9 @@ struct LaunchSink : StepSink {
     cudaError_t gemv(const GemvLaunch& l, const GemvArgs& a) override { return launch_gemv(l, a, s); }
     cudaError_t mamba(const MambaStepArgs& a) override { return launch_mamba_step(a, pdl, s); }
     cudaError_t attn(const AttnArgs& a) override { return launch_attn_decode(a, pdl, s); }
+    cudaError_t paged_attn(const vc_paged_kv& kv, int layer, const PagedAttnArgs& a) override {
+        return paged_attend(kv, layer, a, s);
+    }
 };
 
 struct ProgramSink : StepSink {
@@ -461,11 +477,14 @@ struct ProgramSink : StepSink {
         P.n_attn++;
         return e;
     }
+    cudaError_t paged_attn(const vc_paged_kv&, int, const PagedAttnArgs&) override { return cudaErrorNotSupported; }
 };
 
-// the step's sequence of operations
+// the step's sequence of operations; kv: the paged cache that holds the keys and values, granted the frame's positions
+// (W.pos) by a resize before; null: the state's own rows
 static cudaError_t record_step(vc_backbone* h, const void* x, int B, const int32_t* slots, const vc_state* st,
-                               int32_t* tt, int32_t* tf, const vc_token_embeddings* emb, StepSink& sink) {
+                               int32_t* tt, int32_t* tf, const vc_token_embeddings* emb, const vc_paged_kv* kv,
+                               StepSink& sink) {
     const Dims& D = h->D;
     const Workspace& W = h->ws;
     const int fmt = h->cfg.wfmt, grp = h->cfg.group_size;
@@ -479,7 +498,7 @@ static cudaError_t record_step(vc_backbone* h, const void* x, int B, const int32
     ia.x = (const uint16_t*)x; ia.B = B; ia.d = D.d; ia.unit_rows = unit_rows; ia.n_units = n_units_d;
     ia.r = W.r; ia.gamma = h->layers[0].norm; ia.act = W.act_a; ia.act_ld = W.lda; ia.act_f16 = act_f16;
     ia.parts = W.parts_r; ia.tap = h->tap_hidden; ia.ctx_len = st->ctx_len; ia.slots = slots; ia.cap = D.cap;
-    ia.ok = W.ok; ia.status = st->status;
+    ia.ok = W.ok; ia.status = st->status; ia.pos = kv ? W.pos : nullptr;
     if (emb) {
         ia.emb_t = (const uint16_t*)emb->emb_text; ia.emb_f = (const uint16_t*)emb->emb_func;
         ia.tok_t = tt; ia.tok_f = tf; ia.Vt = D.Vt; ia.Vf = D.Vf;
@@ -541,20 +560,29 @@ static cudaError_t record_step(vc_backbone* h, const void* x, int B, const int32
         } else if (kind == '*') {
             GemvArgs a = base;
             a.mat[0] = gm(Lw.qkv); a.act = W.act_a; a.act_ld = W.lda; a.insc = pre;
-            a.q_out = W.q; a.q_ld = D.Hq * D.Dh;
-            const size_t kvl = (size_t)ai * D.slots * D.Hk * D.cap * D.Dh;
-            a.kcache = (uint16_t*)st->k + kvl; a.vcache = (uint16_t*)st->v + kvl;
-            a.Hq = D.Hq; a.Hk = D.Hk; a.Dh = D.Dh; a.cap = D.cap;
-            gl.epi = EPI_QKV;
-            if ((e = sink.gemv(gl, a)) != cudaSuccess) return e;
+            if (kv) {
+                a.out = W.qkv; a.out_ld = D.qkv_rows; a.out_f16 = 0;
+                gl.epi = EPI_STORE;
+                if ((e = sink.gemv(gl, a)) != cudaSuccess) return e;
+                PagedAttnArgs pa = paged_rows(W.qkv, D.qkv_rows, D.Hq, D.Hk, D.Dh, W.act_o, W.ldo, act_f16);
+                pa.seqs = slots; pa.pos = W.pos; pa.batch = pa.rows = B;
+                if ((e = sink.paged_attn(*kv, ai, pa)) != cudaSuccess) return e;
+            } else {
+                a.q_out = W.q; a.q_ld = D.Hq * D.Dh;
+                const size_t kvl = (size_t)ai * D.slots * D.Hk * D.cap * D.Dh;
+                a.kcache = (uint16_t*)st->k + kvl; a.vcache = (uint16_t*)st->v + kvl;
+                a.Hq = D.Hq; a.Hk = D.Hk; a.Dh = D.Dh; a.cap = D.cap;
+                gl.epi = EPI_QKV;
+                if ((e = sink.gemv(gl, a)) != cudaSuccess) return e;
 
-            AttnArgs aa{};
-            aa.q = W.q; aa.q_ld = D.Hq * D.Dh; aa.kcache = a.kcache; aa.vcache = a.vcache;
-            aa.Hq = D.Hq; aa.Hk = D.Hk; aa.Dh = D.Dh; aa.cap = D.cap; aa.max_splits = (D.cap + kAttnSplit - 1) / kAttnSplit;
-            aa.ctx_len = st->ctx_len; aa.slots = slots; aa.ok = W.ok; aa.scratch = W.attn_scratch;
-            aa.counters = W.attn_counters; aa.act = W.act_o; aa.act_ld = W.ldo; aa.act_f16 = act_f16; aa.B = B;
-            aa.status = st->status;
-            if ((e = sink.attn(aa)) != cudaSuccess) return e;
+                AttnArgs aa{};
+                aa.q = W.q; aa.q_ld = D.Hq * D.Dh; aa.kcache = a.kcache; aa.vcache = a.vcache;
+                aa.Hq = D.Hq; aa.Hk = D.Hk; aa.Dh = D.Dh; aa.cap = D.cap; aa.max_splits = (D.cap + kAttnSplit - 1) / kAttnSplit;
+                aa.ctx_len = st->ctx_len; aa.slots = slots; aa.ok = W.ok; aa.scratch = W.attn_scratch;
+                aa.counters = W.attn_counters; aa.act = W.act_o; aa.act_ld = W.ldo; aa.act_f16 = act_f16; aa.B = B;
+                aa.status = st->status;
+                if ((e = sink.attn(aa)) != cudaSuccess) return e;
+            }
 
             a = base;
             a.mat[0] = gm(Lw.o); a.act = W.act_o; a.act_ld = W.ldo;
@@ -590,12 +618,12 @@ static cudaError_t record_step(vc_backbone* h, const void* x, int B, const int32
 }
 
 static vc_status check_step_args(vc_backbone* h, const void* x, int B, const vc_state* st, const void* tt,
-                                 const void* tf) {
+                                 const void* tf, bool rows = true) {
     if (!h || !x || !st || !tt || !tf) return VC_ERR_INVALID_ARG;
     if (B < 1 || B > h->D.B) return VC_ERR_INVALID_ARG;
     if (!st->ctx_len || !st->status) return VC_ERR_INVALID_ARG;
     if (h->D.nm && (!st->ssm || !st->conv || !aligned16(st->ssm) || !aligned16(st->conv))) return VC_ERR_INVALID_ARG;
-    if (h->D.na && (!st->k || !st->v || !aligned16(st->k) || !aligned16(st->v))) return VC_ERR_INVALID_ARG;
+    if (rows && h->D.na && (!st->k || !st->v || !aligned16(st->k) || !aligned16(st->v))) return VC_ERR_INVALID_ARG;
     return VC_OK;
 }
 
@@ -629,7 +657,7 @@ static cudaError_t run_frame(vc_backbone* h, const void* x, int B, const int32_t
         if (!h->host_prog) h->host_prog.reset(new FrameProgram());
         ProgramSink ps(*h->host_prog, h->D.cap);
         // the frame input and the token buffers are the launch's (FrameParams), not the program's
-        if ((e = record_step(h, x, B, slots, st, tt, tf, emb, ps)) != cudaSuccess) return e;
+        if ((e = record_step(h, x, B, slots, st, tt, tf, emb, nullptr, ps)) != cudaSuccess) return e;
         if ((e = cudaMemcpyAsync(h->ws.prog, h->host_prog.get(), sizeof(FrameProgram), cudaMemcpyHostToDevice, s)))
             return e;
         h->prog_key = key;
@@ -649,15 +677,22 @@ static cudaError_t run_frame(vc_backbone* h, const void* x, int B, const int32_t
 }
 
 static vc_status run_step(vc_backbone* h, const void* x, int B, const int32_t* slots, const vc_state* st, int32_t* tt,
-                          int32_t* tf, cudaStream_t s, const vc_token_embeddings* emb = nullptr) {
-    if (h->use_frame) {
+                          int32_t* tf, cudaStream_t s, const vc_token_embeddings* emb = nullptr,
+                          const vc_paged_kv* kv = nullptr) {
+    if (kv) {
+        // the frame's positions, outside the graph: the page calls' kernels are not among its nodes
+        const cudaError_t e = launch_paged_resize(paged_kernel_kv(*kv), paged_carve(*kv, kv->workspace), B, slots, nullptr,
+                                                  1, h->ws.pos, s);
+        if (e != cudaSuccess) return cuda_fail(e, "vc_step_paged resize");
+    }
+    if (h->use_frame && !kv) {
         const cudaError_t e = run_frame(h, x, B, slots, st, tt, tf, s, emb);
         if (e == cudaSuccess) return VC_OK;
         if (e != cudaErrorNotSupported) return cuda_fail(e, "vc_step frame kernel");
     }
     if (!h->use_graph) {
         LaunchSink ls(s, h->use_pdl);
-        cudaError_t e = record_step(h, x, B, slots, st, tt, tf, emb, ls);
+        cudaError_t e = record_step(h, x, B, slots, st, tt, tf, emb, kv, ls);
         return e == cudaSuccess ? VC_OK : cuda_fail(e, "vc_step launch");
     }
     GraphKey key;
@@ -665,13 +700,18 @@ static vc_status run_step(vc_backbone* h, const void* x, int B, const int32_t* s
     key.B = B; key.slots = slots; key.st = *st; key.tt = tt; key.tf = tf;
     key.th = h->tap_hidden; key.tl = h->tap_logits; key.tz = h->tap_zx;
     if (emb) { key.et = emb->emb_text; key.ef = emb->emb_func; }
+    if (kv) {   // without the struct's padding
+        const PagedKv c = paged_kernel_kv(*kv);
+        memcpy(&key.kv, &c, offsetof(PagedKv, sinks) + sizeof(c.sinks));
+        key.kv_ws = kv->workspace;
+    }
     auto it = h->graphs.find(key);
     if (it == h->graphs.end()) {
         if (h->graphs.size() > 64) clear_graphs(h);
         cudaStream_t cs = h->capture_stream;
         CK(cudaStreamBeginCapture(cs, cudaStreamCaptureModeThreadLocal));
         LaunchSink ls(cs, h->use_pdl);
-        cudaError_t e = record_step(h, x, B, slots, st, tt, tf, emb, ls);
+        cudaError_t e = record_step(h, x, B, slots, st, tt, tf, emb, kv, ls);
         cudaGraph_t g = nullptr;
         cudaError_t e2 = cudaStreamEndCapture(cs, &g);
         if (e != cudaSuccess) {
@@ -749,8 +789,23 @@ extern "C" vc_status vc_step_host(vc_backbone* h, const void* x_host, int B, con
     return VC_OK;
 }
 
-extern "C" vc_status vc_prefill(vc_backbone* h, const void* x, int T, int slot, const vc_state* state,
-                                vc_stream_t stream) {
+// a paged cache of this backbone's attention layers and sessions
+static bool kv_fits(const vc_backbone* h, const vc_paged_kv* kv) {
+    return paged_kv_ok(kv) && kv->layers == h->D.na && kv->kv_heads == h->D.Hk && kv->q_heads == h->D.Hq &&
+           kv->head_dim == h->D.Dh && !kv->f16 && kv->seqs == h->D.slots;
+}
+
+extern "C" vc_status vc_step_paged(vc_backbone* h, const void* x, const vc_token_embeddings* emb, int B,
+                                   const int32_t* slots, const vc_state* state, const vc_paged_kv* kv,
+                                   int32_t* tok_text, int32_t* tok_func, vc_stream_t stream) {
+    vc_status st = check_step_args(h, x, B, state, tok_text, tok_func, false);
+    if (st != VC_OK) return st;
+    if (!aligned16(x) || !kv_fits(h, kv) || (emb && (!emb->emb_text || !emb->emb_func))) return VC_ERR_INVALID_ARG;
+    return run_step(h, x, B, slots, state, tok_text, tok_func, (cudaStream_t)stream, emb, kv);
+}
+
+static vc_status prefill(vc_backbone* h, const void* x, int T, int slot, const vc_state* state, const vc_paged_kv* kv,
+                         vc_stream_t stream) {
     if (!h || !x || !state || !aligned16(x)) return VC_ERR_INVALID_ARG;
     if (T < 1 || slot < 0 || slot >= h->D.slots) return VC_ERR_INVALID_ARG;
     if (T > h->D.cap) return VC_ERR_CAPACITY;
@@ -769,10 +824,26 @@ extern "C" vc_status vc_prefill(vc_backbone* h, const void* x, int T, int slot, 
     c.tap_zx = h->tap_prefill_zx;
     c.side = h->prefill_side;
     for (int i = 0; i < 5; ++i) c.ev[i] = h->pf_ev[i];
+    c.kv = kv;
+    c.kv_pos = h->ws.pf_pos;
     cudaError_t e = run_prefill(c, (const uint16_t*)x, T, slot, (cudaStream_t)stream);
     if (e == cudaErrorNotSupported) return VC_ERR_UNSUPPORTED;
     if (e == cudaErrorInvalidValue) return VC_ERR_INVALID_ARG;
     return e == cudaSuccess ? VC_OK : cuda_fail(e, "vc_prefill");
+}
+
+extern "C" vc_status vc_prefill(vc_backbone* h, const void* x, int T, int slot, const vc_state* state,
+                                vc_stream_t stream) {
+    return prefill(h, x, T, slot, state, nullptr, stream);
+}
+
+extern "C" vc_status vc_prefill_paged(vc_backbone* h, const void* x, int T, int slot, const vc_state* state,
+                                      const vc_paged_kv* kv, vc_stream_t stream) {
+    if (!h || !state || !kv_fits(h, kv)) return VC_ERR_INVALID_ARG;
+    if (h->D.nm && (!state->ssm || !state->conv || !aligned16(state->ssm) || !aligned16(state->conv)))
+        return VC_ERR_INVALID_ARG;
+    if (T > (int64_t)kv->columns * kv->page_size) return VC_ERR_CAPACITY;
+    return prefill(h, x, T, slot, state, kv, stream);
 }
 
 extern "C" vc_status vc_debug_mamba_step(const vc_config* cfg, const vc_layer_weights* layer, const void* zx, int B,

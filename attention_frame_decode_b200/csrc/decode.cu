@@ -25,9 +25,9 @@ __global__ void input_kernel(const InputArgs a) {
     const int b = blockIdx.x;
     const int slot = a.slots ? a.slots[b] : b;
     if (threadIdx.x == 0) {
-        const int okb = a.ctx_len[slot] < a.cap;
+        const int okb = a.pos ? a.pos[b] >= 0 : a.ctx_len[slot] < a.cap;
         a.ok[b] = okb;
-        if (!okb) atomicOr(a.status, VC_DEV_CAPACITY);
+        if (!okb && !a.pos) atomicOr(a.status, VC_DEV_CAPACITY);   // the paged cache's call has set its reason
     }
     const uint16_t* et = nullptr;
     const uint16_t* ef = nullptr;

@@ -25,6 +25,7 @@ struct InputArgs {
     const int* ctx_len;
     const int* slots;
     int cap;
+    const int* pos;         // with a paged cache: [B] the frame's position, < 0: no room (ctx_len and cap are not looked at)
     int* ok;                // [B]
     int* status;
 };

@@ -39,6 +39,9 @@ static constexpr int kTileRows = 128;                  // rows of the largest at
 // the workspace's parts, in order; false where the sizes are outside the documented limits
 bool paged_sizes_ok(const vc_paged_kv& c);
 PagedWorkspace paged_carve(const vc_paged_kv& c, void* base);
+// sizes, pointers and workspace as documented
+bool paged_kv_ok(const vc_paged_kv* c);
+PagedKv paged_kernel_kv(const vc_paged_kv& c);
 
 struct PagedAttnArgs {
     PagedKv c;                   // k, v: this layer's
@@ -47,11 +50,19 @@ struct PagedAttnArgs {
     long long q_ld, k_ld, v_ld, out_ld;
     const int *seqs, *pos, *cu_rows;
     int batch, rows, f16, num_sms;
+    int widen;                   // store bf16 results in fp16's format (the input of a quantized projection)
     float scale_log2;            // scale * log2(e)
     int* merge;
     int* ticket;                 // counts the pieces handed out (zero between calls)
     float* partial;
 };
+
+// appends and attends for one layer: the form by the rows' kind (one per session, or prompts) and the shape.  The
+// caller fills in the rows and the scale, this call the cache, its workspace and the device.
+cudaError_t paged_attend(const vc_paged_kv& kv, int layer, PagedAttnArgs a, cudaStream_t s);
+
+// rows of a fused projection [q | k | v] of ld elements a row, 1 / sqrt(Dh), results of out_ld elements a row
+PagedAttnArgs paged_rows(const uint16_t* qkv, int ld, int Hq, int Hk, int Dh, uint16_t* out, int out_ld, int widen);
 
 cudaError_t launch_paged_append(const PagedAttnArgs& a, cudaStream_t s);
 cudaError_t launch_paged_tiles(const PagedAttnArgs& a, cudaStream_t s);

@@ -49,7 +49,7 @@ PagedWorkspace paged_carve(const vc_paged_kv& c, void* base) {
     return w;
 }
 
-static PagedKv kernel_kv(const vc_paged_kv& c) {
+PagedKv paged_kernel_kv(const vc_paged_kv& c) {
     PagedKv d{};
     d.k = (uint16_t*)c.k; d.v = (uint16_t*)c.v;
     d.table = c.table; d.len = c.len; d.refs = c.refs; d.status = c.status;
@@ -59,10 +59,49 @@ static PagedKv kernel_kv(const vc_paged_kv& c) {
     return d;
 }
 
-static bool kv_ok(const vc_paged_kv* c) {
+bool paged_kv_ok(const vc_paged_kv* c) {
     return c && paged_sizes_ok(*c) && c->k && c->v && c->table && c->len && c->refs && c->status && c->workspace &&
            aligned16(c->k) && aligned16(c->v) && aligned16(c->table) && aligned16(c->len) && aligned16(c->refs) &&
            aligned4(c->status) && aligned16(c->workspace) && c->workspace_bytes >= paged_carve(*c, nullptr).bytes;
+}
+
+static float scale_to_log2(float scale, int head_dim) {
+    return (scale != 0.0f ? scale : 1.0f / sqrtf((float)head_dim)) * 1.4426950408889634f;
+}
+
+PagedAttnArgs paged_rows(const uint16_t* qkv, int ld, int Hq, int Hk, int Dh, uint16_t* out, int out_ld, int widen) {
+    PagedAttnArgs a{};
+    a.q = qkv; a.kn = qkv + (size_t)Hq * Dh; a.vn = a.kn + (size_t)Hk * Dh; a.out = out;
+    a.q_ld = a.k_ld = a.v_ld = ld; a.out_ld = out_ld;
+    a.scale_log2 = scale_to_log2(0.0f, Dh);
+    a.widen = widen;
+    return a;
+}
+
+cudaError_t paged_attend(const vc_paged_kv& kv, int layer, PagedAttnArgs a, cudaStream_t s) {
+    a.c = paged_kernel_kv(kv);
+    const size_t lay = (size_t)layer * kv.pages * kv.kv_heads * kv.page_size * kv.head_dim;
+    a.c.k += lay; a.c.v += lay;
+    a.f16 = kv.f16 != 0;
+    const PagedWorkspace w = paged_carve(kv, kv.workspace);
+    a.merge = w.merge;
+    a.ticket = w.ticket;
+    a.partial = w.partial;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&a.num_sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    if (a.num_sms > kMaxSms) a.num_sms = kMaxSms;
+    if (!a.cu_rows) {
+        e = launch_paged_frames(a, s);
+        if (e != cudaErrorNotSupported) return e;
+    }
+    if (a.kn && (e = launch_paged_append(a, s)) != cudaSuccess) return e;
+    if (a.cu_rows) {
+        e = launch_paged_prompts(a, s);
+        if (e != cudaErrorNotSupported) return e;
+    }
+    return launch_paged_tiles(a, s);
 }
 
 }  // namespace vc
@@ -82,16 +121,16 @@ extern "C" size_t vc_paged_workspace_bytes(const vc_paged_kv* kv) {
 
 extern "C" vc_status vc_paged_resize(const vc_paged_kv* kv, int n, const int32_t* seqs, const int32_t* lens, int add,
                                      int32_t* pos, vc_stream_t stream) {
-    if (!kv_ok(kv) || n < 1 || n > kv->seqs || !aligned4(seqs) || !aligned4(lens) || !aligned4(pos))
+    if (!paged_kv_ok(kv) || n < 1 || n > kv->seqs || !aligned4(seqs) || !aligned4(lens) || !aligned4(pos))
         return VC_ERR_INVALID_ARG;
-    CKP(launch_paged_resize(kernel_kv(*kv), paged_carve(*kv, kv->workspace), n, seqs, lens, add, pos,
+    CKP(launch_paged_resize(paged_kernel_kv(*kv), paged_carve(*kv, kv->workspace), n, seqs, lens, add, pos,
                             (cudaStream_t)stream));
     return VC_OK;
 }
 
 extern "C" vc_status vc_paged_fork(const vc_paged_kv* kv, int n, const int32_t* src, const int32_t* dst,
                                    const vc_session_part* parts, int n_parts, int32_t* done, vc_stream_t stream) {
-    if (!kv_ok(kv) || n < 1 || n > kv->seqs || !src || !dst || !aligned4(src) || !aligned4(dst) || !aligned4(done))
+    if (!paged_kv_ok(kv) || n < 1 || n > kv->seqs || !src || !dst || !aligned4(src) || !aligned4(dst) || !aligned4(done))
         return VC_ERR_INVALID_ARG;
     if (n_parts < 0 || n_parts > 8 || (n_parts && !parts)) return VC_ERR_INVALID_ARG;
     for (int i = 0; i < n_parts; ++i) {
@@ -101,19 +140,19 @@ extern "C" vc_status vc_paged_fork(const vc_paged_kv* kv, int n, const int32_t* 
         // a session's block of one outer index may not reach into the next one's
         if (p.outer > 1 && p.outer_stride < (int64_t)(kv->seqs - 1) * p.stride + p.bytes) return VC_ERR_INVALID_ARG;
     }
-    CKP(launch_paged_fork(kernel_kv(*kv), paged_carve(*kv, kv->workspace), n, src, dst, parts, n_parts, done,
+    CKP(launch_paged_fork(paged_kernel_kv(*kv), paged_carve(*kv, kv->workspace), n, src, dst, parts, n_parts, done,
                           (cudaStream_t)stream));
     return VC_OK;
 }
 
 extern "C" vc_status vc_paged_compact(const vc_paged_kv* kv, int32_t* live, vc_stream_t stream) {
-    if (!kv_ok(kv) || !aligned4(live)) return VC_ERR_INVALID_ARG;
-    CKP(launch_paged_compact(kernel_kv(*kv), paged_carve(*kv, kv->workspace), live, (cudaStream_t)stream));
+    if (!paged_kv_ok(kv) || !aligned4(live)) return VC_ERR_INVALID_ARG;
+    CKP(launch_paged_compact(paged_kernel_kv(*kv), paged_carve(*kv, kv->workspace), live, (cudaStream_t)stream));
     return VC_OK;
 }
 
 extern "C" vc_status vc_paged_attend(const vc_paged_kv* kv, int layer, const vc_attn_rows* rows, vc_stream_t stream) {
-    if (!kv_ok(kv) || !rows || layer < 0 || layer >= kv->layers) return VC_ERR_INVALID_ARG;
+    if (!paged_kv_ok(kv) || !rows || layer < 0 || layer >= kv->layers) return VC_ERR_INVALID_ARG;
     const vc_attn_rows& r = *rows;
     if (!r.q || !r.out || !r.pos || (!r.k != !r.v) || r.batch < 1 || r.batch > kv->seqs || r.rows < 1 ||
         (!r.cu_rows && r.rows != r.batch))
@@ -128,35 +167,11 @@ extern "C" vc_status vc_paged_attend(const vc_paged_kv* kv, int layer, const vc_
     const int group = kv->q_heads / kv->kv_heads;
     if ((long long)r.rows * group > INT_MAX - 4096) return VC_ERR_INVALID_ARG;
     PagedAttnArgs a{};
-    a.c = kernel_kv(*kv);
-    const size_t lay = (size_t)layer * kv->pages * kv->kv_heads * kv->page_size * kv->head_dim;
-    a.c.k += lay; a.c.v += lay;
     a.q = (const uint16_t*)r.q; a.kn = (const uint16_t*)r.k; a.vn = (const uint16_t*)r.v; a.out = (uint16_t*)r.out;
     a.q_ld = r.q_stride; a.k_ld = r.k_stride; a.v_ld = r.v_stride; a.out_ld = r.out_stride;
     a.seqs = r.seqs; a.pos = r.pos; a.cu_rows = r.cu_rows;
-    a.batch = r.batch; a.rows = r.rows; a.f16 = kv->f16 != 0;
-    const float scale = r.scale != 0.0f ? r.scale : 1.0f / sqrtf((float)kv->head_dim);
-    a.scale_log2 = scale * 1.4426950408889634f;
-    const PagedWorkspace w = paged_carve(*kv, kv->workspace);
-    a.merge = w.merge;
-    a.ticket = w.ticket;
-    a.partial = w.partial;
-    int dev = 0;
-    CKP(cudaGetDevice(&dev));
-    CKP(cudaDeviceGetAttribute(&a.num_sms, cudaDevAttrMultiProcessorCount, dev));
-    if (a.num_sms > kMaxSms) a.num_sms = kMaxSms;
-    cudaStream_t s = (cudaStream_t)stream;
-    if (!a.cu_rows) {
-        const cudaError_t e = launch_paged_frames(a, s);
-        if (e == cudaSuccess) return VC_OK;
-        if (e != cudaErrorNotSupported) return record_cuda_failure(e, __func__);
-    }
-    if (a.kn) CKP(launch_paged_append(a, s));
-    if (a.cu_rows) {
-        const cudaError_t e = launch_paged_prompts(a, s);
-        if (e == cudaSuccess) return VC_OK;
-        if (e != cudaErrorNotSupported) return record_cuda_failure(e, __func__);
-    }
-    CKP(launch_paged_tiles(a, s));
+    a.batch = r.batch; a.rows = r.rows;
+    a.scale_log2 = scale_to_log2(r.scale, kv->head_dim);
+    CKP(paged_attend(*kv, layer, a, (cudaStream_t)stream));
     return VC_OK;
 }

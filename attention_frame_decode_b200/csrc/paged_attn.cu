@@ -240,7 +240,8 @@ __global__ void __launch_bounds__(kTThreads) paged_tile_kernel(const PagedAttnAr
             uint16_t* to = out_row(rr);
 #pragma unroll
             for (int n = 0; n < NT; ++n)
-                *reinterpret_cast<uint32_t*>(to + 8 * n + 2 * tq) = pack16<F16>(acc[n][2 * h] * inv, acc[n][2 * h + 1] * inv);
+                *reinterpret_cast<uint32_t*>(to + 8 * n + 2 * tq) =
+                    pack_out<F16>(a.widen, acc[n][2 * h] * inv, acc[n][2 * h + 1] * inv);
         }
         return;
     }
@@ -288,7 +289,7 @@ __global__ void __launch_bounds__(kTThreads) paged_tile_kernel(const PagedAttnAr
         }
         const float inv = w_sum == 0.0f ? 0.0f : 1.0f / w_sum;
         *reinterpret_cast<uint2*>(out_row(r0 + r) + d) =
-            make_uint2(pack16<F16>(v[0] * inv, v[1] * inv), pack16<F16>(v[2] * inv, v[3] * inv));
+            make_uint2(pack_out<F16>(a.widen, v[0] * inv, v[1] * inv), pack_out<F16>(a.widen, v[2] * inv, v[3] * inv));
     }
 }
 

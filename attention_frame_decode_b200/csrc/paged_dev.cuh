@@ -42,6 +42,13 @@ VC_DEV uint32_t pack16(float lo, float hi) {
         return *reinterpret_cast<const uint32_t*>(&v);
     }
 }
+// two results as they are stored: the cache's type, or (widen, a bf16 cache) bf16 values in fp16's format
+template <bool F16>
+VC_DEV uint32_t pack_out(int widen, float lo, float hi) {
+    const uint32_t v = pack16<F16>(lo, hi);
+    if (F16 || !widen) return v;
+    return pack16<true>(bf16_bits_to_f((uint16_t)v), bf16_bits_to_f((uint16_t)(v >> 16)));
+}
 template <bool F16>
 VC_DEV float unpack16(uint16_t u) {
     if constexpr (F16) return __half2float(*reinterpret_cast<const __half*>(&u));

@@ -454,7 +454,7 @@ __global__ void __launch_bounds__(FrameShape<DH>::THREADS, 1)
                     uint16_t* to = out_at(row, at0.j, r, g);
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt) {
-                        const uint32_t v = pack16<F16>(acc[mt][h][e] * inv, acc[mt][h][2 + e] * inv);
+                        const uint32_t v = pack_out<F16>(a.widen, acc[mt][h][e] * inv, acc[mt][h][2 + e] * inv);
                         to[16 * mt] = (uint16_t)v;
                         to[16 * mt + 8] = (uint16_t)(v >> 16);
                     }
@@ -511,7 +511,7 @@ __global__ void __launch_bounds__(FrameShape<DH>::THREADS, 1)
             if (!shared) {
                 const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
                 *reinterpret_cast<uint2*>(out_at(seg.z, seg.w, r, d)) =
-                    make_uint2(pack16<F16>(v[0] * inv, v[1] * inv), pack16<F16>(v[2] * inv, v[3] * inv));
+                    make_uint2(pack_out<F16>(a.widen, v[0] * inv, v[1] * inv), pack_out<F16>(a.widen, v[2] * inv, v[3] * inv));
             } else {
                 __stcg(reinterpret_cast<float4*>(rec + r * DH + d), make_float4(v[0], v[1], v[2], v[3]));
                 if (d == 0) __stcg(reinterpret_cast<float2*>(rec + G * DH + 2 * r), make_float2(top, sum));
@@ -577,7 +577,8 @@ __global__ void __launch_bounds__(FrameShape<DH>::THREADS, 1)
                 v[0] = fmaf(y.x, w, v[0]); v[1] = fmaf(y.y, w, v[1]);
                 v[2] = fmaf(y.z, w, v[2]); v[3] = fmaf(y.w, w, v[3]);
             }
-            *reinterpret_cast<uint2*>(out_at(seg.z, seg.w, r, d)) = make_uint2(pack16<F16>(v[0], v[1]), pack16<F16>(v[2], v[3]));
+            *reinterpret_cast<uint2*>(out_at(seg.z, seg.w, r, d)) =
+                make_uint2(pack_out<F16>(a.widen, v[0], v[1]), pack_out<F16>(a.widen, v[2], v[3]));
         }
         __syncthreads();   // the factors' room is used again
     }

@@ -604,8 +604,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
                     uint4 x[4];
 #pragma unroll
                     for (int u = 0; u < 4; ++u)
-                        x[u] = make_uint4(pack16<F16>(v[8 * u], v[8 * u + 1]), pack16<F16>(v[8 * u + 2], v[8 * u + 3]),
-                                          pack16<F16>(v[8 * u + 4], v[8 * u + 5]), pack16<F16>(v[8 * u + 6], v[8 * u + 7]));
+                        x[u] = make_uint4(pack_out<F16>(a.widen, v[8 * u], v[8 * u + 1]),
+                                          pack_out<F16>(a.widen, v[8 * u + 2], v[8 * u + 3]),
+                                          pack_out<F16>(a.widen, v[8 * u + 4], v[8 * u + 5]),
+                                          pack_out<F16>(a.widen, v[8 * u + 6], v[8 * u + 7]));
                     swap_lanes(x[0], x[1], 1, lane & 1);
                     swap_lanes(x[2], x[3], 1, lane & 1);
                     swap_lanes(x[0], x[2], 2, lane & 2);
@@ -664,7 +666,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
         }
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
         uint16_t* to = a.out + (size_t)(w.row0 + (w.r0 + r) / G) * a.out_ld + (size_t)(w.j * G + (w.r0 + r) % G) * DH + d;
-        *reinterpret_cast<uint2*>(to) = make_uint2(pack16<F16>(v[0] * inv, v[1] * inv), pack16<F16>(v[2] * inv, v[3] * inv));
+        *reinterpret_cast<uint2*>(to) =
+            make_uint2(pack_out<F16>(a.widen, v[0] * inv, v[1] * inv), pack_out<F16>(a.widen, v[2] * inv, v[3] * inv));
     }
 }
 

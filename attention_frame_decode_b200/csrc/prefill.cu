@@ -18,6 +18,8 @@
 // warp-level MMA (prefill_mma.cuh); the scan over chunks, conv, norms in fp32 on CUDA cores.
 // The call (re)initialises the slot: the SSM state ends as the scan's final state, the conv
 // ring holds the last W-1 frames, KV rows 0..T-1 are written and ctx_len[slot] = T.
+// With a paged cache the qkv GEMM leaves its rows as one projection [q | k | v], and the cache's
+// own call appends k and v to the slot's pages and attends (window and sinks included).
 #include <string.h>
 
 #include <algorithm>
@@ -26,6 +28,7 @@
 #include "common.cuh"
 #include "gemm_tc.cuh"
 #include "gemv.cuh"
+#include "paged.cuh"
 #include "prefill_mma.cuh"
 #include "prefill.cuh"
 
@@ -61,7 +64,7 @@ static PfBufs carve_pf(uint8_t* base, int T, int d, int E, int Cx, int H, int P,
     b.act_d = (uint16_t*)take((size_t)T * b.ld_d * 2);
     b.act_big = (uint16_t*)take((size_t)T * b.ld_big * 2);
     b.zx = (uint16_t*)take((size_t)T * std::max(zxw, 1) * 2);
-    b.q = (uint16_t*)take((size_t)T * std::max(Hq * Dh, 1) * 2);
+    b.q = (uint16_t*)take((size_t)T * std::max((Hq + 2 * Hk) * Dh, 1) * 2);   // with a paged cache k and v too
     b.xc = (float*)take((size_t)T * std::max(Cx, 1) * 4);
     b.dt = (float*)take((size_t)T * std::max(H, 1) * 4);
     b.lam = (float*)take((size_t)T * std::max(H, 1) * 4);
@@ -517,7 +520,26 @@ __global__ void __launch_bounds__(256) pf_attn_scalar_kernel(const uint16_t* q, 
     }
 }
 
-__global__ void pf_finish_kernel(int32_t* ctx_len, int slot, int T) { ctx_len[slot] = T; }
+// pos: null, or the paged cache's answer (< 0: it had no room)
+__global__ void pf_finish_kernel(int32_t* ctx_len, int slot, int T, const int* pos) {
+    ctx_len[slot] = pos && *pos < 0 ? 0 : T;
+}
+
+__global__ void pf_paged_args_kernel(int* w, int slot, int T) {
+    w[0] = slot; w[1] = 0; w[2] = T; w[3] = -1; w[4] = 0; w[5] = T;
+}
+
+// the slot gives its pages back and asks for those of T positions
+static cudaError_t pf_paged_begin(const PrefillCtx& c, int slot, int T, cudaStream_t s) {
+    int* w = c.kv_pos;
+    pf_paged_args_kernel<<<1, 1, 0, s>>>(w, slot, T);
+    cudaError_t e = cudaGetLastError();
+    const PagedKv kv = paged_kernel_kv(*c.kv);
+    const PagedWorkspace ws = paged_carve(*c.kv, c.kv->workspace);
+    if (e == cudaSuccess) e = launch_paged_resize(kv, ws, 1, w, w + 1, 0, nullptr, s);
+    if (e == cudaSuccess) e = launch_paged_resize(kv, ws, 1, w, w + 2, 0, w + 3, s);
+    return e;
+}
 
 // ------------------------------------------------------------------------------------------
 // Mamba-2 mixer over the frames (conv -> chunked SSD -> gated norm), shared by the prefill and
@@ -680,6 +702,7 @@ cudaError_t run_prefill(const PrefillCtx& c, const uint16_t* x, int T, int slot,
     const float eps = c.cfg->eps;
     cudaError_t e = gemm.start();
     if (e != cudaSuccess) return e;
+    if (c.kv && (e = pf_paged_begin(c, slot, T, s)) != cudaSuccess) return e;
     pf_rownorm_kernel<<<T, 256, 0, s>>>(x, b.r, c.layers[0].norm, b.act_d, b.ld_d, b.inv, d, eps, f16);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const size_t rbytes = (size_t)T * d * 4;
@@ -710,6 +733,15 @@ cudaError_t run_prefill(const PrefillCtx& c, const uint16_t* x, int T, int slot,
             if ((e = prefill_mixer(m, s))) return e;
             if ((e = gemm(GE_RESID, b.act_big, b.ld_big, T, Lw.out_proj, nullptr, nullptr, 0, b.r, d))) return e;
             mi++;
+        } else if (kind == '*' && c.kv) {
+            const int qkv = (c.Hq + 2 * c.Hk) * c.Dh;
+            if ((e = gemm(GE_ROWSCALE, b.act_d, b.ld_d, T, Lw.qkv, b.inv, b.q, qkv, nullptr, 0))) return e;
+            PagedAttnArgs pa = paged_rows(b.q, qkv, c.Hq, c.Hk, c.Dh, b.act_big, b.ld_big, f16);
+            pa.seqs = c.kv_pos; pa.pos = c.kv_pos + 3; pa.cu_rows = c.kv_pos + 4;
+            pa.batch = 1; pa.rows = T;
+            if ((e = paged_attend(*c.kv, ai, pa, s))) return e;
+            if ((e = gemm(GE_RESID, b.act_big, b.ld_big, T, Lw.o, nullptr, nullptr, 0, b.r, d))) return e;
+            ai++;
         } else if (kind == '*') {
             const size_t kvl = ((size_t)ai * c.n_slots + slot) * c.Hk * c.cap * c.Dh;
             GemmArgs qa{};
@@ -735,7 +767,7 @@ cudaError_t run_prefill(const PrefillCtx& c, const uint16_t* x, int T, int slot,
         if (c.tap && (e = cudaMemcpyAsync(c.tap + (size_t)(l + 1) * T * d, b.r, rbytes, cudaMemcpyDeviceToDevice, s)))
             return e;
     }
-    pf_finish_kernel<<<1, 1, 0, s>>>(c.ctx_len, slot, T);
+    pf_finish_kernel<<<1, 1, 0, s>>>(c.ctx_len, slot, T, c.kv ? c.kv_pos + 3 : nullptr);
     return cudaGetLastError();
 }
 

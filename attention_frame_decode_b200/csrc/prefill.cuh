@@ -23,7 +23,10 @@ struct PrefillCtx {
     uint16_t* tap_zx;   // test tap or null: bf16 in_proj outputs [n_mamba][T][E+Cx+H]
     cudaStream_t side;   // weight unpacking, one GEMM ahead of the caller's stream
     cudaEvent_t ev[5];   // unpacked[2], gemm done[2], call start
+    const vc_paged_kv* kv;   // the paged cache that takes the keys and values; null: k, v
+    int* kv_pos;             // its call's arguments (kPagedPrefillInts)
 };
+static constexpr int kPagedPrefillInts = 8;   // slot, lengths 0 and T, first position granted, row offsets 0 and T
 
 // Mamba-2 mixer of one layer over T frames from zero state: conv (ring written), chunked SSD
 // (final state written to ssm), y (before gating) and the gated-norm output act

@@ -88,12 +88,13 @@ class PagedCache:
 
     @classmethod
     def empty(cls, *, layers, pages, page_size, kv_heads, head_dim, seqs, columns, q_heads, window=0, sinks=0,
-              dtype=torch.bfloat16, device="cuda"):
+              dtype=torch.bfloat16, device="cuda", status=None):
         """a new cache without sessions"""
         k = torch.zeros((layers, pages, kv_heads, page_size, head_dim), dtype=dtype, device=device)
         ints = dict(dtype=torch.int32, device=device)
         return cls(k, torch.zeros_like(k), torch.full((seqs, columns), -1, **ints), torch.zeros((seqs,), **ints),
-                   torch.zeros((pages,), **ints), q_heads=q_heads, window=window, sinks=sinks)
+                   torch.zeros((pages,), **ints), q_heads=q_heads, window=window, sinks=sinks,
+                   status=status)
 
     def _call(self, fn, where, *args, stream=None):
         """fn(cache, *args, stream) on the cache's device"""

@@ -427,6 +427,29 @@ typedef struct {
  * 1 <= rows (rows == batch where cu_rows is NULL). */
 vc_status vc_paged_attend(const vc_paged_kv* kv, int layer, const vc_attn_rows* rows, vc_stream_t stream);
 
+/* One frame as vc_step (emb NULL) or vc_step_fused (emb given: x is the speech embedding and tok_text / tok_func
+ * hold the previous tokens on entry), with the attention layers' keys and values in the paged cache kv in place of
+ * state->k and state->v, which are not used and may be NULL.  kv: this backbone's attention layers in pattern order
+ * (layers = how many, its KV and query heads and head_dim, bf16), seqs = n_slots; its window and sinks apply in every
+ * layer, so that a session whose window is full goes on without an end (kv_capacity does not bound it).  The call
+ * first asks for the frame's position of each row as vc_paged_resize(n = B, add = 1) does; a row that gets none is
+ * skipped: its tokens are -1, its state and length stay, kv->status has the reason (kv->status and state->status may
+ * be one word).  kv->len and state->ctx_len of a session start equal and go on together; a session is ended by
+ * vc_paged_resize to length 0 and copied by vc_paged_fork with ssm, conv and ctx_len as parts.  One kernel per
+ * operation whatever VC_OPT_FRAME says.  kv's workspace is in use: order the call with the other calls on kv. */
+vc_status vc_step_paged(vc_backbone* h, const void* x, const vc_token_embeddings* emb, int B, const int32_t* slots,
+                        const vc_state* state, const vc_paged_kv* kv, int32_t* tok_text, int32_t* tok_func,
+                        vc_stream_t stream);
+
+/* Prefill as vc_prefill with the keys and values in the paged cache kv (as in vc_step_paged): the slot gives
+ * its pages back, takes those of T positions and attends with the cache's window and sinks; the pages that the
+ * window has left behind go back with the session's next step.  Too few free pages (known on the device only):
+ * the slot is left empty, ctx_len 0, its ssm and conv without meaning, VC_DEV_CAPACITY in kv->status.  T at most
+ * kv_capacity and columns * page_size (else VC_ERR_CAPACITY).  Calls on kv run one after another, so this one,
+ * unlike vc_prefill, does not overlap vc_step_paged. */
+vc_status vc_prefill_paged(vc_backbone* h, const void* x, int T, int slot, const vc_state* state,
+                           const vc_paged_kv* kv, vc_stream_t stream);
+
 /* Releases the handle and what the library owns for it (host objects, CUDA graphs, its streams
  * and events); the caller's device memory (weights, state, workspace) is left to the caller.
  * Work the handle queued must be complete (or its stream synchronized) before the call.  The

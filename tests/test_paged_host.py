@@ -168,3 +168,11 @@ def test_reference_book_by_hand():
     assert b.resize([1], [33]) == [-1] and b.status == ref.INVALID | ref.CAPACITY
     assert b.resize([0], [20]) == [-1]                                         # inside a page given up
     assert b.resize([1], [0]) == [0] and b.compact() == (5, [(5, 3)])
+
+
+def test_paged_steps_refuse_a_missing_backbone():
+    m = vc()
+    lib, c, st, emb = m.lib(), kv(), m.VcState(), m.VcTokenEmbeddings()
+    for e in (None, ctypes.byref(emb)):
+        assert lib.vc_step_paged(None, 16, e, 1, None, ctypes.byref(st), ctypes.byref(c), 16, 16, None) == m.VC_ERR_INVALID_ARG
+    assert lib.vc_prefill_paged(None, 16, 1, 0, ctypes.byref(st), ctypes.byref(c), None) == m.VC_ERR_INVALID_ARG
