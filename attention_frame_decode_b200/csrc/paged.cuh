@@ -34,7 +34,9 @@ struct PagedWorkspace {
 static constexpr int kMaxSms = 256;
 static constexpr int kCompactChunk = 4096;
 static constexpr int kMaxSplitCtas = 2 * kMaxSms;      // CTAs of an attention launch that splits the key axis
-static constexpr int kTileRows = 128;                  // rows of the largest attention tile
+// rows of the records that split attention work leaves: kMaxSplitCtas tiles of 64 or 128 rows, or kMaxSms of the
+// prompts' tiles (512 rows of 64 dimensions, 256 of 128)
+static constexpr int kRecordRows = 512 * kMaxSms / 2, kRecordRows64 = 512 * kMaxSms;
 
 // the workspace's parts, in order; false where the sizes are outside the documented limits
 bool paged_sizes_ok(const vc_paged_kv& c);

@@ -44,7 +44,7 @@ PagedWorkspace paged_carve(const vc_paged_kv& c, void* base) {
     w.chunk_live = (int*)take(((size_t)c.pages / kCompactChunk + 1) * 4);
     w.rename = (int*)take((size_t)c.pages * 4);
     w.moves = (int*)take((size_t)c.pages * 8);
-    w.partial = (float*)take((size_t)kMaxSplitCtas * kTileRows * (c.head_dim + 2) * 4);
+    w.partial = (float*)take((size_t)(c.head_dim == 64 ? kRecordRows64 : kRecordRows) * (c.head_dim + 2) * 4);
     w.bytes = off;
     return w;
 }

@@ -19,23 +19,32 @@
 
 namespace vc {
 
-static constexpr int kPRows = 256, kPKeys = 128, kPThreads = 640;
+static constexpr int kPThreads = 640;
 
 template <int DH>
 struct PromptShape {
+    static constexpr int TILES = DH == 128 ? 2 : 4;           // MMA tiles of 128 rows
+    static constexpr int KEYS = DH == 128 ? 128 : 64;         // keys of a block
+    static constexpr int SHARES = KEYS / 64;                  // threads of a row, 64 scores of a block each
+    static constexpr int ROWS = TILES * 128;
     static constexpr int HALVES = DH / 64;                    // 64-wide column parts
-    static constexpr int TILE = kPKeys * DH * 2;              // bytes of a K or V block
-    static constexpr int QBYTES = 2 * TILE;                   // bytes of the rows of Q, [halves][256 rows][128 B]
-    static constexpr int STAGES = DH == 128 ? 4 : 8;          // K and V blocks in turn (a power of two)
+    static constexpr int TILE = KEYS * DH * 2;                // bytes of a K or V block
+    static constexpr int QBYTES = ROWS * DH * 2;              // bytes of the rows of Q, [halves][rows][128 B]
+    static constexpr int STAGES = DH == 128 ? 4 : 16;         // K and V blocks in turn (a power of two)
     static constexpr int BYTES = QBYTES + STAGES * TILE + 1024;
-    static constexpr bool P_APART = DH < 128;
-    // columns from the first 64 keys' weights to the others' (over the scores that they came from, or side by side)
-    static constexpr uint32_t P_HALF = P_APART ? 32 : 64;
-    // tensor memory columns: S of each tile, O of each tile; P shares S's columns where all 512 are needed (the MMAs
-    // of one shape run in order, so S of the next block is written after P of this one is read)
-    static constexpr uint32_t S0 = 0, O0 = 256, P0 = P_APART ? 384 : 0, P_STEP = P_APART ? 64 : 128;
+    static constexpr uint32_t ALL = (1u << (KEYS / 16)) - 1;  // every 16 keys of a block have a page
+    // tensor memory columns: S of each tile, O of each tile.  P lies over S, each thread's weights over the scores that
+    // they came from (the MMAs of one shape run in order, so S of the next block is written after P of this one is read)
+    static constexpr uint32_t S0 = 0, O0 = TILES * KEYS;
+    static_assert(TILES * (KEYS + DH) == 512 && TILES * 4 * SHARES == 16, "tensor memory, warps");
 };
 
+// a warpgroup's registers per thread, all four warps
+template <bool MORE, int N>
+VC_DEV void set_registers() {
+    if constexpr (MORE) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 // one lane of a converged warp.  What that lane alone does needs no proof that its operands are the same in all
 // lanes: the products' descriptors go to uniform registers without a loop over the lanes.
 VC_DEV bool elect_one() {
@@ -141,10 +150,11 @@ struct PromptWork {
 };
 
 // piece `item` of the launch (a whole warp calls); nb is 0 where there is nothing to do, and n_rows too where not even
-// an empty record is wanted, and -1 behind the last piece.  A tile holds whole tokens: tile_rows = (256 / G) G rows.
+// an empty record is wanted, and -1 behind the last piece.  A tile holds whole tokens: tile_rows = (ROWS / G) G rows.
+template <class S>
 VC_DEV PromptWork prompt_work(const PagedAttnArgs& a, int tiles, int splits, int item) {
     PromptWork w{};
-    const int G = a.c.Hq / a.c.Hk, tile_rows = kPRows / G * G;
+    const int G = a.c.Hq / a.c.Hk, tile_rows = S::ROWS / G * G;
     if (item >= tiles * a.c.Hk * splits) {
         w.nb = -1;
         return w;
@@ -164,7 +174,7 @@ VC_DEV PromptWork prompt_work(const PagedAttnArgs& a, int tiles, int splits, int
     w.p_lo = o.p0 + w.r0 / G;
     w.r1 = min(w.r0 + tile_rows, w.n_rows);
     w.p_hi = o.p0 + (w.r1 - 1) / G;
-    w.kb = key_blocks<kPKeys>(a.c.window, a.c.sinks, w.p_lo, w.p_hi);
+    w.kb = key_blocks<S::KEYS>(a.c.window, a.c.sinks, w.p_lo, w.p_hi);
     w.b0 = (int)((long long)w.kb.total * w.split / splits);
     w.nb = (int)((long long)w.kb.total * (w.split + 1) / splits) - w.b0;
     return w;
@@ -179,11 +189,12 @@ __global__ void __launch_bounds__(kPThreads, 1)
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* Qs = smem;                     // [halves][256 rows][128 B]
     uint8_t* ring = smem + S::QBYTES;       // [stages][halves][128 keys][128 B]
-    __shared__ uint64_t full[ST], empty[ST], clean[4], work_ready[2], q_ready[2], q_free, s_full[2], p_ready[2], o_done[2], o_free[2], drained;
-    __shared__ uint32_t tmem_base, block_mapped[16];
+    __shared__ uint64_t full[ST], empty[ST], clean[ST / 2], work_ready[2], q_ready[2], q_free, o_free[2], drained;
+    __shared__ uint64_t s_full[S::TILES], p_ready[S::TILES], o_done[S::TILES];
+    __shared__ uint32_t tmem_base, block_mapped[16];   // of block g at g % 16: at most ST / 2 are in the ring
     __shared__ int odd_values[4], last_flag;
     __shared__ PromptWork work[4];       // piece t at t % 4: written again when the rows are done with it
-    __shared__ float top_x[2][128], l_part[2][2][128];   // a row's highest score, between its two threads; their sums
+    __shared__ float top_x[S::ROWS], l_part[S::SHARES][S::ROWS];   // a row's highest score, between its threads; their sums
 
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int G = a.c.Hq / a.c.Hk, items = tiles * a.c.Hk * splits;   // pieces
@@ -196,16 +207,18 @@ __global__ void __launch_bounds__(kPThreads, 1)
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
-        for (int s = 0; s < 4; ++s) mbar_init(&clean[s], 32);   // values of block g at g % 4: no more are in the ring
+        for (int s = 0; s < ST / 2; ++s) mbar_init(&clean[s], 1);   // values of block g at g % (ST / 2)
         mbar_init(&q_free, 1);
         mbar_init(&drained, 1);
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < S::TILES; ++i) {
             mbar_init(&s_full[i], 1);
-            mbar_init(&p_ready[i], 256);
+            mbar_init(&p_ready[i], 4 * S::SHARES);
             mbar_init(&o_done[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
             mbar_init(&work_ready[i], 1);
             mbar_init(&q_ready[i], 1);
-            mbar_init(&o_free[i], 512 + 32);
+            mbar_init(&o_free[i], 16 + 1);
         }
         fence_mbar_init();
     }
@@ -232,260 +245,272 @@ __global__ void __launch_bounds__(kPThreads, 1)
     // products of piece t + 1 begin after o_free of t, and q_ready of t + 2 after those), the others are held back by
     // the arrivals of the same threads.
 
-    if (warp == 0) {
-        // ---- copies: K of a block, V of the block, K of the next, ... in ring order ----
-        const int box_rows = min(a.c.page, kPKeys), boxes = kPKeys / box_rows;
-        int issued = 0;
-        for (int t = 0; t <= items && ok; ++t) {
-            wait(&work_ready[t & 1], t >> 1);
-            const PromptWork w = work[t & 3];
-            if (w.nb < 0) break;
-            int entry = -1;
-            auto look_up = [&](int n) {   // lane q < boxes: the table entry of block n's q-th box
-                entry = -1;
-                const int t = n < w.nb ? w.kb.block(w.b0 + n) * kPKeys + lane * box_rows : INT32_MAX;
-                if (lane < boxes && t <= w.p_hi) entry = page_of(a.c, w.s, t >> a.c.page_shift);
-            };
-            look_up(0);
-            for (int n = 0; n < w.nb && ok; ++n) {
-                const int t = w.kb.block(w.b0 + n) * kPKeys + lane * box_rows;
-                const bool there = entry >= 0;
-                const unsigned mapped = __ballot_sync(0xffffffffu, there);
-                const int pool_row = (entry * a.c.Hk + w.j) * a.c.page + (t & (a.c.page - 1));
-                look_up(n + 1);
-                for (int kv = 0; kv < 2; ++kv, ++issued) {
-                    const int s = issued & (ST - 1);
-                    if (issued >= ST) wait(&empty[s], issued / ST - 1);
-                    if (!ok) break;
-                    if (lane == 0) {
-                        if (kv == 0) {   // a bit for each 16 keys
-                            uint32_t groups = 0;
-                            for (int u = 0; u < kPKeys / 16; ++u) groups |= ((mapped >> (16 * u / box_rows)) & 1u) << u;
-                            block_mapped[(issued >> 1) & 15] = groups;
+    // the rows' warps take registers that the other four give up; in each SM quarter 4 x 104 + 64 = 5 x 96, the launch's
+    if (warp < 4) {
+        set_registers<false, 64>();
+        if (warp == 0) {
+            // ---- copies: K of a block, V of the block, K of the next, ... in ring order ----
+            const int box_rows = min(a.c.page, S::KEYS), boxes = S::KEYS / box_rows;
+            int issued = 0;
+            for (int t = 0; t <= items && ok; ++t) {
+                wait(&work_ready[t & 1], t >> 1);
+                const PromptWork w = work[t & 3];
+                if (w.nb < 0) break;
+                int entry = -1;
+                auto look_up = [&](int n) {   // lane q < boxes: the table entry of block n's q-th box
+                    entry = -1;
+                    const int t = n < w.nb ? w.kb.block(w.b0 + n) * S::KEYS + lane * box_rows : INT32_MAX;
+                    if (lane < boxes && t <= w.p_hi) entry = page_of(a.c, w.s, t >> a.c.page_shift);
+                };
+                look_up(0);
+                for (int n = 0; n < w.nb && ok; ++n) {
+                    const int t = w.kb.block(w.b0 + n) * S::KEYS + lane * box_rows;
+                    const bool there = entry >= 0;
+                    const unsigned mapped = __ballot_sync(0xffffffffu, there);
+                    const int pool_row = (entry * a.c.Hk + w.j) * a.c.page + (t & (a.c.page - 1));
+                    look_up(n + 1);
+                    for (int kv = 0; kv < 2; ++kv, ++issued) {
+                        const int s = issued & (ST - 1);
+                        if (issued >= ST) wait(&empty[s], issued / ST - 1);
+                        if (!ok) break;
+                        if (lane == 0) {
+                            if (kv == 0) {   // a bit for each 16 keys
+                                uint32_t groups = 0;
+                                for (int u = 0; u < S::KEYS / 16; ++u) groups |= ((mapped >> (16 * u / box_rows)) & 1u) << u;
+                                block_mapped[(issued >> 1) & 15] = groups;
+                            }
+                            mbar_arrive_expect_tx(&full[s], (uint32_t)(__popc(mapped) * box_rows * DH * 2));
                         }
-                        mbar_arrive_expect_tx(&full[s], (uint32_t)(__popc(mapped) * box_rows * DH * 2));
+                        __syncwarp();
+                        if (there)
+#pragma unroll
+                            for (int h = 0; h < S::HALVES; ++h)
+                                tma_load_2d(ring + s * S::TILE + h * (S::KEYS * 128) + lane * box_rows * 128, kv ? &maps.v : &maps.k,
+                                            h * 64, pool_row, &full[s]);
                     }
-                    __syncwarp();
-                    if (there)
-#pragma unroll
-                        for (int h = 0; h < S::HALVES; ++h)
-                            tma_load_2d(ring + s * S::TILE + h * (kPKeys * 128) + lane * box_rows * 128, kv ? &maps.v : &maps.k,
-                                        h * 64, pool_row, &full[s]);
                 }
             }
-        }
-        // no copy outlives the CTA: after a wait that gave up, each gets another bounded while
-        if (!ok)
-            for (int k = max(0, issued - ST); k < issued; ++k) mbar_wait(&full[k & (ST - 1)], (uint32_t)((k / ST) & 1), nullptr);
-    } else if (warp == 1) {
-        // ---- products ----
-        constexpr uint32_t ID_S = umma_idesc(!F16, false, 128, kPKeys), ID_O = umma_idesc(!F16, true, 128, DH);
-        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-        uint32_t fine = 1;
-        const uint64_t q_desc = desc_sw128(smem_u32(Qs)), k_desc = desc_sw128(smem_u32(ring)),
-                       v_desc = umma_desc(smem_u32(ring), kPKeys * 128, 1024, UMMA_SW128);   // addresses count 16 bytes
-        auto mma_s = [&](int i, int s) {   // S_i = Q_i K^T
+            // no copy outlives the CTA: after a wait that gave up, each gets another bounded while
+            if (!ok)
+                for (int k = max(0, issued - ST); k < issued; ++k) mbar_wait(&full[k & (ST - 1)], (uint32_t)((k / ST) & 1), nullptr);
+        } else if (warp == 1) {
+            // ---- products ----
+            constexpr uint32_t ID_S = umma_idesc(!F16, false, 128, S::KEYS), ID_O = umma_idesc(!F16, true, 128, DH);
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            uint32_t fine = 1;
+            const uint64_t q_desc = desc_sw128(smem_u32(Qs)), k_desc = desc_sw128(smem_u32(ring)),
+                           v_desc = umma_desc(smem_u32(ring), S::KEYS * 128, 1024, UMMA_SW128);   // addresses count 16 bytes
+            auto mma_s = [&](int i, int s) {   // S_i = Q_i K^T
 #pragma unroll
-            for (int c = 0; c < DH / 16; ++c) {
-                tc_mma(tm + S::S0 + (uint32_t)(i * 128),
-                       q_desc + (uint32_t)((i * (128 * 128) + (c >> 2) * (256 * 128) + (c & 3) * 32) / 16),
-                       k_desc + (uint32_t)s * (S::TILE / 16) + (uint32_t)(((c >> 2) * (128 * 128) + (c & 3) * 32) / 16), ID_S, c != 0);
-            }
-            tc_commit(&s_full[i]);
-        };
-        auto mma_o = [&](int i, int s, bool first) {   // O_i += P_i V
-#pragma unroll
-            for (int c = 0; c < kPKeys / 16; ++c)
-                tc_mma_ta(tm + S::O0 + (uint32_t)(i * DH), tm + S::P0 + (uint32_t)(i * S::P_STEP + (c >> 2) * S::P_HALF + (c & 3) * 8),
-                          v_desc + (uint32_t)s * (S::TILE / 16) + (uint32_t)(c * 2048 / 16), ID_O, c != 0 || !first);
-            tc_commit(&o_done[i]);
-        };
-        auto hold = [&](uint64_t* bar, int phase) {   // as wait(), with control flow that is the same in all lanes
-            fine &= mbar_poll(bar, (uint32_t)(phase & 1), fine ? kPollLimit : 1u);
-            __syncwarp();
-        };
-        auto slot = [](int k) { return k & (ST - 1); };
-        int g = 0;
-        for (int t = 0; t <= items; ++t) {
-            hold(&q_ready[t & 1], t >> 1);
-            const int nb = __shfl_sync(0xffffffffu, work[t & 3].nb, 0);
-            if (nb < 0) break;
-            if (nb > 0) {
-                hold(&full[slot(2 * g)], 2 * g / ST);
-                tc_fence_after();
-                if (elect_one()) {
-                    mma_s(0, slot(2 * g));
-                    mma_s(1, slot(2 * g));
-                    tc_commit(&empty[slot(2 * g)]);
+                for (int c = 0; c < DH / 16; ++c) {
+                    tc_mma(tm + S::S0 + (uint32_t)(i * S::KEYS),
+                           q_desc + (uint32_t)((i * (128 * 128) + (c >> 2) * (S::ROWS * 128) + (c & 3) * 32) / 16),
+                           k_desc + (uint32_t)s * (S::TILE / 16) + (uint32_t)(((c >> 2) * (S::KEYS * 128) + (c & 3) * 32) / 16), ID_S, c != 0);
                 }
+                tc_commit(&s_full[i]);
+            };
+            auto mma_o = [&](int i, int s, bool first) {   // O_i += P_i V
+#pragma unroll
+                for (int c = 0; c < S::KEYS / 16; ++c)
+                    tc_mma_ta(tm + S::O0 + (uint32_t)(i * DH), tm + S::S0 + (uint32_t)(i * S::KEYS + (c >> 2) * 64 + (c & 3) * 8),
+                              v_desc + (uint32_t)s * (S::TILE / 16) + (uint32_t)(c * 2048 / 16), ID_O, c != 0 || !first);
+                tc_commit(&o_done[i]);
+            };
+            auto hold = [&](uint64_t* bar, int phase) {   // as wait(), with control flow that is the same in all lanes
+                fine &= mbar_poll(bar, (uint32_t)(phase & 1), fine ? kPollLimit : 1u);
                 __syncwarp();
-                if (t > 0) hold(&o_free[(t - 1) & 1], (t - 1) >> 1);   // the outputs of the piece before were read
-                if (nb == 1) {
-                    if (elect_one()) tc_commit(&q_free);
-                    __syncwarp();
-                }
-            } else {
-                if (t > 0) hold(&o_free[(t - 1) & 1], (t - 1) >> 1);
-                if (lane == 0) mbar_arrive(&q_free);
-                __syncwarp();
-            }
-            for (int n = 0; n < nb; ++n, ++g) {
-                const bool more = n + 1 < nb;
-                const int sv = slot(2 * g + 1), sk = slot(2 * g + 2);
-                hold(&clean[g & 3], g >> 2);   // the values are there and clean
-                if (more) hold(&full[sk], (2 * g + 2) / ST);
+            };
+            auto slot = [](int k) { return k & (ST - 1); };
+            int g = 0, gi[S::TILES];   // blocks so far, and those that a tile had rows for
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    hold(&p_ready[i], g);
+            for (int i = 0; i < S::TILES; ++i) gi[i] = 0;
+            for (int t = 0; t <= items; ++t) {
+                hold(&q_ready[t & 1], t >> 1);
+                const int nb = __shfl_sync(0xffffffffu, work[t & 3].nb, 0);
+                const int used = __shfl_sync(0xffffffffu, (work[t & 3].r1 - work[t & 3].r0 + 127) >> 7, 0);   // tiles with rows
+                if (nb < 0) break;
+                if (nb > 0) {
+                    hold(&full[slot(2 * g)], 2 * g / ST);
                     tc_fence_after();
                     if (elect_one()) {
-                        if (S::P_APART && more) mma_s(i, sk);
-                        mma_o(i, sv, n == 0);
-                        if (!S::P_APART && more) mma_s(i, sk);
-                        if (i == 1) {
-                            tc_commit(&empty[sv]);
-                            if (more) tc_commit(&empty[sk]);
-                            if (n + 2 == nb) tc_commit(&q_free);
-                        }
+#pragma unroll
+                        for (int i = 0; i < S::TILES; ++i)
+                            if (i < used) mma_s(i, slot(2 * g));
+                        tc_commit(&empty[slot(2 * g)]);
                     }
                     __syncwarp();
-                }
-            }
-        }
-        if (!fine) {   // no product outlives the tensor memory
-            if (lane == 0) {
-                atomicOr(a.c.status, VC_DEV_TIMEOUT);
-                tc_commit(&drained);
-            }
-            mbar_wait(&drained, 0, nullptr);
-        }
-    } else if (warp == 2) {
-        // ---- the pieces, handed out as CTAs come for them (the first by index), and their rows of Q ----
-        for (int t = 0; t <= items; ++t) {
-            int item = blockIdx.x;
-            if (t > 0) {
-                if (lane == 0) {
-                    const int k = atomicAdd(a.ticket, 1);   // each CTA takes one behind the last piece: `items` in all
-                    if (k == items - 1) *a.ticket = 0;
-                    item = (int)gridDim.x + k;
-                }
-                item = __shfl_sync(0xffffffffu, item, 0);
-            }
-            const PromptWork w = prompt_work(a, tiles, splits, item);
-            if (lane == 0) {
-                work[t & 3] = w;
-                odd_values[t & 3] = 0;
-                mbar_arrive(&work_ready[t & 1]);
-            }
-            if (t > 0) wait(&q_free, t - 1);   // the scores of the piece before are complete
-            if (lane == 0) {
-                if (w.nb > 0 && ok) {
-                    mbar_arrive_expect_tx(&q_ready[t & 1], (uint32_t)(kPRows / G * G * DH * 2));
-                    for (int h = 0; h < S::HALVES; ++h)
-                        tma_load_3d(Qs + h * (256 * 128), &maps.q, h * 64, w.j * G, w.row0 + w.r0 / G, &q_ready[t & 1]);
+                    if (t > 0) hold(&o_free[(t - 1) & 1], (t - 1) >> 1);   // the outputs of the piece before were read
+                    if (nb == 1) {
+                        if (elect_one()) tc_commit(&q_free);
+                        __syncwarp();
+                    }
                 } else {
-                    mbar_arrive(&q_ready[t & 1]);
+                    if (t > 0) hold(&o_free[(t - 1) & 1], (t - 1) >> 1);
+                    if (lane == 0) mbar_arrive(&q_free);
+                    __syncwarp();
                 }
-            }
-            __syncwarp();
-            if (w.nb < 0) break;
-        }
-    } else if (warp == 3) {
-        // ---- values that not every row of the tile sees: those that no row sees become 0, and so do infinities and
-        // NaN (the rows that see them get them at the end), so that a weight of 0 takes nothing in ----
-        int g = 0;
-        for (int t = 0; t <= items; ++t) {
-            wait(&q_ready[t & 1], t >> 1);
-            const PromptWork w = work[t & 3];
-            if (w.nb < 0) break;
-            for (int n = 0; n < w.nb; ++n, ++g) {
-                const int s = (2 * g + 1) & (ST - 1), t0 = w.kb.block(w.b0 + n) * kPKeys;
-                wait(&full[s], (2 * g + 1) / ST);
-                const uint32_t groups = block_mapped[g & 15];
-                const bool whole = groups == 0xffu && t0 + kPKeys - 1 <= w.p_lo &&
-                                   (a.c.window == 0 || t0 > w.p_hi - a.c.window || t0 + kPKeys - 1 < a.c.sinks);
-                if (!whole && ok) {
-                    uint8_t* Vs = ring + s * S::TILE;
-                    constexpr int ROW = S::HALVES * 8;   // 16-byte chunks of a row (their order does not matter)
-                    bool odd = false;
-                    // rows first .. last - 1 of the block: seen by none, or by some
-                    auto sweep = [&](int first, int last, bool none) {
-                        const int n_chunks = max(last - first, 0) * ROW;
-#pragma unroll 4
-                        for (int k = lane; k < n_chunks; k += 32) {
-                            const int c = k % ROW;
-                            uint4* at = reinterpret_cast<uint4*>(Vs + (c >> 3) * (kPKeys * 128) + (first + k / ROW) * 128 + (c & 7) * 16);
-                            if (none) {
-                                *at = make_uint4(0u, 0u, 0u, 0u);
-                            } else {
-                                const uint4 x = *at;
-                                if (any_nonfinite<F16>(x)) {
-                                    odd = true;
-                                    *at = make_uint4(finite2<F16>(x.x), finite2<F16>(x.y), finite2<F16>(x.z), finite2<F16>(x.w));
-                                }
+                for (int n = 0; n < nb; ++n, ++g) {
+                    const bool more = n + 1 < nb;
+                    const int sv = slot(2 * g + 1), sk = slot(2 * g + 2);
+                    hold(&clean[g & (ST / 2 - 1)], g / (ST / 2));   // the values are there and clean
+                    if (more) hold(&full[sk], (2 * g + 2) / ST);
+#pragma unroll
+                    for (int i = 0; i < S::TILES; ++i) {
+                        if (i >= used) continue;
+                        hold(&p_ready[i], gi[i]);
+                        ++gi[i];
+                        tc_fence_after();
+                        if (elect_one()) {
+                            mma_o(i, sv, n == 0);
+                            if (more) mma_s(i, sk);
+                            if (i == used - 1) {
+                                tc_commit(&empty[sv]);
+                                if (more) tc_commit(&empty[sk]);
+                                if (n + 2 == nb) tc_commit(&q_free);
                             }
                         }
                         __syncwarp();
-                    };
-                    auto clip = [&](long long at) { return (int)(at < t0 ? 0 : at > t0 + kPKeys ? kPKeys : at - t0); };
-                    // no page: whatever an earlier block left there
-                    for (int u = 0; u < kPKeys / 16; ++u)
-                        if (!((groups >> u) & 1u)) sweep(16 * u, 16 * u + 16, true);
-                    sweep(clip(w.p_lo + 1LL), clip(w.p_hi + 1LL), false);   // the first row sees up to p_lo, the last to p_hi
-                    sweep(clip(w.p_hi + 1LL), kPKeys, true);
-                    if (a.c.window > 0) {                                    // and from p_lo - window + 1 on, behind the sinks
-                        const long long from = w.p_lo - (long long)a.c.window + 1, to = w.p_hi - (long long)a.c.window + 1;
-                        sweep(clip(a.c.sinks), clip(from), true);
-                        sweep(clip(from > a.c.sinks ? from : a.c.sinks), clip(to), false);
                     }
-                    if (odd) odd_values[t & 3] = 1;
-                    fence_proxy_async();
                 }
-                mbar_arrive(&clean[g & 3]);
             }
-            mbar_arrive(&o_free[t & 1]);   // this role is done with the piece, too
+            if (!fine) {   // no product outlives the tensor memory
+                if (lane == 0) {
+                    atomicOr(a.c.status, VC_DEV_TIMEOUT);
+                    tc_commit(&drained);
+                }
+                mbar_wait(&drained, 0, nullptr);
+            }
+        } else if (warp == 2) {
+            // ---- the pieces, handed out as CTAs come for them (the first by index), and their rows of Q ----
+            for (int t = 0; t <= items; ++t) {
+                int item = blockIdx.x;
+                if (t > 0) {
+                    if (lane == 0) {
+                        const int k = atomicAdd(a.ticket, 1);   // each CTA takes one behind the last piece: `items` in all
+                        if (k == items - 1) *a.ticket = 0;
+                        item = (int)gridDim.x + k;
+                    }
+                    item = __shfl_sync(0xffffffffu, item, 0);
+                }
+                const PromptWork w = prompt_work<S>(a, tiles, splits, item);
+                if (lane == 0) {
+                    work[t & 3] = w;
+                    odd_values[t & 3] = 0;
+                    mbar_arrive(&work_ready[t & 1]);
+                }
+                if (t > 0) wait(&q_free, t - 1);   // the scores of the piece before are complete
+                if (lane == 0) {
+                    if (w.nb > 0 && ok) {
+                        mbar_arrive_expect_tx(&q_ready[t & 1], (uint32_t)(S::ROWS / G * G * DH * 2));
+                        for (int h = 0; h < S::HALVES; ++h)
+                            for (int k = 0; k < S::ROWS / G; k += 256)   // tokens of a box (more than one where G is 1)
+                                tma_load_3d(Qs + (h * S::ROWS + k) * 128, &maps.q, h * 64, w.j * G, w.row0 + w.r0 / G + k,
+                                            &q_ready[t & 1]);
+                    } else {
+                        mbar_arrive(&q_ready[t & 1]);
+                    }
+                }
+                __syncwarp();
+                if (w.nb < 0) break;
+            }
+        } else if (warp == 3) {
+            // ---- values that not every row of the tile sees: those that no row sees become 0, and so do infinities and
+            // NaN (the rows that see them get them at the end), so that a weight of 0 takes nothing in ----
+            int g = 0;
+            for (int t = 0; t <= items; ++t) {
+                wait(&q_ready[t & 1], t >> 1);
+                const PromptWork w = work[t & 3];
+                if (w.nb < 0) break;
+                for (int n = 0; n < w.nb; ++n, ++g) {
+                    const int s = (2 * g + 1) & (ST - 1), t0 = w.kb.block(w.b0 + n) * S::KEYS;
+                    wait(&full[s], (2 * g + 1) / ST);
+                    const uint32_t groups = block_mapped[g & 15];
+                    const bool whole = groups == S::ALL && t0 + S::KEYS - 1 <= w.p_lo &&
+                                       (a.c.window == 0 || t0 > w.p_hi - a.c.window || t0 + S::KEYS - 1 < a.c.sinks);
+                    if (!whole && ok) {
+                        uint8_t* Vs = ring + s * S::TILE;
+                        constexpr int ROW = S::HALVES * 8;   // 16-byte chunks of a row (their order does not matter)
+                        bool odd = false;
+                        // rows first .. last - 1 of the block: seen by none, or by some
+                        auto sweep = [&](int first, int last, bool none) {
+                            const int n_chunks = max(last - first, 0) * ROW;
+#pragma unroll 4
+                            for (int k = lane; k < n_chunks; k += 32) {
+                                const int c = k % ROW;
+                                uint4* at = reinterpret_cast<uint4*>(Vs + (c >> 3) * (S::KEYS * 128) + (first + k / ROW) * 128 + (c & 7) * 16);
+                                if (none) {
+                                    *at = make_uint4(0u, 0u, 0u, 0u);
+                                } else {
+                                    const uint4 x = *at;
+                                    if (any_nonfinite<F16>(x)) {
+                                        odd = true;
+                                        *at = make_uint4(finite2<F16>(x.x), finite2<F16>(x.y), finite2<F16>(x.z), finite2<F16>(x.w));
+                                    }
+                                }
+                            }
+                            __syncwarp();
+                        };
+                        auto clip = [&](long long at) { return (int)(at < t0 ? 0 : at > t0 + S::KEYS ? S::KEYS : at - t0); };
+                        // no page: whatever an earlier block left there
+                        for (int u = 0; u < S::KEYS / 16; ++u)
+                            if (!((groups >> u) & 1u)) sweep(16 * u, 16 * u + 16, true);
+                        sweep(clip(w.p_lo + 1LL), clip(w.p_hi + 1LL), false);   // the first row sees up to p_lo, the last to p_hi
+                        sweep(clip(w.p_hi + 1LL), S::KEYS, true);
+                        if (a.c.window > 0) {                                    // and from p_lo - window + 1 on, behind the sinks
+                            const long long from = w.p_lo - (long long)a.c.window + 1, to = w.p_hi - (long long)a.c.window + 1;
+                            sweep(clip(a.c.sinks), clip(from), true);
+                            sweep(clip(from > a.c.sinks ? from : a.c.sinks), clip(to), false);
+                        }
+                        if (odd) odd_values[t & 3] = 1;
+                        fence_proxy_async();
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&clean[g & (ST / 2 - 1)]);
+                }
+                if (lane == 0) mbar_arrive(&o_free[t & 1]);   // this role is done with the piece, too
+            }
         }
+        set_registers<true, 96>();
     } else {
-        // ---- rows: a row's scores of a block belong to two threads, a half each, whose warps (and those of the other
-        // tile) share the special function units of an SM quarter ----
-        const int i = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1, quarter = warp & 3, rr = quarter * 32 + lane;
+        set_registers<true, 104>();
+        // ---- rows: a row's scores of a block belong to one thread or two (64 each).  The warps of an SM quarter, four
+        // tiles' or two tiles' with two shares each, take turns at its special function units ----
+        const int i = (warp - 4) / (4 * S::SHARES), half = ((warp - 4) >> 2) % S::SHARES, quarter = warp & 3, rr = quarter * 32 + lane;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-        const uint32_t tS = tmem + lanes + S::S0 + (uint32_t)(i * 128 + half * 64), tO = tmem + lanes + S::O0 + (uint32_t)(i * DH),
-                       tP = tmem + lanes + S::P0 + (uint32_t)(i * S::P_STEP + half * S::P_HALF);
-        const int pair = 1 + i * 4 + quarter;   // the barrier of the rows' two warps
+        const uint32_t tS = tmem + lanes + S::S0 + (uint32_t)(i * S::KEYS + half * 64), tO = tmem + lanes + S::O0 + (uint32_t)(i * DH);
+        const int pair = 1 + i * 4 + quarter;   // the barrier of a row's two warps
         const float2 by = make_float2(a.scale_log2, a.scale_log2);
+        int gi = 0;   // blocks so far for this tile
         int g = 0;
         for (int t = 0; t <= items; ++t) {
             wait(&q_ready[t & 1], t >> 1);
             const PromptWork& w = work[t & 3];
-            const int nb = w.nb, r = w.r0 + i * 128 + rr;
-            if (nb < 0) break;
+            const int n_all = w.nb, r = w.r0 + i * 128 + rr;
+            if (n_all < 0) break;
+            const int nb = w.r0 + i * 128 < w.r1 ? n_all : 0;   // a tile without rows has nothing to do
             const bool in = r < w.r1;   // rows behind the tile's last decide nothing (whatever their Q is)
             const PromptRow me{w.p0 + r / G, a.c.window, a.c.sinks};
             const int w_lo = w.p0 + (r - lane) / G, w_hi = w.p0 + (r - lane + 31) / G;   // the warp's rows
             // m: the maximum under which the row's weights stand (its threads agree on it); l: the sum of this thread's
             float m = -INFINITY, l = 0.0f;
-            for (int n = 0; n < nb; ++n, ++g) {
-                const int t0 = w.kb.block(w.b0 + n) * kPKeys + half * 64;
-                wait(&s_full[i], g);
+            for (int n = 0; n < nb; ++n, ++gi) {
+                const int t0 = w.kb.block(w.b0 + n) * S::KEYS + half * 64;
+                const bool inside = t0 + 63 <= w_lo && (a.c.window == 0 || t0 > w_hi - a.c.window || t0 + 63 < a.c.sinks);
+                const bool standing = __all_sync(0xffffffffu, m != -INFINITY || !in);   // of the same rows in both warps
+                wait(&s_full[i], gi);
                 tc_fence_after();
-                const uint32_t groups = block_mapped[g & 15] >> (4 * half);
-                const bool whole = (groups & 0xfu) == 0xfu && t0 + 63 <= w_lo &&
-                                   (a.c.window == 0 || t0 > w_hi - a.c.window || t0 + 63 < a.c.sinks);
-                float t4[4], v[32];
+                const uint32_t groups = block_mapped[(g + n) & 15] >> (4 * half);
+                const bool whole = inside && (groups & 0xfu) == 0xfu;
+                float v[32];
                 float2 part[2];
                 uint32_t pk[2][16];
-                auto take = [&](int c) {   // scores of columns c .. c + 31, -inf where not seen, and their maximum
+                auto take = [&](int c) {   // scores of columns c .. c + 31, -inf where not seen
                     tc_ld32(tS + (uint32_t)c, v);
                     if (!whole) {
                         const uint32_t seen = me.seen(t0 + c, groups >> (c >> 4));
 #pragma unroll
                         for (int e = 0; e < 32; ++e) v[e] = (seen >> e) & 1u ? v[e] : -INFINITY;
                     }
-#pragma unroll
-                    for (int e = 0; e < 32; e += 8)
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) t4[u] = max3(t4[u], v[e + u], v[e + 4 + u]);
                 };
                 // the weights 2^(z scale - base): added to the sum, and rounded to 16 bits as the tensor core takes them
                 // (2^-9 of a weight in bf16, 2^-12 in fp16); 0 where not seen
@@ -499,35 +524,50 @@ __global__ void __launch_bounds__(kPThreads, 1)
                         u[e] = pack16<F16>(z.x, z.y);
                     }
                 };
-                auto clear = [&]() {
+                auto weigh_all = [&](float base) {   // one pass over the thread's scores -> the sum of its weights
+                    const float2 off = make_float2(-base, -base);
                     part[0] = part[1] = make_float2(0.0f, 0.0f);
-                    t4[0] = t4[1] = t4[2] = t4[3] = -INFINITY;
+                    take(0);
+                    weigh(pk[0], off);
+                    take(32);
+                    weigh(pk[1], off);
+                    return (part[0].x + part[0].y) + (part[1].x + part[1].y);
                 };
-                auto top = [&]() { return max3(t4[0], max3(t4[1], t4[2], t4[3]), t4[3]) * a.scale_log2; };   // scale above 0
-                // the weights under the maximum that stands, which holds nearly always: the scores are passed over once
-                clear();
-                const bool standing = __all_sync(0xffffffffu, m != -INFINITY || !in);   // of the same rows in both warps
-                take(0);
-                if (standing) weigh(pk[0], make_float2(-m, -m));
-                take(32);
-                if (standing) weigh(pk[1], make_float2(-m, -m));
-                if (!standing || any_of_pair(pair, in && !(top() <= m + 8.0f))) {   // (not where a score is not a number)
+                // The weights under the maximum that stands, which holds nearly always: a sum of at most 2^14 has no weight
+                // above it, which both 16-bit types hold.  (64 weights of at most 2^8 do not pass it.)
+                float sum = 0.0f;
+                if (standing) sum = weigh_all(m);
+                const bool grew = in && !(sum <= 16384.0f);   // or a score is not a number
+                if (!standing || (S::SHARES == 2 ? any_of_pair(pair, grew) : __any_sync(0xffffffffu, grew))) {
                     // it moves where it grew by more than 8 (a factor of 2^8), or was none (then all weights so far were 0)
-                    float tp = top();
-                    if (half == 0) top_x[i][rr] = tp;
-                    sync_pair(pair);
-                    if (half == 1) top_x[i][rr] = max3(tp, top_x[i][rr], tp);
-                    sync_pair(pair);
-                    tp = top_x[i][rr];
+                    float t4[4];
+                    t4[0] = t4[1] = t4[2] = t4[3] = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < 64; c += 32) {
+                        take(c);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8)
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) t4[u] = max3(t4[u], v[e + u], v[e + 4 + u]);
+                    }
+                    float tp = max3(t4[0], max3(t4[1], t4[2], t4[3]), t4[3]) * a.scale_log2;   // scale above 0
+                    if (S::SHARES == 2) {
+                        float& x = top_x[i * 128 + rr];
+                        if (half == 0) x = tp;
+                        sync_pair(pair);
+                        if (half == 1) x = max3(tp, x, tp);
+                        sync_pair(pair);
+                        tp = x;
+                    }
                     const float m_new = tp <= m + 8.0f ? m : tp;   // NaN moves it too, and makes the row's sum NaN
                     const float f = !in || m == -INFINITY || m_new == m ? 1.0f : exp2_approx(m - m_new);
                     m = m_new;
                     l *= f;
-                    if (n > 0 && __any_sync(0xffffffffu, f != 1.0f)) {   // the products so far are in O_i; a half of it each
-                        wait(&o_done[i], g - 1);
+                    if (n > 0 && __any_sync(0xffffffffu, f != 1.0f)) {   // the products so far are in O_i; the row's threads share its columns
+                        wait(&o_done[i], gi - 1);
                         tc_fence_after();
 #pragma unroll 1
-                        for (int c = half * (DH / 2); c < (half + 1) * (DH / 2); c += 16) {
+                        for (int c = half * (DH / S::SHARES); c < (half + 1) * (DH / S::SHARES); c += 16) {
                             float x[16];
                             tc_ld16(tO + (uint32_t)c, x);
                             uint32_t u[16];
@@ -536,30 +576,23 @@ __global__ void __launch_bounds__(kPThreads, 1)
                             tc_st16(tO + (uint32_t)c, u);
                         }
                     }
-                    const float base = m == -INFINITY ? 0.0f : m;
-                    const float2 off_new = make_float2(-base, -base);
-                    clear();
-                    take(0);
-                    weigh(pk[0], off_new);
-                    take(32);
-                    weigh(pk[1], off_new);
+                    sum = weigh_all(m == -INFINITY ? 0.0f : m);
                 }
-                l += (part[0].x + part[0].y) + (part[1].x + part[1].y);
-                if (S::P_APART && g > 0) {   // the products with the weights before are complete (elsewhere: they were before S)
-                    wait(&o_done[i], g - 1);
-                    tc_fence_after();
-                }
-                tc_st16(tP, pk[0]);
-                tc_st16(tP + 16, pk[1]);
+                l += sum;
+                tc_st16(tS, pk[0]);
+                tc_st16(tS + 16, pk[1]);
                 tc_wait_st();
                 tc_fence_before();
-                mbar_arrive(&p_ready[i]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_ready[i]);   // (arrivals of all lanes would take turns)
             }
-            // ---- out, or a split's record: [256][DH] sums, [256] maxima, [256] sums of weights ----
+            // ---- out, or a split's record: [ROWS][DH] sums, [ROWS] maxima, [ROWS] sums of weights ----
             if (nb > 0) {
-                l_part[i][half][rr] = l;
-                sync_pair(pair);
-                l = l_part[i][0][rr] + l_part[i][1][rr];
+                if (S::SHARES == 2) {
+                    l_part[half][i * 128 + rr] = l;
+                    sync_pair(pair);
+                    l = l_part[0][i * 128 + rr] + l_part[S::SHARES - 1][i * 128 + rr];
+                }
             }
             const int at = i * 128 + rr;
             const long long mine = in ? (long long)(w.row0 + r / G) * a.out_ld + (long long)(w.j * G + r % G) * DH : -1;
@@ -567,30 +600,31 @@ __global__ void __launch_bounds__(kPThreads, 1)
 #pragma unroll
             for (int u = 0; u < 4; ++u) to[u] = __shfl_sync(0xffffffffu, mine, (lane & ~3) + u);
             const float inv = splits > 1 ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
-            float* rec = a.partial + ((size_t)w.unit * splits + w.split) * (kPRows * (DH + 2));
+            float* rec = a.partial + ((size_t)w.unit * splits + w.split) * (S::ROWS * (DH + 2));
             if (nb > 0) {
-                wait(&o_done[i], g - 1);
+                wait(&o_done[i], gi - 1);
                 tc_fence_after();
             }
             const bool odd = odd_values[t & 3] != 0;
 #pragma unroll 1
-            for (int c = half * (DH / 2); c < (half + 1) * (DH / 2); c += 32) {   // a half each
+            for (int c = half * (DH / S::SHARES); c < (half + 1) * (DH / S::SHARES); c += 32) {
                 float v[32];
                 if (nb > 0) tc_ld32(tO + (uint32_t)c, v);
                 else
 #pragma unroll
                     for (int e = 0; e < 32; ++e) v[e] = 0.0f;
-                if (c + 32 == (half + 1) * (DH / 2)) {   // O_i may be written again
+                if (c + 32 == (half + 1) * (DH / S::SHARES)) {   // O_i may be written again
                     tc_fence_before();
-                    mbar_arrive(&o_free[t & 1]);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&o_free[t & 1]);
                 }
                 if (!ok) continue;
 #pragma unroll
                 for (int e = 0; e < 32; ++e) v[e] *= inv;
                 if (odd && in)   // the infinities and NaN that were taken out of the values, to the rows that see them
                     for (int n = 0; n < nb; ++n)
-                        for (int u = 0; u < kPKeys; ++u) {
-                            const int p = w.kb.block(w.b0 + n) * kPKeys + u;
+                        for (int u = 0; u < S::KEYS; ++u) {
+                            const int p = w.kb.block(w.b0 + n) * S::KEYS + u;
                             if (p > me.p || !(a.c.window == 0 || p < a.c.sinks || p > me.p - a.c.window)) continue;
                             const int e = page_of(a.c, w.s, p >> a.c.page_shift);
                             if (e < 0) continue;
@@ -622,10 +656,12 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 }
             }
             if (splits > 1 && half == 0 && in) {
-                __stcg(rec + kPRows * DH + at, m);
-                __stcg(rec + kPRows * DH + kPRows + at, l);
+                __stcg(rec + S::ROWS * DH + at, m);
+                __stcg(rec + S::ROWS * DH + S::ROWS + at, l);
             }
+            g += n_all;
         }
+        set_registers<false, 96>();
     }
     tc_fence_before();
     __syncthreads();
@@ -647,20 +683,20 @@ __global__ void __launch_bounds__(kPThreads, 1)
     }
     __syncthreads();
     if (!last_flag) return;
-    constexpr int REC = kPRows * (DH + 2);
+    constexpr int REC = S::ROWS * (DH + 2);
     const float* all = a.partial + (size_t)w.unit * splits * REC;
     for (int idx = tid; idx < (w.r1 - w.r0) * (DH / 4); idx += kPThreads) {
         const int r = idx / (DH / 4), d = 4 * (idx % (DH / 4));
         float top = -INFINITY;
-        for (int sp = 0; sp < splits; ++sp) top = fmaxf(top, __ldcg(all + (size_t)sp * REC + kPRows * DH + r));
+        for (int sp = 0; sp < splits; ++sp) top = fmaxf(top, __ldcg(all + (size_t)sp * REC + S::ROWS * DH + r));
         if (top == -INFINITY) top = 0.0f;
         float sum = 0.0f, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 4
         for (int sp = 0; sp < splits; ++sp) {   // a split that saw nothing: maximum -inf, factor 0, sums 0
             const float* p = all + (size_t)sp * REC;
-            const float f = exp2_approx(__ldcg(p + kPRows * DH + r) - top);
+            const float f = exp2_approx(__ldcg(p + S::ROWS * DH + r) - top);
             const float4 x = __ldcg(reinterpret_cast<const float4*>(p + r * DH + d));
-            sum = fmaf(__ldcg(p + kPRows * DH + kPRows + r), f, sum);
+            sum = fmaf(__ldcg(p + S::ROWS * DH + S::ROWS + r), f, sum);
             v[0] = fmaf(x.x, f, v[0]); v[1] = fmaf(x.y, f, v[1]);
             v[2] = fmaf(x.z, f, v[2]); v[3] = fmaf(x.w, f, v[3]);
         }
@@ -675,19 +711,19 @@ template <int DH, bool F16>
 static cudaError_t launch_prompts_t(const PagedAttnArgs& a, cudaStream_t s) {
     using S = PromptShape<DH>;
     const long long G = a.c.Hq / a.c.Hk;
-    if (G > kPRows) return cudaErrorNotSupported;
+    if (G > 256) return cudaErrorNotSupported;
     // at most: every session's last tile may be part-filled
-    const long long tile_rows = kPRows / G * G, tiles = (a.rows * G + tile_rows - 1) / tile_rows + a.batch,
+    const long long tile_rows = S::ROWS / G * G, tiles = (a.rows * G + tile_rows - 1) / tile_rows + a.batch,
                     units = tiles * a.c.Hk;
     if (units > INT32_MAX) return cudaErrorNotSupported;
     const int splits = units < a.num_sms ? (int)(a.num_sms / units) : 1;
     PromptMaps maps;
-    const int rows = a.c.pages * a.c.Hk * a.c.page, box = a.c.page < kPKeys ? a.c.page : kPKeys;
+    const int rows = a.c.pages * a.c.Hk * a.c.page, box = a.c.page < S::KEYS ? a.c.page : S::KEYS;
     EncodeTiledFn encode = tma_encode_fn();
     // a tile's rows of Q: whole tokens, the heads of one KV head of each, packed as they come
     const cuuint64_t dims[3] = {(cuuint64_t)DH, (cuuint64_t)a.c.Hq, (cuuint64_t)a.rows};
     const cuuint64_t strides[2] = {(cuuint64_t)DH * 2, (cuuint64_t)a.q_ld * 2};
-    const cuuint32_t q_box[3] = {64, (cuuint32_t)G, (cuuint32_t)(kPRows / G)}, unit[3] = {1, 1, 1};
+    const cuuint32_t q_box[3] = {64, (cuuint32_t)G, (cuuint32_t)(S::ROWS / G < 256 ? S::ROWS / G : 256)}, unit[3] = {1, 1, 1};
     if (!encode ||
         encode(&maps.q, F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(a.q),
                dims, strides, q_box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
