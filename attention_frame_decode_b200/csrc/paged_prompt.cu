@@ -1,19 +1,27 @@
 // paged_prompt.cu -- windowed attention over the paged KV cache for prompts, on tcgen05 tensor cores.
 //
-// The packed rows of a session and KV head (paged_attn.cu) are cut into tiles of 256 = two MMA tiles of 128 rows;
-// one CTA per SM takes tiles in turn and walks the blocks of 128 keys that a tile's rows can see.  Per block and MMA
-// tile i:
+// The packed rows of a session and KV head (paged_attn.cu) are cut into tiles of 256 (head dim 128) or 512 rows (head
+// dim 64): two or four MMA tiles of 128 rows.  One CTA per SM takes tiles in turn and walks the blocks of 128 or 64
+// keys that a tile's rows can see.  Per block and MMA tile i:
 //     S_i = Q_i K^T (tcgen05.mma into tensor memory, fp32)
-//     P_i = exp2(scale S_i - m_i), two threads per row, written back to tensor memory as the 16-bit A operand
+//     P_i = exp2(scale S_i - m_i), 64 scores a thread, written back to tensor memory as the 16-bit A operand
 //     O_i += P_i V (tcgen05.mma, A from tensor memory)
-// The two tiles alternate: while the threads of one form its weights, the tensor core works on the other's
-// products.  The running maximum moves only when it grew by more than 2^8 (weights up to 2^8 lose no precision in
-// fp32 or the 16-bit formats), so O_i is rarely read back to be rescaled, and a block's weights are formed in one pass
-// over its scores.
-// Bound: per block and SM about 2 x 1008 cycles of products (M = N = 128: 63 each) and 2 x 1024 of exponentials; what
-// it takes is the chain of one tile, weights then products, since tensor memory has no room for scores ahead.
-// Warps: 0 copies K and V page by page (TMA, 128-byte swizzle) into a ring; 1 issues the MMAs; 2 brings the rows of Q;
-// 3 cleans the values of edge blocks; 4-11 and 12-19 are the rows of the two tiles.
+// The MMA tiles alternate: while the threads of one form its weights, the tensor core works on the others' products.
+// m_i moves only where a row's highest score grew by more than 8 (a factor of 2^8), and what is checked on the way is
+// the sum of a thread's 64 weights: at most 2^14, no weight is above it (the 16-bit types hold that; fp32 sums lose
+// nothing by the common factor).  So O_i is rarely read back to be rescaled, a block's scores are passed over once, and
+// no maximum is taken: at head dim 64, where issue slots and exponentials are what is short, that was worth 9%.
+// Bound, per block of 128 keys x 256 rows (or 64 x 512) and SM: 2048 cycles of exponentials (8 a warp and register) and
+// 2016 (head dim 128: M = N = 128, 63 each) or 1256 of products.  What it takes is the chain of one tile -- scores on
+// their way 600 to 1300, weights 1100 alone, their way back 200 -- against the other tiles' chains: about 3400 cycles
+// at head dim 128, whose tensor memory has no room for a third tile, and 2800 at head dim 64 with four tiles (with two
+// tiles of 128 keys and two threads a row 3700: 219 us where four tiles take 198).
+// Measured on a B200: 8192 rows of 40 heads over 8 of 128, window 4096, 64 sinks: 494 us, 1060 TFLOP/s of what the rows
+// see; 12 blocks of 1 to 900 rows, 32 heads over 8 of 64, window 2048: 181 us, of which a quarter is the last round of
+// tiles (2.4 a CTA; splitting that round's key blocks gave back in records and joins what it evened out, and cost the
+// other launch 2%).  A polynomial on the FMA units for every fourth or eighth exponential: 4 to 9% slower (issue slots).
+// Warps: 0 copies K and V page by page (TMA, 128-byte swizzle) into a ring; 1 issues the MMAs; 2 hands out pieces and
+// brings the rows of Q; 3 cleans the values of edge blocks; 4-19 are the rows.
 #include "paged_dev.cuh"
 #include "tc.cuh"
 
