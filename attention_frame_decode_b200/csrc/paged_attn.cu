@@ -82,7 +82,9 @@ __global__ void __launch_bounds__(kTThreads) paged_tile_kernel(const PagedAttnAr
     const int n_rows = o.n * G, r0 = tile * kTR;
     const int p_lo = o.p0 + r0 / G, p_hi = o.p0 + (min(r0 + kTR, n_rows) - 1) / G;
     const KeyBlocks kb = key_blocks<kTK>(a.c.window, a.c.sinks, p_lo, p_hi);
-    const int i0 = (int)((long long)kb.total * split / splits), i1 = (int)((long long)kb.total * (split + 1) / splits);
+    const int of = key_splits(kb.total, splits);
+    if (split >= of) return;
+    const int i0 = (int)((long long)kb.total * split / of), i1 = (int)((long long)kb.total * (split + 1) / of);
 
     auto load = [&](int i) {
         if (i < i1) {
@@ -231,7 +233,7 @@ __global__ void __launch_bounds__(kTThreads) paged_tile_kernel(const PagedAttnAr
         l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
     }
     auto out_row = [&](int rr) { return a.out + (size_t)(o.row0 + rr / G) * a.out_ld + (size_t)(j * G + rr % G) * DH; };
-    if (splits == 1) {
+    if (of == 1) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int rr = r0 + 16 * warp + g + 8 * h;
@@ -263,33 +265,48 @@ __global__ void __launch_bounds__(kTThreads) paged_tile_kernel(const PagedAttnAr
     __threadfence();
     __syncthreads();
     if (tid == 0) {
-        last_flag = atomicAdd(a.merge + unit, 1) == splits - 1;
+        last_flag = atomicAdd(a.merge + unit, 1) == of - 1;
         if (last_flag) a.merge[unit] = 0;
     }
     __syncthreads();
     if (!last_flag) return;
     __threadfence();
     const float* all = a.partial + (size_t)unit * splits * REC;
-    for (int idx = tid; idx < kTR * (DH / 4); idx += kTThreads) {
-        const int r = idx / (DH / 4), d = 4 * (idx % (DH / 4));
-        if (r0 + r >= n_rows) break;
-        float top = -INFINITY;
-        for (int sp = 0; sp < splits; ++sp) top = fmaxf(top, __ldcg(all + (size_t)sp * REC + kTR * DH + r));
+    float* factor = reinterpret_cast<float*>(smem);   // [of][64], where the rows of Q, K and V were
+    const int rows = min(kTR, n_rows - r0);
+    if (tid < rows) {
+        const float* x = all + kTR * DH + tid;
+        float top = -INFINITY, sum = 0.0f;
+#pragma unroll 8
+        for (int sp = 0; sp < of; ++sp) {
+            const float t = __ldcg(x + (size_t)sp * REC);
+            factor[sp * kTR + tid] = t;
+            top = fmaxf(top, t);
+        }
         if (top == -INFINITY) top = 0.0f;
-        float w_sum = 0.0f, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (int sp = 0; sp < splits; ++sp) {
-            const float* p = all + (size_t)sp * REC;
-            const float ls = __ldcg(p + kTR * DH + kTR + r);
-            if (ls == 0.0f) continue;   // the split saw nothing for this row
-            const float w = exp2_approx(__ldcg(p + kTR * DH + r) - top);
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(p + r * DH + d));
-            w_sum = fmaf(ls, w, w_sum);
+#pragma unroll 8
+        for (int sp = 0; sp < of; ++sp) {   // a split that saw nothing for this row: maximum -inf, factor 0, sums 0
+            const float f = exp2_approx(factor[sp * kTR + tid] - top);
+            factor[sp * kTR + tid] = f;
+            sum = fmaf(__ldcg(x + (size_t)sp * REC + kTR), f, sum);
+        }
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        for (int sp = 0; sp < of; ++sp) factor[sp * kTR + tid] *= inv;
+    }
+    __syncthreads();
+#pragma unroll 2
+    for (int idx = tid; idx < rows * (DH / 4); idx += kTThreads) {
+        const int r = idx / (DH / 4), d = 4 * (idx % (DH / 4));
+        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
+        for (int sp = 0; sp < of; ++sp) {
+            const float w = factor[sp * kTR + r];
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(all + (size_t)sp * REC + r * DH + d));
             v[0] = fmaf(x.x, w, v[0]); v[1] = fmaf(x.y, w, v[1]);
             v[2] = fmaf(x.z, w, v[2]); v[3] = fmaf(x.w, w, v[3]);
         }
-        const float inv = w_sum == 0.0f ? 0.0f : 1.0f / w_sum;
         *reinterpret_cast<uint2*>(out_row(r0 + r) + d) =
-            make_uint2(pack_out<F16>(a.widen, v[0] * inv, v[1] * inv), pack_out<F16>(a.widen, v[2] * inv, v[3] * inv));
+            make_uint2(pack_out<F16>(a.widen, v[0], v[1]), pack_out<F16>(a.widen, v[2], v[3]));
     }
 }
 

@@ -156,6 +156,10 @@ VC_DEV KeyBlocks key_blocks(int window, int sinks, int p_lo, int p_hi) {
     return k;
 }
 
+// into how many ranges a tile's key blocks are split: at most `splits`, and two blocks or more in each (a record and its
+// join take about as long)
+VC_DEV int key_splits(int blocks, int splits) { return max(min(splits, blocks / 2), 1); }
+
 // the session and the tile within it of the launch's `tile`-th tile; false behind the last (a whole warp calls)
 VC_DEV bool find_tile(const PagedAttnArgs& a, int group, int tile_rows, int tile, int& session, int& t) {
     const int lane = threadIdx.x & 31;

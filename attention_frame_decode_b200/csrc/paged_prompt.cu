@@ -154,7 +154,7 @@ struct PromptWork {
     int b0, nb;
     int s, row0, n_rows;     // the session's index and first row; its packed rows
     int r0, r1, p0;          // the tile's packed rows r0 .. r1 - 1; the position of the session's first row
-    int p_lo, p_hi, j, unit, split;
+    int p_lo, p_hi, j, unit, split, of;   // of: into how many pieces the tile is split
 };
 
 // piece `item` of the launch (a whole warp calls); nb is 0 where there is nothing to do, and n_rows too where not even
@@ -183,8 +183,13 @@ VC_DEV PromptWork prompt_work(const PagedAttnArgs& a, int tiles, int splits, int
     w.r1 = min(w.r0 + tile_rows, w.n_rows);
     w.p_hi = o.p0 + (w.r1 - 1) / G;
     w.kb = key_blocks<S::KEYS>(a.c.window, a.c.sinks, w.p_lo, w.p_hi);
-    w.b0 = (int)((long long)w.kb.total * w.split / splits);
-    w.nb = (int)((long long)w.kb.total * (w.split + 1) / splits) - w.b0;
+    w.of = key_splits(w.kb.total, splits);
+    if (w.split >= w.of) {   // nothing left for it
+        w.n_rows = w.r1 = 0;
+        return w;
+    }
+    w.b0 = (int)((long long)w.kb.total * w.split / w.of);
+    w.nb = (int)((long long)w.kb.total * (w.split + 1) / w.of) - w.b0;
     return w;
 }
 
@@ -607,7 +612,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
             long long to[4];   // where the rows of the thread's group of four go
 #pragma unroll
             for (int u = 0; u < 4; ++u) to[u] = __shfl_sync(0xffffffffu, mine, (lane & ~3) + u);
-            const float inv = splits > 1 ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
+            const int of = w.of;
+            const float inv = of > 1 ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
             float* rec = a.partial + ((size_t)w.unit * splits + w.split) * (S::ROWS * (DH + 2));
             if (nb > 0) {
                 wait(&o_done[i], gi - 1);
@@ -641,7 +647,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                             for (int q = 0; q < 32; ++q)
                                 if ((x[q] & exponent_mask<F16>()) == exponent_mask<F16>()) v[q] += unpack16<F16>(x[q]);
                         }
-                if (splits == 1) {
+                if (of == 1) {
                     // four lanes exchange the 16-byte pieces of their rows, so that each writes 64 bytes of a row together
                     uint4 x[4];
 #pragma unroll
@@ -663,7 +669,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                         __stcg(reinterpret_cast<float4*>(rec + at * DH + c + e), make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]));
                 }
             }
-            if (splits > 1 && half == 0 && in) {
+            if (of > 1 && half == 0 && in) {
                 __stcg(rec + S::ROWS * DH + at, m);
                 __stcg(rec + S::ROWS * DH + S::ROWS + at, l);
             }
@@ -682,10 +688,11 @@ __global__ void __launch_bounds__(kPThreads, 1)
 
     // ---- the last split of the tile to arrive joins them in order (a CTA has one piece where tiles are split) ----
     const PromptWork& w = work[0];
-    if (w.n_rows == 0) return;
+    if (w.n_rows == 0 || w.of == 1) return;
+    const int of = w.of;
     if (tid == 0) {
         __threadfence();   // the CTA's record, ordered by the barrier, before its arrival
-        last_flag = atomicAdd(a.merge + w.unit, 1) == splits - 1;
+        last_flag = atomicAdd(a.merge + w.unit, 1) == of - 1;
         if (last_flag) a.merge[w.unit] = 0;
         __threadfence();
     }
@@ -693,25 +700,41 @@ __global__ void __launch_bounds__(kPThreads, 1)
     if (!last_flag) return;
     constexpr int REC = S::ROWS * (DH + 2);
     const float* all = a.partial + (size_t)w.unit * splits * REC;
-    for (int idx = tid; idx < (w.r1 - w.r0) * (DH / 4); idx += kPThreads) {
-        const int r = idx / (DH / 4), d = 4 * (idx % (DH / 4));
-        float top = -INFINITY;
-        for (int sp = 0; sp < splits; ++sp) top = fmaxf(top, __ldcg(all + (size_t)sp * REC + S::ROWS * DH + r));
+    float* factor = reinterpret_cast<float*>(smem);   // [of][ROWS], where the rows of Q and the ring were
+    const int n_rows = w.r1 - w.r0;
+    for (int r = tid; r < n_rows; r += kPThreads) {
+        const float* x = all + S::ROWS * DH + r;   // a split that saw nothing: maximum -inf, factor 0, sums 0
+        float top = -INFINITY, sum = 0.0f;
+#pragma unroll 8
+        for (int sp = 0; sp < of; ++sp) {
+            const float t = __ldcg(x + (size_t)sp * REC);
+            factor[sp * S::ROWS + r] = t;
+            top = fmaxf(top, t);
+        }
         if (top == -INFINITY) top = 0.0f;
-        float sum = 0.0f, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-        for (int sp = 0; sp < splits; ++sp) {   // a split that saw nothing: maximum -inf, factor 0, sums 0
-            const float* p = all + (size_t)sp * REC;
-            const float f = exp2_approx(__ldcg(p + S::ROWS * DH + r) - top);
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(p + r * DH + d));
-            sum = fmaf(__ldcg(p + S::ROWS * DH + S::ROWS + r), f, sum);
+#pragma unroll 8
+        for (int sp = 0; sp < of; ++sp) {
+            const float f = exp2_approx(factor[sp * S::ROWS + r] - top);
+            factor[sp * S::ROWS + r] = f;
+            sum = fmaf(__ldcg(x + (size_t)sp * REC + S::ROWS), f, sum);
+        }
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        for (int sp = 0; sp < of; ++sp) factor[sp * S::ROWS + r] *= inv;
+    }
+    __syncthreads();
+    for (int idx = tid; idx < n_rows * (DH / 4); idx += kPThreads) {
+        const int r = idx / (DH / 4), d = 4 * (idx % (DH / 4));
+        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
+        for (int sp = 0; sp < of; ++sp) {
+            const float f = factor[sp * S::ROWS + r];
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(all + (size_t)sp * REC + r * DH + d));
             v[0] = fmaf(x.x, f, v[0]); v[1] = fmaf(x.y, f, v[1]);
             v[2] = fmaf(x.z, f, v[2]); v[3] = fmaf(x.w, f, v[3]);
         }
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
         uint16_t* to = a.out + (size_t)(w.row0 + (w.r0 + r) / G) * a.out_ld + (size_t)(w.j * G + (w.r0 + r) % G) * DH + d;
         *reinterpret_cast<uint2*>(to) =
-            make_uint2(pack_out<F16>(a.widen, v[0] * inv, v[1] * inv), pack_out<F16>(a.widen, v[2] * inv, v[3] * inv));
+            make_uint2(pack_out<F16>(a.widen, v[0], v[1]), pack_out<F16>(a.widen, v[2], v[3]));
     }
 }
 
@@ -724,7 +747,9 @@ static cudaError_t launch_prompts_t(const PagedAttnArgs& a, cudaStream_t s) {
     const long long tile_rows = S::ROWS / G * G, tiles = (a.rows * G + tile_rows - 1) / tile_rows + a.batch,
                     units = tiles * a.c.Hk;
     if (units > INT32_MAX) return cudaErrorNotSupported;
-    const int splits = units < a.num_sms ? (int)(a.num_sms / units) : 1;
+    // (the join's factors take the room of the rows of Q and the ring)
+    constexpr int most = (S::BYTES - 1024) / (S::ROWS * 4) < 64 ? (S::BYTES - 1024) / (S::ROWS * 4) : 64;
+    const int splits = units < a.num_sms ? (int)(a.num_sms / units < most ? a.num_sms / units : most) : 1;
     PromptMaps maps;
     const int rows = a.c.pages * a.c.Hk * a.c.page, box = a.c.page < S::KEYS ? a.c.page : S::KEYS;
     EncodeTiledFn encode = tma_encode_fn();
