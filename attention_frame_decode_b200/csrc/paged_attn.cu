@@ -51,20 +51,24 @@ cudaError_t launch_paged_append(const PagedAttnArgs& a, cudaStream_t s) {
 }
 
 // ------------------------------------------------------------------------------------------
-// row tiles: 64 packed rows per CTA, 16 per warp, key blocks of 64 positions double-buffered with cp.async.
+// row tiles: 64 or 128 packed rows per CTA, 16 per warp, key blocks of 64 positions double-buffered with cp.async.
 // The key axis is split over `splits` CTAs where there are few tiles; the last CTA of a tile to arrive joins
 // them in split order.
 // ------------------------------------------------------------------------------------------
-static constexpr int kTR = 64, kTK = 64, kTThreads = 128;
+static constexpr int kTK = 64;
+// 64 rows a CTA, or 128 (8 warps in place of 4)
+template <int DH, int ROWS>
+struct TileShape {
+    static constexpr int THREADS = 2 * ROWS;
+    static constexpr size_t BYTES = (size_t)(ROWS + 4 * kTK) * (DH + 8) * 2;
+};
 
-template <int DH>
-static constexpr size_t tile_smem_bytes() { return (size_t)5 * 64 * (DH + 8) * 2; }
-
-template <int DH, bool F16>
-__global__ void __launch_bounds__(kTThreads) paged_tile_kernel(const PagedAttnArgs a, int splits) {
+template <int DH, bool F16, int ROWS>
+__global__ void __launch_bounds__(TileShape<DH, ROWS>::THREADS) paged_tile_kernel(const PagedAttnArgs a, int splits) {
+    constexpr int kTR = ROWS, kTThreads = TileShape<DH, ROWS>::THREADS;
     constexpr int SK = DH + 8, CH = DH / 8, NT = DH / 8;
     extern __shared__ __align__(16) uint8_t smem[];
-    uint16_t* Qs = reinterpret_cast<uint16_t*>(smem);   // [64][SK]
+    uint16_t* Qs = reinterpret_cast<uint16_t*>(smem);   // [rows][SK]
     uint16_t* KV = Qs + kTR * SK;                         // [2 stages][K, V][64][SK]
     __shared__ int last_flag;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tq = lane & 3;
@@ -86,17 +90,24 @@ __global__ void __launch_bounds__(kTThreads) paged_tile_kernel(const PagedAttnAr
     if (split >= of) return;
     const int i0 = (int)((long long)kb.total * split / of), i1 = (int)((long long)kb.total * (split + 1) / of);
 
+    unsigned mapped_next = 0;   // of the block loaded last: 16-key groups whose page is mapped
     auto load = [&](int i) {
+        mapped_next = 0;
         if (i < i1) {
             const int t0 = kb.block(i) * kTK;
             uint16_t* Ks = KV + (i & 1) * 2 * kTK * SK;
             uint16_t* Vs = Ks + kTK * SK;
-            for (int idx = tid; idx < kTK * CH; idx += kTThreads) {
-                const int r = idx / CH, c = idx % CH, t = t0 + r;
-                const int e = t <= p_hi ? page_of(a.c, o.s, t >> a.c.page_shift) : -1;
-                const size_t from = (((size_t)max(e, 0) * a.c.Hk + j) * a.c.page + (t & (a.c.page - 1))) * DH + c * 8;
-                cp_async16(Ks + r * SK + c * 8, a.c.k + from, e >= 0);
-                cp_async16(Vs + r * SK + c * 8, a.c.v + from, e >= 0);
+            int mine = -1;   // lane u: the page of the block's u-th 16 keys
+            if (lane < kTK / 16 && t0 + 16 * lane <= p_hi) mine = page_of(a.c, o.s, (t0 + 16 * lane) >> a.c.page_shift);
+            mapped_next = __ballot_sync(0xffffffffu, mine >= 0);
+#pragma unroll
+            for (int k = 0; k < kTK * CH / kTThreads; ++k) {
+                const int idx = tid + k * kTThreads, r = idx / CH, c = idx % CH, t = t0 + r;
+                const int page = __shfl_sync(0xffffffffu, mine, r / 16);
+                const bool in = page >= 0 && t <= p_hi;
+                const size_t from = (((size_t)max(page, 0) * a.c.Hk + j) * a.c.page + (t & (a.c.page - 1))) * DH + c * 8;
+                cp_async16(Ks + r * SK + c * 8, a.c.k + from, in);
+                cp_async16(Vs + r * SK + c * 8, a.c.v + from, in);
             }
         }
         cp_async_commit();
@@ -117,19 +128,13 @@ __global__ void __launch_bounds__(kTThreads) paged_tile_kernel(const PagedAttnAr
     const int mi = lane >> 3, lr = lane & 7;
 
     for (int i = i0; i < i1; ++i) {
+        const unsigned mapped = mapped_next;
         load(i + 1);
         cp_async_wait<1>();
         __syncthreads();
         const int t0 = kb.block(i) * kTK;
         uint16_t* Ks = KV + (i & 1) * 2 * kTK * SK;
         uint16_t* Vs = Ks + kTK * SK;
-        // 16-key groups whose page is mapped
-        unsigned mapped = 0;
-#pragma unroll
-        for (int u = 0; u < kTK / 16; ++u) {
-            const int t = t0 + 16 * u;
-            if (t <= p_hi && page_of(a.c, o.s, t >> a.c.page_shift) >= 0) mapped |= 1u << u;
-        }
         const bool whole = mapped == (1u << (kTK / 16)) - 1u && t0 + kTK - 1 <= p_lo &&
                            (a.c.window == 0 || t0 > p_hi - a.c.window || t0 + kTK - 1 < a.c.sinks);
         float s[kTK / 8][4];
@@ -247,7 +252,7 @@ __global__ void __launch_bounds__(kTThreads) paged_tile_kernel(const PagedAttnAr
         }
         return;
     }
-    // a split's record: [64][DH] sums, then [64] maxima and [64] sums of weights
+    // a split's record: [rows][DH] sums, then [rows] maxima and [rows] sums of weights
     const int unit = blockIdx.x * gridDim.y + j;
     constexpr int REC = kTR * (DH + 2);
     float* rec = a.partial + ((size_t)unit * splits + split) * REC;
@@ -272,7 +277,7 @@ __global__ void __launch_bounds__(kTThreads) paged_tile_kernel(const PagedAttnAr
     if (!last_flag) return;
     __threadfence();
     const float* all = a.partial + (size_t)unit * splits * REC;
-    float* factor = reinterpret_cast<float*>(smem);   // [of][64], where the rows of Q, K and V were
+    float* factor = reinterpret_cast<float*>(smem);   // [of][rows], where the rows of Q, K and V were
     const int rows = min(kTR, n_rows - r0);
     if (tid < rows) {
         const float* x = all + kTR * DH + tid;
@@ -310,27 +315,39 @@ __global__ void __launch_bounds__(kTThreads) paged_tile_kernel(const PagedAttnAr
     }
 }
 
-template <int DH, bool F16>
+template <int DH, bool F16, int ROWS>
 static cudaError_t launch_tiles_t(const PagedAttnArgs& a, cudaStream_t s) {
-    auto kern = paged_tile_kernel<DH, F16>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)tile_smem_bytes<DH>());
+    using S = TileShape<DH, ROWS>;
+    auto kern = paged_tile_kernel<DH, F16, ROWS>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::BYTES);
     if (e != cudaSuccess) return e;
     const long long G = a.c.Hq / a.c.Hk;
     // at most: every session's last tile may be part-filled
-    const long long tiles = a.cu_rows ? (a.rows * G + kTR - 1) / kTR + a.batch : a.batch * ((G + kTR - 1) / kTR);
-    const long long units = tiles * a.c.Hk, most = 2LL * a.num_sms;
+    const long long tiles = a.cu_rows ? (a.rows * G + ROWS - 1) / ROWS + a.batch : a.batch * ((G + ROWS - 1) / ROWS);
+    // two CTAs on each SM, or one of twice the rows; the join's factors fit where the tile's operands were
+    const long long units = tiles * a.c.Hk, most = 128LL * a.num_sms / ROWS;
+    static_assert(S::BYTES >= (size_t)64 * ROWS * 4, "room for the factors of 64 splits");
     const int splits = units < most ? (int)(most / units < 64 ? most / units : 64) : 1;
     if (tiles > INT32_MAX || a.c.Hk > 65535) return cudaErrorInvalidValue;
-    kern<<<dim3((unsigned)tiles, (unsigned)a.c.Hk, (unsigned)splits), kTThreads, tile_smem_bytes<DH>(), s>>>(a, splits);
+    kern<<<dim3((unsigned)tiles, (unsigned)a.c.Hk, (unsigned)splits), S::THREADS, S::BYTES, s>>>(a, splits);
     return cudaGetLastError();
+}
+
+template <int DH, int ROWS = 64>
+static cudaError_t launch_tiles(const PagedAttnArgs& a, cudaStream_t s) {
+    return a.f16 ? launch_tiles_t<DH, true, ROWS>(a, s) : launch_tiles_t<DH, false, ROWS>(a, s);
 }
 
 cudaError_t launch_paged_tiles(const PagedAttnArgs& a, cudaStream_t s) {
     switch (a.c.Dh) {
-        case 32: return a.f16 ? launch_tiles_t<32, true>(a, s) : launch_tiles_t<32, false>(a, s);
-        case 64: return a.f16 ? launch_tiles_t<64, true>(a, s) : launch_tiles_t<64, false>(a, s);
-        case 128: return a.f16 ? launch_tiles_t<128, true>(a, s) : launch_tiles_t<128, false>(a, s);
-        case 256: return a.f16 ? launch_tiles_t<256, true>(a, s) : launch_tiles_t<256, false>(a, s);
+        case 32: return launch_tiles<32>(a, s);
+        case 64: return launch_tiles<64>(a, s);
+        case 128: return launch_tiles<128>(a, s);
+        case 256:
+            // one CTA fills an SM's shared memory: 128 rows where the sessions have them (8 heads over 4, 16 sessions of
+            // 300 rows behind 1000 positions: 318 us for 388; one of 40 rows behind 16000: 117 for 142), 64 where they
+            // have not (30 rows behind 30000: 157 for 171; 4 sessions of 2 rows: 16.8 for 18.4)
+            return (long long)a.rows * (a.c.Hq / a.c.Hk) > 64LL * a.batch ? launch_tiles<256, 128>(a, s) : launch_tiles<256>(a, s);
     }
     return cudaErrorInvalidValue;
 }
