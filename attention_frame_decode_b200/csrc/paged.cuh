@@ -18,7 +18,7 @@ struct PagedKv {
 struct PagedWorkspace {
     int* head;        // [0] copies listed by a resize or fork, [1], [2] a compaction's moves and live pages
     int* ticket;      // work handed out by attention (zero between calls)
-    int* merge;       // arrival counters of split attention work [kMergeCounters] (zero between calls)
+    int* merge;       // arrival counters of split attention work [kMaxSplitCtas] (zero between calls)
     int* copies;      // [seqs][3]: source page, destination page, positions to copy
     int* ok;          // [seqs]: rows of a fork that are done
     int* first;       // [seqs]: the lowest row that names a session
@@ -66,6 +66,18 @@ cudaError_t paged_attend(const vc_paged_kv& kv, int layer, PagedAttnArgs a, cuda
 // rows of a fused projection [q | k | v] of ld elements a row, 1 / sqrt(Dh), results of out_ld elements a row
 PagedAttnArgs paged_rows(const uint16_t* qkv, int ld, int Hq, int Hk, int Dh, uint16_t* out, int out_ld, int widen);
 
+// joins the records of tiles of attention whose key blocks were split over CTAs
+struct JoinShape {
+    int rows, tile_rows;     // of a record; packed rows of a tile (tiles of prompts hold whole tokens)
+    int keys;                // of a block
+    int most_tiles, ctas;    // as the launch before was given them
+};
+// whether a row may see so many keys that joins take a launch of their own.  (8 heads of 64 over 32, 30 rows behind 30000
+// positions: 57 us for 73; 4 sessions of 2 rows behind 107: 17.7 for 12.0)
+inline bool many_keys(const PagedAttnArgs& a) {
+    return (a.c.window > 0 ? (long long)a.c.window + a.c.sinks + a.rows : (long long)a.c.columns * a.c.page) > 8192;
+}
+cudaError_t launch_paged_join(const PagedAttnArgs& a, const JoinShape& w, cudaStream_t s);
 cudaError_t launch_paged_append(const PagedAttnArgs& a, cudaStream_t s);
 cudaError_t launch_paged_tiles(const PagedAttnArgs& a, cudaStream_t s);
 // the tensor-core form for many rows; cudaErrorNotSupported: the shape is not covered

@@ -64,23 +64,24 @@ struct TileShape {
 };
 
 template <int DH, bool F16, int ROWS>
-__global__ void __launch_bounds__(TileShape<DH, ROWS>::THREADS) paged_tile_kernel(const PagedAttnArgs a, int splits) {
+__global__ void __launch_bounds__(TileShape<DH, ROWS>::THREADS) paged_tile_kernel(const PagedAttnArgs a, int most_tiles, int ctas, bool join_later) {
     constexpr int kTR = ROWS, kTThreads = TileShape<DH, ROWS>::THREADS;
     constexpr int SK = DH + 8, CH = DH / 8, NT = DH / 8;
     extern __shared__ __align__(16) uint8_t smem[];
     uint16_t* Qs = reinterpret_cast<uint16_t*>(smem);   // [rows][SK]
     uint16_t* KV = Qs + kTR * SK;                         // [2 stages][K, V][64][SK]
-    __shared__ int last_flag;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tq = lane & 3;
-    const int G = a.c.Hq / a.c.Hk, j = blockIdx.y, split = blockIdx.z;
+    const int G = a.c.Hq / a.c.Hk;
 
     int session, tile;
-    if (blockIdx.x == 0 && j == 0 && split == 0)   // reports every session whose indices do not fit
+    if (blockIdx.x == 0)   // reports every session whose indices do not fit
         for (int i = tid; i < a.batch; i += kTThreads) {
             AttnSession o;
             attn_session(a, i, o);
         }
-    if (!find_tile(a, G, kTR, blockIdx.x, session, tile)) return;
+    const int tiles = count_tiles(a, G, kTR, most_tiles), units = tiles * a.c.Hk, splits = ctas ? unit_splits(units, ctas) : 1;
+    const int unit = (int)blockIdx.x / splits, split = (int)blockIdx.x % splits, j = unit % a.c.Hk;
+    if (unit >= units || !find_tile(a, G, kTR, tiles - 1 - unit / a.c.Hk, session, tile)) return;   // the longest rows first
     AttnSession o;
     if (!attn_session(a, session, o)) return;
     const int n_rows = o.n * G, r0 = tile * kTR;
@@ -253,7 +254,6 @@ __global__ void __launch_bounds__(TileShape<DH, ROWS>::THREADS) paged_tile_kerne
         return;
     }
     // a split's record: [rows][DH] sums, then [rows] maxima and [rows] sums of weights
-    const int unit = blockIdx.x * gridDim.y + j;
     constexpr int REC = kTR * (DH + 2);
     float* rec = a.partial + ((size_t)unit * splits + split) * REC;
 #pragma unroll
@@ -267,52 +267,65 @@ __global__ void __launch_bounds__(TileShape<DH, ROWS>::THREADS) paged_tile_kerne
             rec[kTR * DH + kTR + r] = l[h];
         }
     }
-    __threadfence();
-    __syncthreads();
-    if (tid == 0) {
-        last_flag = atomicAdd(a.merge + unit, 1) == of - 1;
-        if (last_flag) a.merge[unit] = 0;
+    if (join_later || !last_to_arrive(a.merge + unit, of)) return;
+    join_records<DH, F16, kTThreads>(a, a.partial + (size_t)unit * splits * REC, kTR, of, 0, min(kTR, n_rows - r0),
+                                     reinterpret_cast<float*>(smem), [&](int r) { return out_row(r0 + r); });
+}
+
+// ------------------------------------------------------------------------------------------
+// joins as a launch of their own, 16 rows a CTA, for caches that may hold many keys: every SM reads records (by the last
+// CTA of a tile to arrive, 37 records of 64 rows of 256 took 100 us).  Where there cannot be many, the last CTA to arrive
+// joins: the launch takes 2 to 5 us.
+// ------------------------------------------------------------------------------------------
+static constexpr int kJRows = 16, kJThreads = 128;
+
+template <int DH, bool F16, int BK>
+__global__ void __launch_bounds__(kJThreads) paged_join_kernel(const PagedAttnArgs a, const JoinShape w) {
+    __shared__ float factor[kMostSplits * kJRows];
+    pdl_trigger();
+    pdl_wait();
+    const int G = a.c.Hq / a.c.Hk, unit = blockIdx.x, j = unit % a.c.Hk;
+    const int tiles = count_tiles(a, G, w.tile_rows, w.most_tiles), units = tiles * a.c.Hk, splits = unit_splits(units, w.ctas);
+    int session, tile;
+    AttnSession o;
+    if (unit >= units || !find_tile(a, G, w.tile_rows, tiles - 1 - unit / a.c.Hk, session, tile) || !attn_session(a, session, o))
+        return;
+    const int r0 = tile * w.tile_rows, r1 = min(r0 + w.tile_rows, o.n * G), first = blockIdx.y * kJRows;
+    const int rows = min(kJRows, r1 - r0 - first);
+    const KeyBlocks kb = key_blocks<BK>(a.c.window, a.c.sinks, o.p0 + r0 / G, o.p0 + (r1 - 1) / G);
+    const int of = key_splits(kb.total, splits);
+    if (rows <= 0 || of == 1) return;
+    join_records<DH, F16, kJThreads>(a, a.partial + (size_t)unit * splits * (w.rows * (DH + 2)), w.rows, of, first, rows, factor, [&](int r) {
+        const int packed = r0 + first + r;
+        return a.out + (size_t)(o.row0 + packed / G) * a.out_ld + (size_t)(j * G + packed % G) * DH;
+    });
+}
+
+template <int DH, int BK>
+static cudaError_t launch_join_t(const PagedAttnArgs& a, const JoinShape& w, cudaStream_t s) {
+    // units that may be split: the others are as many as half of the CTAs, or more
+    const long long units = (long long)w.most_tiles * a.c.Hk, most = w.ctas / 2;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(units < most ? units : most), (unsigned)((w.rows + kJRows - 1) / kJRows));
+    cfg.blockDim = dim3(kJThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return a.f16 ? cudaLaunchKernelEx(&cfg, paged_join_kernel<DH, true, BK>, a, w)
+                 : cudaLaunchKernelEx(&cfg, paged_join_kernel<DH, false, BK>, a, w);
+}
+
+cudaError_t launch_paged_join(const PagedAttnArgs& a, const JoinShape& w, cudaStream_t s) {
+    switch (a.c.Dh) {
+        case 32: return launch_join_t<32, 64>(a, w, s);
+        case 64: return launch_join_t<64, 64>(a, w, s);
+        case 128: return w.keys == 64 ? launch_join_t<128, 64>(a, w, s) : launch_join_t<128, 128>(a, w, s);
+        case 256: return launch_join_t<256, 64>(a, w, s);
     }
-    __syncthreads();
-    if (!last_flag) return;
-    __threadfence();
-    const float* all = a.partial + (size_t)unit * splits * REC;
-    float* factor = reinterpret_cast<float*>(smem);   // [of][rows], where the rows of Q, K and V were
-    const int rows = min(kTR, n_rows - r0);
-    if (tid < rows) {
-        const float* x = all + kTR * DH + tid;
-        float top = -INFINITY, sum = 0.0f;
-#pragma unroll 8
-        for (int sp = 0; sp < of; ++sp) {
-            const float t = __ldcg(x + (size_t)sp * REC);
-            factor[sp * kTR + tid] = t;
-            top = fmaxf(top, t);
-        }
-        if (top == -INFINITY) top = 0.0f;
-#pragma unroll 8
-        for (int sp = 0; sp < of; ++sp) {   // a split that saw nothing for this row: maximum -inf, factor 0, sums 0
-            const float f = exp2_approx(factor[sp * kTR + tid] - top);
-            factor[sp * kTR + tid] = f;
-            sum = fmaf(__ldcg(x + (size_t)sp * REC + kTR), f, sum);
-        }
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-        for (int sp = 0; sp < of; ++sp) factor[sp * kTR + tid] *= inv;
-    }
-    __syncthreads();
-#pragma unroll 2
-    for (int idx = tid; idx < rows * (DH / 4); idx += kTThreads) {
-        const int r = idx / (DH / 4), d = 4 * (idx % (DH / 4));
-        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 8
-        for (int sp = 0; sp < of; ++sp) {
-            const float w = factor[sp * kTR + r];
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(all + (size_t)sp * REC + r * DH + d));
-            v[0] = fmaf(x.x, w, v[0]); v[1] = fmaf(x.y, w, v[1]);
-            v[2] = fmaf(x.z, w, v[2]); v[3] = fmaf(x.w, w, v[3]);
-        }
-        *reinterpret_cast<uint2*>(out_row(r0 + r) + d) =
-            make_uint2(pack_out<F16>(a.widen, v[0], v[1]), pack_out<F16>(a.widen, v[2], v[3]));
-    }
+    return cudaErrorInvalidValue;
 }
 
 template <int DH, bool F16, int ROWS>
@@ -324,13 +337,17 @@ static cudaError_t launch_tiles_t(const PagedAttnArgs& a, cudaStream_t s) {
     const long long G = a.c.Hq / a.c.Hk;
     // at most: every session's last tile may be part-filled
     const long long tiles = a.cu_rows ? (a.rows * G + ROWS - 1) / ROWS + a.batch : a.batch * ((G + ROWS - 1) / ROWS);
-    // two CTAs on each SM, or one of twice the rows; the join's factors fit where the tile's operands were
-    const long long units = tiles * a.c.Hk, most = 128LL * a.num_sms / ROWS;
-    static_assert(S::BYTES >= (size_t)64 * ROWS * 4, "room for the factors of 64 splits");
-    const int splits = units < most ? (int)(most / units < 64 ? most / units : 64) : 1;
-    if (tiles > INT32_MAX || a.c.Hk > 65535) return cudaErrorInvalidValue;
-    kern<<<dim3((unsigned)tiles, (unsigned)a.c.Hk, (unsigned)splits), S::THREADS, S::BYTES, s>>>(a, splits);
-    return cudaGetLastError();
+    const long long units = tiles * a.c.Hk;
+    if (units > INT32_MAX) return cudaErrorInvalidValue;
+    // the key blocks are split where that gives more SMs work: two CTAs on each, one at head dim 256
+    const int ctas = a.num_sms * (DH == 256 ? 1 : 2);
+    const long long least = a.cu_rows ? (a.rows * G + ROWS - 1) / ROWS : tiles;
+    const bool may_split = least * a.c.Hk * 2 <= ctas, join_later = may_split && many_keys(a);
+    static_assert(S::BYTES >= (size_t)kMostSplits * ROWS * 4, "room for the join's factors");
+    kern<<<(unsigned)(may_split && units < ctas ? ctas : units), S::THREADS, S::BYTES, s>>>(a, (int)tiles, may_split ? ctas : 0,
+                                                                                         join_later);
+    e = cudaGetLastError();
+    return e == cudaSuccess && join_later ? launch_paged_join(a, JoinShape{ROWS, ROWS, kTK, (int)tiles, ctas}, s) : e;
 }
 
 template <int DH, int ROWS = 64>

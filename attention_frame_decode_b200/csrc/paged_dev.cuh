@@ -156,9 +156,123 @@ VC_DEV KeyBlocks key_blocks(int window, int sinks, int p_lo, int p_hi) {
     return k;
 }
 
-// into how many ranges a tile's key blocks are split: at most `splits`, and two blocks or more in each (a record and its
-// join take about as long)
+// how many tiles the sessions' rows make (a whole warp calls): at most `most`, as the launch counted them from the rows
+// and sessions (more only where cu_rows overlap; those sessions are refused)
+VC_DEV int count_tiles(const PagedAttnArgs& a, int group, int tile_rows, int most) {
+    long long n = 0;
+    for (int b = threadIdx.x & 31; b < a.batch; b += 32) n += ((long long)session_rows(a, b) * group + tile_rows - 1) / tile_rows;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+    return (int)min(n, (long long)most);
+}
+
+// units of work (a tile and a KV head) of which a launch has fewer than CTAs: how many CTAs each gets at most ...
+static constexpr int kMostSplits = 64;
+VC_DEV int unit_splits(int units, int ctas) { return max(min(ctas / max(units, 1), kMostSplits), 1); }
+// ... and into how many ranges its key blocks are split: two blocks or more in each (a record and its join take as long)
 VC_DEV int key_splits(int blocks, int splits) { return max(min(splits, blocks / 2), 1); }
+
+template <int N>
+struct Count {
+    static constexpr int value = N;
+};
+
+// a CTA's record of a unit is written: whether it was the last of `of` (all threads call)
+VC_DEV bool last_to_arrive(int* counter, int of) {
+    __shared__ int last;
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        last = atomicAdd(counter, 1) == of - 1;
+        if (last) *counter = 0;
+    }
+    __syncthreads();
+    __threadfence();
+    return last != 0;
+}
+
+// Joins, in split order, the records of a unit whose key blocks were split into `of` ranges: rows first .. first + rows - 1
+// of the tile, by all THREADS threads of the CTA.  A record: sums [rec_rows][DH], maxima and sums of weights [rec_rows],
+// each under its own maximum; out(r): where row first + r goes; factor: room for [of][rows].
+template <int DH, bool F16, int THREADS, class Out>
+VC_DEV void join_records(const PagedAttnArgs& a, const float* all, int rec_rows, int of, int first, int rows, float* factor, Out out) {
+    const int tid = threadIdx.x, rec = rec_rows * (DH + 2);
+    const float* tops = all + rec_rows * DH + first;   // a split that saw nothing: maximum -inf, factor 0, sums 0
+    if (of <= 4) {   // a thread a row
+        for (int q = tid; q < rows; q += THREADS) {
+            float t[4], l[4], top = -INFINITY, sum = 0.0f;
+#pragma unroll
+            for (int sp = 0; sp < 4; ++sp) {
+                t[sp] = sp < of ? __ldcg(tops + (size_t)sp * rec + q) : -INFINITY;
+                l[sp] = sp < of ? __ldcg(tops + (size_t)sp * rec + rec_rows + q) : 0.0f;
+            }
+#pragma unroll
+            for (int sp = 0; sp < 4; ++sp) top = fmaxf(top, t[sp]);
+            if (top == -INFINITY) top = 0.0f;
+#pragma unroll
+            for (int sp = 0; sp < 4; ++sp) {
+                t[sp] = exp2_approx(t[sp] - top);
+                sum = fmaf(l[sp], t[sp], sum);
+            }
+            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+            for (int sp = 0; sp < 4; ++sp)
+                if (sp < of) factor[sp * rows + q] = t[sp] * inv;
+        }
+    } else {   // eight threads a row
+        for (int q = tid / 8; q < rows; q += THREADS / 8) {
+            const unsigned lanes = 0xffu << (tid & 24);
+            float top = -INFINITY, sum = 0.0f;
+            for (int sp = tid % 8; sp < of; sp += 8) {
+                factor[sp * rows + q] = __ldcg(tops + (size_t)sp * rec + q);
+                top = fmaxf(top, factor[sp * rows + q]);
+            }
+#pragma unroll
+            for (int m = 1; m < 8; m <<= 1) top = fmaxf(top, __shfl_xor_sync(lanes, top, m));
+            if (top == -INFINITY) top = 0.0f;
+            for (int sp = tid % 8; sp < of; sp += 8) {
+                factor[sp * rows + q] = exp2_approx(factor[sp * rows + q] - top);
+                sum = fmaf(__ldcg(tops + (size_t)sp * rec + rec_rows + q), factor[sp * rows + q], sum);
+            }
+#pragma unroll
+            for (int m = 1; m < 8; m <<= 1) sum += __shfl_xor_sync(lanes, sum, m);
+            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+            for (int sp = tid % 8; sp < of; sp += 8) factor[sp * rows + q] *= inv;
+        }
+    }
+    __syncthreads();
+    // few ranges: four pieces of a row a thread at a time; many: one, and eight ranges of it (what counts is loads in flight)
+    const int total = rows * (DH / 4);
+    auto gather = [&](auto pieces, auto ranges) {
+        constexpr int U = decltype(pieces)::value, N = decltype(ranges)::value;
+        for (int base = tid; base < total; base += U * THREADS) {
+            float4 v[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) v[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll N
+            for (int sp = 0; sp < of; ++sp) {
+                const float4* from = reinterpret_cast<const float4*>(all + (size_t)sp * rec + first * DH);
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int idx = min(base + u * THREADS, total - 1);
+                    const float f = factor[sp * rows + idx / (DH / 4)];
+                    const float4 x = __ldcg(from + idx);
+                    v[u].x = fmaf(x.x, f, v[u].x); v[u].y = fmaf(x.y, f, v[u].y);
+                    v[u].z = fmaf(x.z, f, v[u].z); v[u].w = fmaf(x.w, f, v[u].w);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int idx = base + u * THREADS;
+                if (idx < total)
+                    *reinterpret_cast<uint2*>(out(idx / (DH / 4)) + 4 * (idx % (DH / 4))) =
+                        make_uint2(pack_out<F16>(a.widen, v[u].x, v[u].y), pack_out<F16>(a.widen, v[u].z, v[u].w));
+            }
+        }
+    };
+    if (of <= 4) gather(Count<4>{}, Count<2>{});
+    else gather(Count<1>{}, Count<8>{});
+}
 
 // the session and the tile within it of the launch's `tile`-th tile; false behind the last (a whole warp calls)
 VC_DEV bool find_tile(const PagedAttnArgs& a, int group, int tile_rows, int tile, int& session, int& t) {

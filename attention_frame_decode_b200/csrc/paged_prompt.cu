@@ -154,7 +154,8 @@ struct PromptWork {
     int b0, nb;
     int s, row0, n_rows;     // the session's index and first row; its packed rows
     int r0, r1, p0;          // the tile's packed rows r0 .. r1 - 1; the position of the session's first row
-    int p_lo, p_hi, j, unit, split, of;   // of: into how many pieces the tile is split
+    int p_lo, p_hi, j;
+    int splits, of, record;  // the launch's pieces of a tile; how many of them have blocks; this piece's record
 };
 
 // piece `item` of the launch (a whole warp calls); nb is 0 where there is nothing to do, and n_rows too where not even
@@ -167,13 +168,14 @@ VC_DEV PromptWork prompt_work(const PagedAttnArgs& a, int tiles, int splits, int
         w.nb = -1;
         return w;
     }
-    w.split = item % splits;
-    w.unit = item / splits;
-    w.j = w.unit % a.c.Hk;
+    const int unit = item / splits, split = item % splits;
+    w.record = item;
+    w.splits = splits;
+    w.j = unit % a.c.Hk;
     int session, tile;
     AttnSession o;
     // the longest rows first
-    if (!find_tile(a, G, tile_rows, tiles - 1 - w.unit / a.c.Hk, session, tile) || !attn_session(a, session, o)) return w;
+    if (!find_tile(a, G, tile_rows, tiles - 1 - unit / a.c.Hk, session, tile) || !attn_session(a, session, o)) return w;
     w.s = o.s;
     w.row0 = o.row0;
     w.n_rows = o.n * G;
@@ -184,18 +186,19 @@ VC_DEV PromptWork prompt_work(const PagedAttnArgs& a, int tiles, int splits, int
     w.p_hi = o.p0 + (w.r1 - 1) / G;
     w.kb = key_blocks<S::KEYS>(a.c.window, a.c.sinks, w.p_lo, w.p_hi);
     w.of = key_splits(w.kb.total, splits);
-    if (w.split >= w.of) {   // nothing left for it
+    if (split >= w.of) {   // nothing left for it
         w.n_rows = w.r1 = 0;
         return w;
     }
-    w.b0 = (int)((long long)w.kb.total * w.split / w.of);
-    w.nb = (int)((long long)w.kb.total * (w.split + 1) / w.of) - w.b0;
+    w.b0 = (int)((long long)w.kb.total * split / w.of);
+    w.nb = (int)((long long)w.kb.total * (split + 1) / w.of) - w.b0;
     return w;
 }
 
 template <int DH, bool F16>
 __global__ void __launch_bounds__(kPThreads, 1)
-    paged_prompt_kernel(const __grid_constant__ PromptMaps maps, const PagedAttnArgs a, int tiles, int splits) {
+    paged_prompt_kernel(const __grid_constant__ PromptMaps maps, const PagedAttnArgs a, int most_tiles, bool may_split,
+                        bool join_later) {
     using S = PromptShape<DH>;
     constexpr int ST = S::STAGES;
     extern __shared__ uint8_t smem_raw[];
@@ -205,12 +208,12 @@ __global__ void __launch_bounds__(kPThreads, 1)
     __shared__ uint64_t full[ST], empty[ST], clean[ST / 2], work_ready[2], q_ready[2], q_free, o_free[2], drained;
     __shared__ uint64_t s_full[S::TILES], p_ready[S::TILES], o_done[S::TILES];
     __shared__ uint32_t tmem_base, block_mapped[16];   // of block g at g % 16: at most ST / 2 are in the ring
-    __shared__ int odd_values[4], last_flag;
+    __shared__ int odd_values[4];
     __shared__ PromptWork work[4];       // piece t at t % 4: written again when the rows are done with it
     __shared__ float top_x[S::ROWS], l_part[S::SHARES][S::ROWS];   // a row's highest score, between its threads; their sums
 
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-    const int G = a.c.Hq / a.c.Hk, items = tiles * a.c.Hk * splits;   // pieces
+    const int G = a.c.Hq / a.c.Hk, most = most_tiles * a.c.Hk + (int)gridDim.x;   // pieces at most
     pdl_trigger();
     if (tid == 0) {
         tma_prefetch_map(&maps.q);
@@ -265,7 +268,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             // ---- copies: K of a block, V of the block, K of the next, ... in ring order ----
             const int box_rows = min(a.c.page, S::KEYS), boxes = S::KEYS / box_rows;
             int issued = 0;
-            for (int t = 0; t <= items && ok; ++t) {
+            for (int t = 0; t <= most && ok; ++t) {
                 wait(&work_ready[t & 1], t >> 1);
                 const PromptWork w = work[t & 3];
                 if (w.nb < 0) break;
@@ -337,7 +340,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             int g = 0, gi[S::TILES];   // blocks so far, and those that a tile had rows for
 #pragma unroll
             for (int i = 0; i < S::TILES; ++i) gi[i] = 0;
-            for (int t = 0; t <= items; ++t) {
+            for (int t = 0; t <= most; ++t) {
                 hold(&q_ready[t & 1], t >> 1);
                 const int nb = __shfl_sync(0xffffffffu, work[t & 3].nb, 0);
                 const int used = __shfl_sync(0xffffffffu, (work[t & 3].r1 - work[t & 3].r0 + 127) >> 7, 0);   // tiles with rows
@@ -395,7 +398,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
             }
         } else if (warp == 2) {
             // ---- the pieces, handed out as CTAs come for them (the first by index), and their rows of Q ----
-            for (int t = 0; t <= items; ++t) {
+            const int tiles = count_tiles(a, G, S::ROWS / G * G, most_tiles), units = tiles * a.c.Hk;
+            const int splits = may_split ? unit_splits(units, (int)gridDim.x) : 1, items = units * splits;
+            for (int t = 0; t <= most; ++t) {
                 int item = blockIdx.x;
                 if (t > 0) {
                     if (lane == 0) {
@@ -430,7 +435,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             // ---- values that not every row of the tile sees: those that no row sees become 0, and so do infinities and
             // NaN (the rows that see them get them at the end), so that a weight of 0 takes nothing in ----
             int g = 0;
-            for (int t = 0; t <= items; ++t) {
+            for (int t = 0; t <= most; ++t) {
                 wait(&q_ready[t & 1], t >> 1);
                 const PromptWork w = work[t & 3];
                 if (w.nb < 0) break;
@@ -495,7 +500,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         const float2 by = make_float2(a.scale_log2, a.scale_log2);
         int gi = 0;   // blocks so far for this tile
         int g = 0;
-        for (int t = 0; t <= items; ++t) {
+        for (int t = 0; t <= most; ++t) {
             wait(&q_ready[t & 1], t >> 1);
             const PromptWork& w = work[t & 3];
             const int n_all = w.nb, r = w.r0 + i * 128 + rr;
@@ -614,7 +619,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             for (int u = 0; u < 4; ++u) to[u] = __shfl_sync(0xffffffffu, mine, (lane & ~3) + u);
             const int of = w.of;
             const float inv = of > 1 ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
-            float* rec = a.partial + ((size_t)w.unit * splits + w.split) * (S::ROWS * (DH + 2));
+            float* rec = a.partial + (size_t)w.record * (S::ROWS * (DH + 2));
             if (nb > 0) {
                 wait(&o_done[i], gi - 1);
                 tc_fence_after();
@@ -684,58 +689,14 @@ __global__ void __launch_bounds__(kPThreads, 1)
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
-    if (splits == 1) return;
-
-    // ---- the last split of the tile to arrive joins them in order (a CTA has one piece where tiles are split) ----
-    const PromptWork& w = work[0];
-    if (w.n_rows == 0 || w.of == 1) return;
-    const int of = w.of;
-    if (tid == 0) {
-        __threadfence();   // the CTA's record, ordered by the barrier, before its arrival
-        last_flag = atomicAdd(a.merge + w.unit, 1) == of - 1;
-        if (last_flag) a.merge[w.unit] = 0;
-        __threadfence();
-    }
-    __syncthreads();
-    if (!last_flag) return;
-    constexpr int REC = S::ROWS * (DH + 2);
-    const float* all = a.partial + (size_t)w.unit * splits * REC;
-    float* factor = reinterpret_cast<float*>(smem);   // [of][ROWS], where the rows of Q and the ring were
-    const int n_rows = w.r1 - w.r0;
-    for (int r = tid; r < n_rows; r += kPThreads) {
-        const float* x = all + S::ROWS * DH + r;   // a split that saw nothing: maximum -inf, factor 0, sums 0
-        float top = -INFINITY, sum = 0.0f;
-#pragma unroll 8
-        for (int sp = 0; sp < of; ++sp) {
-            const float t = __ldcg(x + (size_t)sp * REC);
-            factor[sp * S::ROWS + r] = t;
-            top = fmaxf(top, t);
-        }
-        if (top == -INFINITY) top = 0.0f;
-#pragma unroll 8
-        for (int sp = 0; sp < of; ++sp) {
-            const float f = exp2_approx(factor[sp * S::ROWS + r] - top);
-            factor[sp * S::ROWS + r] = f;
-            sum = fmaf(__ldcg(x + (size_t)sp * REC + S::ROWS), f, sum);
-        }
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-        for (int sp = 0; sp < of; ++sp) factor[sp * S::ROWS + r] *= inv;
-    }
-    __syncthreads();
-    for (int idx = tid; idx < n_rows * (DH / 4); idx += kPThreads) {
-        const int r = idx / (DH / 4), d = 4 * (idx % (DH / 4));
-        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 8
-        for (int sp = 0; sp < of; ++sp) {
-            const float f = factor[sp * S::ROWS + r];
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(all + (size_t)sp * REC + r * DH + d));
-            v[0] = fmaf(x.x, f, v[0]); v[1] = fmaf(x.y, f, v[1]);
-            v[2] = fmaf(x.z, f, v[2]); v[3] = fmaf(x.w, f, v[3]);
-        }
-        uint16_t* to = a.out + (size_t)(w.row0 + (w.r0 + r) / G) * a.out_ld + (size_t)(w.j * G + (w.r0 + r) % G) * DH + d;
-        *reinterpret_cast<uint2*>(to) =
-            make_uint2(pack_out<F16>(a.widen, v[0], v[1]), pack_out<F16>(a.widen, v[2], v[3]));
-    }
+    const PromptWork& w = work[0];   // a CTA has one piece where tiles are split
+    if (!may_split || join_later || w.n_rows == 0 || w.of <= 1) return;
+    if (!last_to_arrive(a.merge + w.record / w.splits, w.of)) return;
+    const int first = w.row0 * G + w.r0;   // packed rows of the whole call
+    join_records<DH, F16, kPThreads>(a, a.partial + (size_t)(w.record - w.record % w.splits) * (S::ROWS * (DH + 2)), S::ROWS, w.of,
+                                     0, w.r1 - w.r0, reinterpret_cast<float*>(smem), [&](int r) {
+                                         return a.out + (size_t)((first + r) / G) * a.out_ld + (size_t)(w.j * G + (first + r) % G) * DH;
+                                     });
 }
 
 template <int DH, bool F16>
@@ -746,10 +707,10 @@ static cudaError_t launch_prompts_t(const PagedAttnArgs& a, cudaStream_t s) {
     // at most: every session's last tile may be part-filled
     const long long tile_rows = S::ROWS / G * G, tiles = (a.rows * G + tile_rows - 1) / tile_rows + a.batch,
                     units = tiles * a.c.Hk;
-    if (units > INT32_MAX) return cudaErrorNotSupported;
-    // (the join's factors take the room of the rows of Q and the ring)
-    constexpr int most = (S::BYTES - 1024) / (S::ROWS * 4) < 64 ? (S::BYTES - 1024) / (S::ROWS * 4) : 64;
-    const int splits = units < a.num_sms ? (int)(a.num_sms / units < most ? a.num_sms / units : most) : 1;
+    if (units > INT32_MAX - kMaxSms) return cudaErrorNotSupported;
+    // the key blocks are split where that gives more SMs work
+    const bool may_split = (a.rows * G + tile_rows - 1) / tile_rows * a.c.Hk * 2 <= a.num_sms, join_later = may_split && many_keys(a);
+    static_assert(S::BYTES - 1024 >= kMostSplits * S::ROWS * 4, "room for the join's factors");
     PromptMaps maps;
     const int rows = a.c.pages * a.c.Hk * a.c.page, box = a.c.page < S::KEYS ? a.c.page : S::KEYS;
     EncodeTiledFn encode = tma_encode_fn();
@@ -768,7 +729,7 @@ static cudaError_t launch_prompts_t(const PagedAttnArgs& a, cudaStream_t s) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::BYTES);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(units * splits < a.num_sms ? units * splits : a.num_sms));
+    cfg.gridDim = dim3((unsigned)(!may_split && units < a.num_sms ? units : a.num_sms));
     cfg.blockDim = dim3(kPThreads);
     cfg.dynamicSmemBytes = S::BYTES;
     cfg.stream = s;
@@ -777,7 +738,10 @@ static cudaError_t launch_prompts_t(const PagedAttnArgs& a, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, maps, a, (int)tiles, splits);
+    e = cudaLaunchKernelEx(&cfg, kern, maps, a, (int)tiles, may_split, join_later);
+    return e == cudaSuccess && join_later
+               ? launch_paged_join(a, JoinShape{S::ROWS, (int)tile_rows, S::KEYS, (int)tiles, a.num_sms}, s)
+               : e;
 }
 
 cudaError_t launch_paged_prompts(const PagedAttnArgs& a, cudaStream_t s) {
