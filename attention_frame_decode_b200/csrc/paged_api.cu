@@ -55,7 +55,9 @@ PagedKv paged_kernel_kv(const vc_paged_kv& c) {
     d.table = c.table; d.len = c.len; d.refs = c.refs; d.status = c.status;
     d.layers = c.layers; d.pages = c.pages; d.page = c.page_size; d.page_shift = __builtin_ctz((unsigned)c.page_size);
     d.Hk = c.kv_heads; d.Dh = c.head_dim; d.Hq = c.q_heads; d.seqs = c.seqs; d.columns = c.columns;
-    d.window = c.window; d.sinks = c.sinks;
+    // positions are below 2^30: a window or sinks of that many cover all, and differences of positions stay in 32 bits
+    d.window = c.window < (1 << 30) ? c.window : 1 << 30;
+    d.sinks = c.sinks < (1 << 30) ? c.sinks : 1 << 30;
     return d;
 }
 

@@ -14,6 +14,8 @@
 // order, so that results do not depend on timing.
 // The weights go into the products as a 16-bit value and the 16-bit rest of it: the error of a weight is
 // 2^-16 (bf16), and the products are not what this kernel waits for.
+#include <algorithm>
+
 #include "paged_dev.cuh"
 #include "tc.cuh"
 
@@ -615,7 +617,9 @@ static cudaError_t launch_frames_t(const PagedAttnArgs& a, cudaStream_t s) {
 cudaError_t launch_paged_frames(const PagedAttnArgs& a, cudaStream_t s) {
     // a line of units that 32 bits count, in blocks of at least 16 keys; up to 16 query heads to a KV head (the rows
     // of one matrix instruction); sessions that the line's table in shared memory holds
-    const long long most = (long long)a.c.columns * a.c.page / 16 + 2;
+    long long reach = (long long)a.c.columns * a.c.page;
+    if (a.c.window > 0) reach = std::min(reach, (long long)a.c.window + a.c.sinks);
+    const long long most = reach / 16 + 4;
     if (a.c.Hq / a.c.Hk > 16 || a.batch > kFMaxBatch || most * a.c.Hk * a.batch > INT32_MAX) return cudaErrorNotSupported;
     switch (a.c.Dh) {
         case 32: return a.f16 ? launch_frames_t<32, true>(a, s) : launch_frames_t<32, false>(a, s);

@@ -4,6 +4,8 @@
     python -m attention_frame_decode_b200.kernel_cases gemm --m 4096 --n 15680 --k 4480
     python -m attention_frame_decode_b200.kernel_cases ssd --frames 1024
     python -m attention_frame_decode_b200.kernel_cases attn --batch 16
+    python -m attention_frame_decode_b200.kernel_cases paged --batch 16
+    python -m attention_frame_decode_b200.kernel_cases paged --batch 1 --rows 4096 --ctx 0
 
 Each case builds its inputs on the device from the seeded generators, runs the kernel a few
 times, and prints the mean time of `--reps` further launches measured with CUDA events.  The
@@ -151,6 +153,35 @@ def case_attn(a):
     bb.close()
 
 
+def case_paged(a):
+    """attention over a paged cache with a window and sinks: `batch` sessions behind contexts of `ctx` positions, each
+    with `rows` new rows (1: the frames' form; more: the prompts'), Nano heads (40 over 8 of 128) or, at head dim 64,
+    32 over 8"""
+    import torch
+    import attention_frame_decode_b200 as vc
+    hq, hk, d, B, page = (40 if a.head_dim == 128 else 32), 8, a.head_dim, a.batch, 64
+    columns = -(-(a.ctx + a.rows) // page)
+    cache = vc.PagedCache.empty(layers=1, pages=B * columns, page_size=page, kv_heads=hk, head_dim=d, seqs=B, columns=columns,
+                                q_heads=hq, window=a.window, sinks=a.sinks)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    cache.k.normal_(generator=g)
+    cache.v.normal_(generator=g)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    pos = torch.empty(B, **i32)
+    cache.resize(lens=torch.full((B,), a.ctx, **i32))
+    cache.resize(add=a.rows, pos=pos)
+    qkv = torch.randn((B * a.rows, (hq + 2 * hk) * d), generator=g, device="cuda").to(torch.bfloat16)
+    q, k, v = (x.unflatten(1, (-1, d)) for x in qkv.split([hq * d, hk * d, hk * d], 1))
+    out = torch.empty((B * a.rows, hq, d), dtype=torch.bfloat16, device="cuda")
+    cu = None if a.rows == 1 else torch.arange(0, (B + 1) * a.rows, a.rows, **i32)
+    run = lambda: cache.attend(0, q, k, v, out, pos, cu_rows=cu)
+    for _ in range(a.warmup):
+        run()
+    us = _time(run, a.reps)
+    print(f"paged attention, {B} sessions, {a.rows} rows behind {a.ctx}, window {a.window}, sinks {a.sinks}, heads {hq} over "
+          f"{hk} of {d}: {us:.1f} us/call, status {int(cache.status)}")
+
+
 def main(argv=None):
     ap = argparse.ArgumentParser()
     sub = ap.add_subparsers(dest="case", required=True)
@@ -170,11 +201,19 @@ def main(argv=None):
     mb.add_argument("--batch", type=int, default=16)
     at = sub.add_parser("attn")
     at.add_argument("--batch", type=int, default=16)
-    for p in (g, m, s, mb, at):
+    pg = sub.add_parser("paged")
+    pg.add_argument("--batch", type=int, default=16)
+    pg.add_argument("--rows", type=int, default=1)
+    pg.add_argument("--ctx", type=int, default=4096)
+    pg.add_argument("--window", type=int, default=4096)
+    pg.add_argument("--sinks", type=int, default=64)
+    pg.add_argument("--head-dim", type=int, default=128, choices=(64, 128))
+    for p in (g, m, s, mb, at, pg):
         p.add_argument("--warmup", type=int, default=3)
         p.add_argument("--reps", type=int, default=20)
     a = ap.parse_args(argv)
-    {"gemv": case_gemv, "gemm": case_gemm, "ssd": case_ssd, "mamba": case_mamba, "attn": case_attn}[a.case](a)
+    {"gemv": case_gemv, "gemm": case_gemm, "ssd": case_ssd, "mamba": case_mamba, "attn": case_attn,
+     "paged": case_paged}[a.case](a)
 
 
 if __name__ == "__main__":

@@ -82,6 +82,19 @@ def test_scores_that_keep_rising(single, dtype, d, step):
     s.check(s.run(single=single), only=some(rows, 20))
 
 
+@pytest.mark.parametrize("heads", [(4, 2, 64), (4, 2, 128), (4, 2, 32)])
+@pytest.mark.parametrize("window,sinks", [(2 ** 31 - 1, 0), (2 ** 31 - 1, 2 ** 31 - 1), (1, 2 ** 31 - 1), (2 ** 30, 5)])
+def test_windows_and_sinks_of_any_size(heads, window, sinks):
+    """as large as the type holds: every key up to the row's is seen; and the pages of a session stay"""
+    s = Setup(heads, 16, "bf16", window, sinks, [300, 0], [140, 200], seed=10)
+    s.check(s.run(), only=some([140, 200], 10))
+    f = Setup(heads, 16, "bf16", window, sinks, [300, 0], [1, 1], seed=10)
+    f.check(f.run(single=True))
+    before = f.table.clone()
+    f.cache.resize(add=1)
+    assert torch.equal(f.table[before >= 0], before[before >= 0]) and f.lens.tolist() == [302, 2]
+
+
 def test_two_graphs_that_share_a_workspace():
     """a prompt's graph and a frame's over one cache, replayed in turn, eager calls in between"""
     s = Setup((8, 2, 64), 16, "bf16", 90, 4, [700, 1300, 20], [60, 1, 33], seed=7)
