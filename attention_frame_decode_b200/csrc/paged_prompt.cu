@@ -17,9 +17,9 @@
 // at head dim 128, whose tensor memory has no room for a third tile, and 2800 at head dim 64 with four tiles (with two
 // tiles of 128 keys and two threads a row 3700: 219 us where four tiles take 198).
 // Measured on a B200: 8192 rows of 40 heads over 8 of 128, window 4096, 64 sinks: 494 us, 1060 TFLOP/s of what the rows
-// see; 12 blocks of 1 to 900 rows, 32 heads over 8 of 64, window 2048: 181 us, of which a quarter is the last round of
-// tiles (2.4 a CTA; splitting that round's key blocks gave back in records and joins what it evened out, and cost the
-// other launch 2%).  A polynomial on the FMA units for every fourth or eighth exponential: 4 to 9% slower (issue slots).
+// see; 12 blocks of 1 to 900 rows, 32 heads over 8 of 64, window 2048: 147 us with the longest tiles first (splitting the
+// last round's key blocks gave back in records and joins what it evened out, and cost the other launch 2%).  A polynomial
+// on the FMA units for every fourth or eighth exponential: 4 to 9% slower (issue slots).
 // Warps: 0 copies K and V page by page (TMA, 128-byte swizzle) into a ring; 1 issues the MMAs; 2 hands out pieces and
 // brings the rows of Q; 3 cleans the values of edge blocks; 4-19 are the rows.
 #include "paged_dev.cuh"
@@ -158,10 +158,58 @@ struct PromptWork {
     int splits, of, record;  // the launch's pieces of a tile; how many of them have blocks; this piece's record
 };
 
+// The launch's tiles, longest first, so that the CTAs end together: 12 blocks of 1 to 900 rows 147 us in this order, 181 in
+// the sessions'.  Every CTA ranks them alike (the whole CTA calls; up to kSortTiles tiles and sessions).
+static constexpr int kSortTiles = 512;
+struct TileOrder {
+    int first[kSortTiles + 1], key[kSortTiles], tile[kSortTiles];   // tile: session << 16 | tile within it, by rank
+    int warp_sum[kPThreads / 32], count;
+};
+template <class S>
+VC_DEV void order_tiles(const PagedAttnArgs& a, int most_tiles, TileOrder& o) {
+    const int tid = threadIdx.x, lane = tid & 31, G = a.c.Hq / a.c.Hk, tile_rows = S::ROWS / G * G;
+    const int mine = tid < a.batch ? (int)(((long long)session_rows(a, tid) * G + tile_rows - 1) / tile_rows) : 0;
+    int incl = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += u;
+    }
+    if (lane == 31) o.warp_sum[tid >> 5] = incl;
+    __syncthreads();
+    int before = incl - mine;
+    for (int w = 0; w < tid >> 5; ++w) before += o.warp_sum[w];
+    if (tid <= a.batch) o.first[tid] = before;   // (first[batch]: all of them)
+    __syncthreads();
+    const int count = min(o.first[a.batch], most_tiles);   // more only where cu_rows overlap (those sessions are refused)
+    int key = 0, at = 0;
+    if (tid < count) {
+        int lo = 0, hi = a.batch - 1;   // the last session that starts at or before the tile
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (o.first[mid] <= tid) lo = mid;
+            else hi = mid - 1;
+        }
+        const int tile = tid - o.first[lo], r0 = tile * tile_rows, r1 = min(r0 + tile_rows, session_rows(a, lo) * G), p0 = a.pos[lo];
+        at = lo << 16 | tile;
+        if (p0 >= 0 && p0 < 1 << 30)   // key blocks, and what one takes by the MMA tiles that have rows
+            key = key_blocks<S::KEYS>(a.c.window, a.c.sinks, p0 + r0 / G, p0 + (r1 - 1) / G).total * ((r1 - r0 + 127) / 128 + 3);
+        o.key[tid] = key;
+    }
+    __syncthreads();
+    if (tid < count) {
+        int rank = 0;
+        for (int k = 0; k < count; ++k) rank += o.key[k] > key || (o.key[k] == key && k < tid);
+        o.tile[rank] = at;
+    }
+    if (tid == 0) o.count = count;
+    __syncthreads();
+}
+
 // piece `item` of the launch (a whole warp calls); nb is 0 where there is nothing to do, and n_rows too where not even
 // an empty record is wanted, and -1 behind the last piece.  A tile holds whole tokens: tile_rows = (ROWS / G) G rows.
 template <class S>
-VC_DEV PromptWork prompt_work(const PagedAttnArgs& a, int tiles, int splits, int item) {
+VC_DEV PromptWork prompt_work(const PagedAttnArgs& a, const TileOrder* order, int tiles, int splits, int item) {
     PromptWork w{};
     const int G = a.c.Hq / a.c.Hk, tile_rows = S::ROWS / G * G;
     if (item >= tiles * a.c.Hk * splits) {
@@ -174,8 +222,13 @@ VC_DEV PromptWork prompt_work(const PagedAttnArgs& a, int tiles, int splits, int
     w.j = unit % a.c.Hk;
     int session, tile;
     AttnSession o;
-    // the longest rows first
-    if (!find_tile(a, G, tile_rows, tiles - 1 - unit / a.c.Hk, session, tile) || !attn_session(a, session, o)) return w;
+    if (order) {
+        session = order->tile[unit / a.c.Hk] >> 16;
+        tile = order->tile[unit / a.c.Hk] & 0xffff;
+    } else if (!find_tile(a, G, tile_rows, tiles - 1 - unit / a.c.Hk, session, tile)) {   // a session's last rows first
+        return w;
+    }
+    if (!attn_session(a, session, o)) return w;
     w.s = o.s;
     w.row0 = o.row0;
     w.n_rows = o.n * G;
@@ -209,6 +262,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     __shared__ uint64_t s_full[S::TILES], p_ready[S::TILES], o_done[S::TILES];
     __shared__ uint32_t tmem_base, block_mapped[16];   // of block g at g % 16: at most ST / 2 are in the ring
     __shared__ int odd_values[4];
+    __shared__ TileOrder order;
     __shared__ PromptWork work[4];       // piece t at t % 4: written again when the rows are done with it
     __shared__ float top_x[S::ROWS], l_part[S::SHARES][S::ROWS];   // a row's highest score, between its threads; their sums
 
@@ -244,6 +298,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
     tc_fence_after();
     const uint32_t tmem = tmem_base;
     pdl_wait();
+    const bool ordered = !may_split && most_tiles <= kSortTiles && a.batch <= kSortTiles;
+    if (ordered) order_tiles<S>(a, most_tiles, order);
     if (blockIdx.x == 0)   // reports every session whose indices do not fit
         for (int i = tid; i < a.batch; i += kPThreads) {
             AttnSession o;
@@ -398,7 +454,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             }
         } else if (warp == 2) {
             // ---- the pieces, handed out as CTAs come for them (the first by index), and their rows of Q ----
-            const int tiles = count_tiles(a, G, S::ROWS / G * G, most_tiles), units = tiles * a.c.Hk;
+            const int tiles = ordered ? order.count : count_tiles(a, G, S::ROWS / G * G, most_tiles), units = tiles * a.c.Hk;
             const int splits = may_split ? unit_splits(units, (int)gridDim.x) : 1, items = units * splits;
             for (int t = 0; t <= most; ++t) {
                 int item = blockIdx.x;
@@ -410,7 +466,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                     }
                     item = __shfl_sync(0xffffffffu, item, 0);
                 }
-                const PromptWork w = prompt_work<S>(a, tiles, splits, item);
+                const PromptWork w = prompt_work<S>(a, ordered ? &order : nullptr, tiles, splits, item);
                 if (lane == 0) {
                     work[t & 3] = w;
                     odd_values[t & 3] = 0;

@@ -49,14 +49,50 @@ def test_more_tiles_than_sms(heads, page):
         s.check(out, only=some(rows, 40))
 
 
+class Sessions(Setup):
+    """Setup whose check looks up the sessions of `only` alone"""
+
+    def check(self, out, only):
+        full = self.ctx, self.rows, self.seqs, self.starts
+        for i in sorted({i for i, _ in only}):
+            a, n = int(full[3][i]), full[1][i]
+            self.ctx, self.rows, self.seqs, self.starts = [full[0][i]], [n], [full[2][i]], np.array([a, a + n])
+            super().check(out, only={(0, r) for j, r in only if j == i})
+        self.ctx, self.rows, self.seqs, self.starts = full
+
+    def parts(self, total=None):
+        return super().parts(self.qkv.shape[0] - 5 if total is None else total)
+
+
+@pytest.mark.parametrize("sessions", [60, 520])
+def test_skipped_sessions_among_many_tiles(sessions):
+    """tiles taken longest first (up to 512) or as the sessions come; sessions without a position, with one behind their
+    length, and without rows change nothing for the others"""
+    m = vc()
+    r = np.random.default_rng(12)
+    rows = [int(x) for x in r.integers(100, 300, sessions)] if sessions < 100 else [30] * sessions
+    ctx = [int(x) for x in r.integers(0, 300, sessions)]
+    rows[3] = rows[sessions - 1] = 0
+    s = Sessions((16, 8, 64), 16, "bf16", 120, 3, ctx, rows, seed=13)
+    pos = list(ctx)
+    pos[1], pos[10], pos[20] = -1, ctx[10] + 1, -1
+    out = s.run(pos=pos)
+    assert int(s.cache.status) == m.VC_DEV_INVALID
+    s.cache.status.zero_()
+    for i in (1, 10, 20):
+        part = out[s.starts[i]:s.starts[i + 1]]
+        assert torch.equal(part, torch.full_like(part, 7.0))
+    s.check(out, {p for p in some(rows, 40) if p[0] not in (1, 10, 20) and (p[0] < 30 or p[0] > sessions - 10)})
+
+
 @pytest.mark.parametrize("batch", [1, 2, 40, 300])
 def test_one_row_a_session_as_a_prompt(batch):
     """blocks of one row, in the prompts' form: as the frames' form gives them, within both forms' bounds"""
     ctx = [(37 * i) % 260 for i in range(batch)]
-    s = Setup((8, 2, 64), 16, "bf16", 100, 3, ctx, [1] * batch, seed=6)
+    s = Sessions((8, 2, 64), 16, "bf16", 100, 3, ctx, [1] * batch, seed=6)
     only = some([1] * batch, 20)
-    s.check(s.run(), only=only)
-    s.check(s.run(single=True), only=only)
+    s.check(s.run(), only)
+    s.check(s.run(single=True), only)
 
 
 @pytest.mark.parametrize("single", [True, False])
