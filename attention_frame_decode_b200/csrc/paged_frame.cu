@@ -21,7 +21,7 @@
 
 namespace vc {
 
-static constexpr int kFMaxStages = 4;
+static constexpr int kFMaxStages = 4;   // below eight (see look_up)
 static constexpr int kFMaxBatch = 2048;
 // Whole (session, KV head)s go to warps, and no join is needed, where that gives no warp more than this many units
 // over an equal share: a join costs about as much as four units (2 us).
@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(FrameShape<DH>::THREADS, 1)
         if (looked < copies) forward(look, batch);
         return o;
     };
-    Look now = look_up(), next = look_up();
+    Look now = look_up(), next{-1, 0};
     auto issue = [&]() {   // starts the next copy
         if (copy >= copies) return;
         const int from = copy % batch * boxes + (lane & (boxes - 1));
@@ -262,6 +262,7 @@ __global__ void __launch_bounds__(FrameShape<DH>::THREADS, 1)
     };
 #pragma unroll 1
     for (int s = 0; s < L.stages; ++s) issue();
+    next = look_up();   // (a batch is at least eight copies: the first stages come from the first)
 
     auto out_at = [&](int row, int j, int r, int d) { return a.out + (size_t)row * a.out_ld + (size_t)(j * G + r) * DH + d; };
     auto rec_a = [&](int w) { return comb + (size_t)w * ((G * (CS + 2) + 3) & ~3); };   // 16-byte aligned
@@ -539,15 +540,50 @@ __global__ void __launch_bounds__(FrameShape<DH>::THREADS, 1)
         open_last[tid] = is_last;
     }
     __syncthreads();
+    // up to twelve contributors: a thread takes four columns of a row with everything that it needs in flight at once
+    // (the maxima and sums are the same addresses for the row's threads)
+    constexpr int kFew = 12;
+    const int pieces = G * (DH / 4);
+    auto record_of = [&](const int4& seg, int cta) { return (2 * cta + (seg.x <= range_start(cta * kWarps) ? 0 : 1)) * rec_floats; };
+    for (int i = tid; i < 2 * pieces; i += kThreads) {
+        const int which = i >= pieces, r = i % pieces / (DH / 4), d = 4 * (i % (DH / 4));
+        const int4 seg = open_seg[which];
+        if (!open_last[which]) continue;
+        const int f = owner(seg.x) / kWarps, n = owner(seg.y - 1) / kWarps - f + 1;
+        if (n > kFew) continue;
+        float2 w[kFew];
+        float4 y[kFew];
+#pragma unroll
+        for (int k = 0; k < kFew; ++k) {
+            const float* rec = a.partial + (k < n ? record_of(seg, f + k) : 0);
+            w[k] = k < n ? __ldcg(reinterpret_cast<const float2*>(rec + G * DH + 2 * r)) : make_float2(-INFINITY, 0.0f);
+            y[k] = k < n ? __ldcg(reinterpret_cast<const float4*>(rec + r * DH + d)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
+        float top = -INFINITY, sum = 0.0f, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int k = 0; k < kFew; ++k) top = fmaxf(top, w[k].x);
+        if (top == -INFINITY) top = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kFew; ++k) {
+            const float x = exp2_approx(w[k].x - top);
+            sum = fmaf(w[k].y, x, sum);
+            v[0] = fmaf(y[k].x, x, v[0]); v[1] = fmaf(y[k].y, x, v[1]);
+            v[2] = fmaf(y[k].z, x, v[2]); v[3] = fmaf(y[k].w, x, v[3]);
+        }
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        *reinterpret_cast<uint2*>(out_at(seg.z, seg.w, r, d)) =
+            make_uint2(pack_out<F16>(a.widen, v[0] * inv, v[1] * inv), pack_out<F16>(a.widen, v[2] * inv, v[3] * inv));
+    }
     for (int which = 0; which < 2; ++which) {
         if (!open_last[which]) continue;
         const int4 seg = open_seg[which];
         const int f = owner(seg.x) / kWarps, n = owner(seg.y - 1) / kWarps - f + 1;
+        if (n <= kFew) continue;
         // wts[k][r]: the k-th contributor's (maximum, sum), then its factor; its record is that of its range's start
         // if the segment began there or before
         int* rec_at = reinterpret_cast<int*>(wts + 2 * n * G);
         for (int k = tid; k < n; k += kThreads)
-            rec_at[k] = (2 * (f + k) + (seg.x <= range_start((f + k) * kWarps) ? 0 : 1)) * rec_floats;
+            rec_at[k] = record_of(seg, f + k);
         __syncthreads();
         for (int i = tid; i < n * G; i += kThreads)
             reinterpret_cast<float2*>(wts)[i] =
