@@ -20,6 +20,10 @@ from . import VcAttnRows, VcError, VcPagedKv, VcSessionPart, VC_ERR_INVALID_ARG,
 _lib = lib()
 
 
+# the handle of a device's current stream; without the Stream object where torch has that (3 us of a call's 12 otherwise)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -98,13 +102,13 @@ class PagedCache:
 
     def _call(self, fn, where, *args, stream=None):
         """fn(cache, *args, stream) on the cache's device"""
-        if torch.cuda.current_device() == self.device.index:
-            s = stream if stream is not None else torch.cuda.current_stream()
-            _check(fn(self._ref, *args, s.cuda_stream), where)
+        index = self.device.index
+        s = stream.cuda_stream if stream is not None else _current_stream(index)
+        if torch.cuda.current_device() == index:
+            _check(fn(self._ref, *args, s), where)
         else:
-            with torch.cuda.device(self.device):
-                s = stream if stream is not None else torch.cuda.current_stream()
-                _check(fn(self._ref, *args, s.cuda_stream), where)
+            with torch.cuda.device(index):
+                _check(fn(self._ref, *args, s), where)
 
     def _index(self, t, n, name):
         """an int32 tensor of n values on the cache's device"""
