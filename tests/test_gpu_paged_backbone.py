@@ -351,6 +351,32 @@ def test_two_caches_take_turns(cuda):
     assert float((one.hid - two.hid).abs().max()) <= TOL * float(two.hid.square().mean().sqrt())
 
 
+def test_frames_in_a_callers_graph(cuda):
+    """with direct launches a frame can be captured by the caller: every replay is the next frame"""
+    import torch
+    import attention_frame_decode_b200 as vc
+    cfg = synth.tiny_config()
+    one, two = PagedRun(cfg, 4, 2, 64, window=20, sinks=2), PagedRun(cfg, 4, 2, 64, window=20, sinks=2)
+    one.bb.set_option(vc.OPT_GRAPH, 0)
+    one.bb.set_taps(one.hid, one.lg)
+    x = torch.zeros((2, cfg.d_model), dtype=torch.bfloat16, device="cuda")
+    frame = lambda run: run.bb.step_paged(x, run.st, run.cache, run.tt, run.tf)  # noqa: E731
+    x.copy_(bits(synth.frame_inputs(cfg, 4, 0, 2)))
+    for run in (one, two):
+        frame(run)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        frame(one)
+    for t in range(1, 40):
+        x.copy_(bits(synth.frame_inputs(cfg, 4, t, 2)))
+        graph.replay()
+        frame(two)
+        assert float((one.hid - two.hid).abs().max()) <= TOL * float(two.hid.square().mean().sqrt())
+    assert one.cache.lens.tolist() == [40, 40] == two.cache.lens.tolist() and torch.equal(one.cache.table, two.cache.table)
+    assert int(one.cache.status[0]) == 0
+
+
 def test_refusals(cuda):
     import torch
     import attention_frame_decode_b200 as vc

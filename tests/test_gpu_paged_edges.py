@@ -272,3 +272,43 @@ def test_appending_keeps_the_rest_of_a_page():
             same = (now == old).all(-1)[0].all(1).cpu()      # [pages][page], over the heads
             assert bool(same[~touched].all())
         s.check_appended()
+
+
+@pytest.mark.parametrize("single", [True, False])
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_session_read_twice_in_one_call(single, d):
+    """without new rows a session may be named again: its rows at two places, each as alone"""
+    rows = [1, 1] if single else [50, 33]
+    s = Setup((8, 2, d), 32, "bf16", 60, 3, [200, 90], rows, seed=14)
+    s.run(single=single)
+    q = s.parts()[0]
+    i32 = dict(dtype=torch.int32, device="cuda")
+    want = s.run(append=False, single=single)
+    twice = torch.cat([q[:rows[0]], q[:rows[0]]])
+    out = torch.zeros_like(twice)
+    cu = None if single else torch.tensor([0, rows[0], 2 * rows[0]], **i32)
+    s.cache.attend(0, twice, None, None, out, torch.tensor([200, 200], **i32), seqs=torch.tensor([0, 0], **i32), cu_rows=cu)
+    assert int(s.cache.status) == 0
+    # each of the two is off by at most 2^-8 of sum w |v| (weights in bf16), 2^-8 of its value (rounded once) and, with a
+    # 16th on top, the sums in fp32
+    tol = 2 * 2.0 ** -8 * (float(s.v.float().abs().max()) + float(want.float().abs().max())) * 17 / 16
+    assert float((out[:rows[0]].float() - want[:rows[0]].float()).abs().max()) <= tol
+    assert float((out[rows[0]:].float() - want[:rows[0]].float()).abs().max()) <= tol
+
+
+def test_two_caches_on_two_streams():
+    """prompts and frames of caches with workspaces of their own, at the same time"""
+    a = Setup((8, 2, 64), 16, "bf16", 150, 4, [700, 1300], [260, 133], seed=15)
+    b = Setup((8, 2, 128), 32, "fp16", 0, 0, [900, 2100, 5], [1, 1, 1], seed=16)
+    want = a.run(), b.run(single=True)
+    torch.cuda.synchronize()
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    outs = [torch.zeros_like(w) for w in want]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        with torch.cuda.stream(streams[0]):
+            a.run(out=outs[0])
+        with torch.cuda.stream(streams[1]):
+            b.run(single=True, out=outs[1])
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o, w in zip(outs, want))
