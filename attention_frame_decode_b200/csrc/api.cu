@@ -118,7 +118,7 @@ struct Workspace {
     FrameProgram* prog;  // the frame kernel's program (device copy)
     int* fk_sync;        // [0] barrier arrivals, [1] abort flag of the frame kernel
     uint16_t* qkv;       // a step's queries, keys and values for a paged cache
-    int *pos, *pf_pos;   // positions that a paged cache granted: a step's rows; a prefill (kPagedPrefillInts)
+    int *pos, *slots, *pf_pos;   // a paged step's rows: positions granted, slots; a prefill's (kPagedPrefillInts)
 };
 
 struct GraphKey {
@@ -252,7 +252,7 @@ extern "C" size_t vc_workspace_bytes(const vc_config* cfg) {
     add(sizeof(FrameProgram));                // the frame kernel's program
     add(256);                                 // its barrier and abort words
     add((size_t)B * D.qkv_rows * 2 + 16);     // a paged step's queries, keys and values
-    add((16 + kPagedPrefillInts) * 4);        // positions of a paged cache
+    add((32 + kPagedPrefillInts) * 4);        // positions and slots of a paged cache's calls
     return align_up(total, 256);
 }
 
@@ -295,8 +295,9 @@ static void carve(vc_backbone* h, uint8_t* base) {
     W.prog = (FrameProgram*)take(sizeof(FrameProgram));
     W.fk_sync = (int*)take(256);
     W.qkv = (uint16_t*)take((size_t)B * D.qkv_rows * 2 + 16);
-    W.pos = (int*)take((16 + kPagedPrefillInts) * 4);
-    W.pf_pos = W.pos + 16;
+    W.pos = (int*)take((32 + kPagedPrefillInts) * 4);
+    W.slots = W.pos + 16;
+    W.pf_pos = W.pos + 32;
 }
 
 static bool qmat_ok(const vc_qmat& m, int fmt, int group, int N, int K) {
@@ -681,9 +682,11 @@ static vc_status run_step(vc_backbone* h, const void* x, int B, const int32_t* s
                           const vc_paged_kv* kv = nullptr) {
     if (kv) {
         // the frame's positions, outside the graph: the page calls' kernels are not among its nodes
-        const cudaError_t e = launch_paged_resize(paged_kernel_kv(*kv), paged_carve(*kv, kv->workspace), B, slots, nullptr,
-                                                  1, h->ws.pos, s);
+        cudaError_t e = launch_paged_resize(paged_kernel_kv(*kv), paged_carve(*kv, kv->workspace), B, slots, nullptr, 1,
+                                            h->ws.pos, s);
+        if (e == cudaSuccess && slots) e = launch_step_slots(slots, B, h->D.slots, h->ws.slots, s);
         if (e != cudaSuccess) return cuda_fail(e, "vc_step_paged resize");
+        if (slots) slots = h->ws.slots;   // a row whose slot is out of range got no position: it is skipped, and reads slot 0
     }
     if (h->use_frame && !kv) {
         const cudaError_t e = run_frame(h, x, B, slots, st, tt, tf, s, emb);

@@ -60,6 +60,16 @@ __global__ void input_kernel(const InputArgs a) {
     }
 }
 
+__global__ void step_slots_kernel(const int* slots, int B, int n_slots, int* out) {
+    const int b = threadIdx.x;
+    if (b < B) out[b] = (unsigned)slots[b] < (unsigned)n_slots ? slots[b] : 0;
+}
+
+cudaError_t launch_step_slots(const int* slots, int B, int n_slots, int* out, cudaStream_t s) {
+    step_slots_kernel<<<1, 32, 0, s>>>(slots, B, n_slots, out);
+    return cudaGetLastError();
+}
+
 cudaError_t launch_input(const InputArgs& a, cudaStream_t s) {
     input_kernel<<<a.B, 256, 0, s>>>(a);
     return cudaGetLastError();

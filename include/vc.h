@@ -432,11 +432,11 @@ vc_status vc_paged_attend(const vc_paged_kv* kv, int layer, const vc_attn_rows* 
  * state->k and state->v, which are not used and may be NULL.  kv: this backbone's attention layers in pattern order
  * (layers = how many, its KV and query heads and head_dim, bf16), seqs = n_slots; its window and sinks apply in every
  * layer, so that a session whose window is full goes on without an end (kv_capacity does not bound it).  The call
- * first asks for the frame's position of each row as vc_paged_resize(n = B, add = 1) does; a row that gets none is
- * skipped: its tokens are -1, its state and length stay, kv->status has the reason (kv->status and state->status may
- * be one word).  kv->len and state->ctx_len of a session start equal and go on together; a session is ended by
+ * first asks for the frame's position of each row as vc_paged_resize(n = B, add = 1) does; a row that gets none (no page,
+ * a slot out of range or named by an earlier row) is skipped: its tokens are -1, its state and length stay, kv->status
+ * has the reason (kv->status and state->status may be one word).  kv->len and state->ctx_len of a session start equal and go on together; a session is ended by
  * vc_paged_resize to length 0 and copied by vc_paged_fork with ssm, conv and ctx_len as parts.  One kernel per
- * operation whatever VC_OPT_FRAME says.  kv's workspace is in use: order the call with the other calls on kv. */
+ * operation whatever VC_OPT_FRAME says; with VC_OPT_GRAPH 0 the call can be captured into a graph of the caller's.  kv's workspace is in use: order the call with the other calls on kv. */
 vc_status vc_step_paged(vc_backbone* h, const void* x, const vc_token_embeddings* emb, int B, const int32_t* slots,
                         const vc_state* state, const vc_paged_kv* kv, int32_t* tok_text, int32_t* tok_func,
                         vc_stream_t stream);

@@ -264,6 +264,20 @@ def test_a_slot_named_twice_steps_once(cuda):
     assert run.cache.lens.tolist() == [0, 1] == run.st.ctx_len.tolist() and int(run.cache.status[0]) == INVALID
 
 
+def test_slots_out_of_range_are_skipped(cuda):
+    cfg = synth.tiny_config()
+    run, alone = PagedRun(cfg, 8, 3, 64), PagedRun(cfg, 8, 3, 64)
+    for t in range(3):
+        x = bits(synth.frame_inputs(cfg, 8, t, 3))
+        run.bb.step_paged(x, run.st, run.cache, run.tt, run.tf, slots=i32([-1, 1, 1 << 30]))
+        alone.bb.step_paged(x, alone.st, alone.cache, alone.tt, alone.tf, slots=i32([0, 1, 2]))
+        assert run.tt.tolist()[0] == -1 == run.tt.tolist()[2] and run.tt.tolist()[1] >= 0
+        a, b = run.hid[:, 1].double(), alone.hid[:, 1].double()
+        assert float((a - b).abs().max()) <= TOL * float(b.square().mean().sqrt())
+    assert run.cache.lens.tolist() == [0, 3, 0] == run.st.ctx_len.tolist() and int(run.cache.status[0]) == INVALID
+    assert not bool(run.st.ssm[:, 0].any()) and not bool(run.st.ssm[:, 2].any())
+
+
 def test_prefill_without_room_leaves_the_slot_empty(cuda):
     cfg = synth.tiny_config()
     run = PagedRun(cfg, 8, 2, 64, pages=3)
