@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* Qs = smem;                     // [halves][256 rows][128 B]
     uint8_t* ring = smem + S::QBYTES;       // [stages][halves][128 keys][128 B]
-    __shared__ uint64_t full[ST], empty[ST], clean[ST / 2], work_ready[2], q_ready[2], q_free, o_free[2], drained;
+    __shared__ uint64_t full[ST], empty[ST], clean[ST / 2], work_ready[2], work_taken[2], q_ready[2], q_free, o_free[2], drained;
     __shared__ uint64_t s_full[S::TILES], p_ready[S::TILES], o_done[S::TILES];
     __shared__ uint32_t tmem_base, block_mapped[16];   // of block g at g % 16: at most ST / 2 are in the ring
     __shared__ int odd_values[4];
@@ -287,6 +287,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&work_ready[i], 1);
+            mbar_init(&work_taken[i], 1);
             mbar_init(&q_ready[i], 1);
             mbar_init(&o_free[i], 16 + 1);
         }
@@ -313,9 +314,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
     };
     // Every role goes through the CTA's pieces in turn (t counts them, g the key blocks since the launch) and is held
     // up by barriers alone: the copies, the rows of Q and the first scores of a piece come while the one before ends.
-    // No barrier completes twice before all that wait for it have seen it once: q_ready and o_free alternate (the
-    // products of piece t + 1 begin after o_free of t, and q_ready of t + 2 after those), the others are held back by
-    // the arrivals of the same threads.
+    // No barrier completes twice before all that wait for it have seen it once: work_ready, q_ready and o_free alternate
+    // (piece t + 2 is handed out after the copies' warp took piece t, which nothing else waits for where pieces have no
+    // blocks; the products of piece t + 1 begin after o_free of t, and q_ready of t + 2 after those), the others are held
+    // back by the arrivals of the same threads.
 
     // the rows' warps take registers that the other four give up; in each SM quarter 4 x 104 + 64 = 5 x 96, the launch's
     if (warp < 4) {
@@ -327,6 +329,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
             for (int t = 0; t <= most && ok; ++t) {
                 wait(&work_ready[t & 1], t >> 1);
                 const PromptWork w = work[t & 3];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&work_taken[t & 1]);
                 if (w.nb < 0) break;
                 int entry = -1;
                 auto look_up = [&](int n) {   // lane q < boxes: the table entry of block n's q-th box
@@ -467,6 +471,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                     item = __shfl_sync(0xffffffffu, item, 0);
                 }
                 const PromptWork w = prompt_work<S>(a, ordered ? &order : nullptr, tiles, splits, item);
+                if (t > 1) wait(&work_taken[t & 1], (t - 2) >> 1);
                 if (lane == 0) {
                     work[t & 3] = w;
                     odd_values[t & 3] = 0;
