@@ -460,7 +460,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
             // ---- the pieces, handed out as CTAs come for them (the first by index), and their rows of Q ----
             const int tiles = ordered ? order.count : count_tiles(a, G, S::ROWS / G * G, most_tiles), units = tiles * a.c.Hk;
             const int splits = may_split ? unit_splits(units, (int)gridDim.x) : 1, items = units * splits;
-            for (int t = 0; t <= most; ++t) {
+            int t = 0;
+            for (; t <= most; ++t) {
                 int item = blockIdx.x;
                 if (t > 0) {
                     if (lane == 0) {
@@ -492,6 +493,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 __syncwarp();
                 if (w.nb < 0) break;
             }
+            // no rows of Q on their way outlive the CTA: these have come, unless a wait gave up (then a bounded while more)
+            for (int b = max(t - 1, 0); b <= t; ++b) mbar_poll(&q_ready[b & 1], (uint32_t)((b >> 1) & 1), kPollLimit);
         } else if (warp == 3) {
             // ---- values that not every row of the tile sees: those that no row sees become 0, and so do infinities and
             // NaN (the rows that see them get them at the end), so that a weight of 0 takes nothing in ----
