@@ -63,6 +63,10 @@ VC_DEV bool nonfinite2(uint32_t u) {
     return (u & m) == m || ((u >> 16) & m) == m;
 }
 
+// whether the lower 16 bits are an infinity or NaN
+template <bool F16>
+VC_DEV bool nonfinite1(uint32_t u) { return (u & exponent_mask<F16>()) == exponent_mask<F16>(); }
+
 // whether one of eight 16-bit values is an infinity or NaN: the exponent's carry reaches the sign bit of its half
 template <bool F16>
 VC_DEV bool any_nonfinite(const uint4& x) {
@@ -154,6 +158,57 @@ VC_DEV KeyBlocks key_blocks(int window, int sinks, int p_lo, int p_hi) {
     }
     k.total = k.n_sink + max(end - k.start, 0);
     return k;
+}
+
+// What products cannot tell of values that are not finite (0 inf, inf - inf and a weight that is 0 in 32 bits make NaN): the
+// sum of the infinities and NaN among four dimensions, d .. d + 3, of the values that the row at position p sees; 0 where
+// there are none.  Rare, and so a function of its own behind the sums: inlined there it took 7% of the frames' time.
+template <int DH>
+struct SeenValues {
+    const uint16_t* v;   // the layer's values, those of the KV head from here on
+    const int* row;      // the session's row of the table
+    int pages, page_shift, Hk, p, window, sinks;
+};
+template <int DH>
+VC_DEV SeenValues<DH> seen_values(const PagedKv& c, int s, int j, int p) {
+    return {c.v + (size_t)j * c.page * DH, c.table + (size_t)s * c.columns, c.pages, c.page_shift, c.Hk, p, c.window, c.sinks};
+}
+template <int DH, bool F16>
+__device__ __noinline__ float4 odd_values(const SeenValues<DH> c, int d) {
+    float4 z = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int t0 = 0; t0 <= c.p; t0 += 16) {   // 16 keys of a page
+        if (c.window != 0 && t0 >= c.sinks && t0 + 15 <= c.p - c.window) {   // the window has given them up, and those to its start
+            t0 = (c.p - c.window + 1) / 16 * 16 - 16;
+            continue;
+        }
+        const int e = c.row[t0 >> c.page_shift];
+        if ((unsigned)e >= (unsigned)c.pages) continue;
+        const uint16_t* from = c.v + (((size_t)e * c.Hk << c.page_shift) + (t0 & ((1 << c.page_shift) - 1))) * DH + d;
+        uint2 x[16];
+#pragma unroll
+        for (int u = 0; u < 16; ++u) x[u] = __ldcg(reinterpret_cast<const uint2*>(from + u * DH));
+#pragma unroll
+        for (int u = 0; u < 16; ++u) {
+            const int t = t0 + u;
+            if (t > c.p || (c.window != 0 && t >= c.sinks && t <= c.p - c.window)) continue;
+            if (nonfinite1<F16>(x[u].x)) z.x += unpack16<F16>((uint16_t)x[u].x);
+            if (nonfinite1<F16>(x[u].x >> 16)) z.y += unpack16<F16>((uint16_t)(x[u].x >> 16));
+            if (nonfinite1<F16>(x[u].y)) z.z += unpack16<F16>((uint16_t)x[u].y);
+            if (nonfinite1<F16>(x[u].y >> 16)) z.w += unpack16<F16>((uint16_t)(x[u].y >> 16));
+        }
+    }
+    return z;
+}
+// whether one of a thread's four results is not finite
+VC_DEV bool odd_results(const float (&v)[4]) { return !(v[0] * 0.0f + v[1] * 0.0f + v[2] * 0.0f + v[3] * 0.0f == 0.0f); }
+// ... and those that a seen infinity or NaN decides, put right (the sum of the weights is a number)
+template <int DH, bool F16>
+VC_DEV void decide_odd(float (&v)[4], const SeenValues<DH>& c, int d) {
+    const float4 z = odd_values<DH, F16>(c, d);
+    if (z.x != 0.0f) v[0] = z.x;
+    if (z.y != 0.0f) v[1] = z.y;
+    if (z.z != 0.0f) v[2] = z.z;
+    if (z.w != 0.0f) v[3] = z.w;
 }
 
 // how many tiles the sessions' rows make (a whole warp calls): at most `most`, as the launch counted them from the rows

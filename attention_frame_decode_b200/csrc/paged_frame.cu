@@ -13,7 +13,8 @@
 // the CTA joins its warps' records at the end, and where CTAs share it the last of them to arrive joins theirs, in
 // order, so that results do not depend on timing.
 // The weights go into the products as a 16-bit value and the 16-bit rest of it: the error of a weight is
-// 2^-16 (bf16), and the products are not what this kernel waits for.
+// 2^-16 (bf16), and the products are not what this kernel waits for.  Of an infinite value that is seen they make NaN: results
+// that are not finite are decided by the values themselves (paged_dev.cuh).
 #include <algorithm>
 
 #include "paged_dev.cuh"
@@ -442,6 +443,7 @@ __global__ void __launch_bounds__(FrameShape<DH>::THREADS, 1)
         // ---- the end of the (session, KV head), or of the range ----
         const bool ends_here = s0 >= c0 && s1 <= c1;
         float* rec = x_seg == c0 ? rec_a(warp) : rec_b(warp);   // the ring is free where the range ends
+        unsigned odd = 0;   // heads of which a result is not finite and the weights' sum is a number
 #pragma unroll
         for (int h = 0; h < NH; ++h)
 #pragma unroll
@@ -455,6 +457,10 @@ __global__ void __launch_bounds__(FrameShape<DH>::THREADS, 1)
                 if (ends_here) {
                     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
                     uint16_t* to = out_at(row, at0.j, r, g);
+                    float x = 0.0f;
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) x += acc[mt][h][e] * 0.0f + acc[mt][h][2 + e] * 0.0f;
+                    if (x != 0.0f && sum == sum) odd |= 1u << r;
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt) {
                         const uint32_t v = pack_out<F16>(a.widen, acc[mt][h][e] * inv, acc[mt][h][2 + e] * inv);
@@ -470,6 +476,25 @@ __global__ void __launch_bounds__(FrameShape<DH>::THREADS, 1)
                     if (g == 0) *reinterpret_cast<float2*>(rec + G * CS + 2 * r) = make_float2(m[h][e], sum);
                 }
             }
+        if (__any_sync(0xffffffffu, odd != 0)) {
+            odd = __reduce_or_sync(0xffffffffu, odd);
+            __threadfence_block();
+            __syncwarp();   // the outputs, and the new row in its page
+            const SeenValues<DH> values = seen_values<DH>(a.c, me.s, at0.j, me.p);
+#pragma unroll 1
+            for (int d = 4 * lane; d < DH; d += 128) {
+                const float4 z = odd_values<DH, F16>(values, d);
+#pragma unroll 1
+                for (int r = 0; r < G; ++r) {
+                    if (!((odd >> r) & 1u)) continue;
+                    uint16_t* to = out_at(row, at0.j, r, d);
+                    if (z.x != 0.0f) to[0] = (uint16_t)pack_out<F16>(a.widen, z.x, 0.0f);
+                    if (z.y != 0.0f) to[1] = (uint16_t)pack_out<F16>(a.widen, z.y, 0.0f);
+                    if (z.z != 0.0f) to[2] = (uint16_t)pack_out<F16>(a.widen, z.z, 0.0f);
+                    if (z.w != 0.0f) to[3] = (uint16_t)pack_out<F16>(a.widen, z.w, 0.0f);
+                }
+            }
+        }
         if (!ends_here) {
             seg_last = make_int4(s0, s1, row, at0.j);
             if (x_seg == c0) seg_first = seg_last;
@@ -482,6 +507,9 @@ __global__ void __launch_bounds__(FrameShape<DH>::THREADS, 1)
     // ---- the CTA's warps: each joins what begins with it (warp 0: also what began before the CTA) ----
     __syncthreads();
     const int rec_floats = (G * (DH + 2) + 3) & ~3;   // 16-byte aligned records
+    auto decide = [&](float (&v)[4], float sum, const int4& seg, int d) {   // results of a segment's row (times its sum or not)
+        if (odd_results(v) && sum == sum) decide_odd<DH, F16>(v, seen_values<DH>(a.c, line[seg.z].s, seg.w, line[seg.z].p), d);
+    };
     const int C0 = range_start(range0), C1 = range_start(range0 + kWarps);
     auto join_warps = [&](const int4& seg) {
         const int s0 = seg.x, s1 = seg.y, last = owner(min(s1, C1) - 1) - range0;
@@ -513,6 +541,7 @@ __global__ void __launch_bounds__(FrameShape<DH>::THREADS, 1)
             }
             if (!shared) {
                 const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                decide(v, sum, seg, d);
                 *reinterpret_cast<uint2*>(out_at(seg.z, seg.w, r, d)) =
                     make_uint2(pack_out<F16>(a.widen, v[0] * inv, v[1] * inv), pack_out<F16>(a.widen, v[2] * inv, v[3] * inv));
             } else {
@@ -571,6 +600,7 @@ __global__ void __launch_bounds__(FrameShape<DH>::THREADS, 1)
             v[2] = fmaf(y[k].z, x, v[2]); v[3] = fmaf(y[k].w, x, v[3]);
         }
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        decide(v, sum, seg, d);
         *reinterpret_cast<uint2*>(out_at(seg.z, seg.w, r, d)) =
             make_uint2(pack_out<F16>(a.widen, v[0] * inv, v[1] * inv), pack_out<F16>(a.widen, v[2] * inv, v[3] * inv));
     }
@@ -615,6 +645,7 @@ __global__ void __launch_bounds__(FrameShape<DH>::THREADS, 1)
                 v[0] = fmaf(y.x, w, v[0]); v[1] = fmaf(y.y, w, v[1]);
                 v[2] = fmaf(y.z, w, v[2]); v[3] = fmaf(y.w, w, v[3]);
             }
+            decide(v, wts[2 * r], seg, d);
             *reinterpret_cast<uint2*>(out_at(seg.z, seg.w, r, d)) =
                 make_uint2(pack_out<F16>(a.widen, v[0], v[1]), pack_out<F16>(a.widen, v[2], v[3]));
         }
