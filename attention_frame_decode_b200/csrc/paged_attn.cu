@@ -125,6 +125,7 @@ __global__ void __launch_bounds__(TileShape<DH, ROWS>::THREADS) paged_tile_kerne
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+    bool cleaned = false;   // infinities or NaN were taken out of some block's values
     const int pr[2] = {o.p0 + (r0 + 16 * warp + g) / G, o.p0 + (r0 + 16 * warp + g + 8) / G};
     const int mi = lane >> 3, lr = lane & 7;
 
@@ -190,26 +191,17 @@ __global__ void __launch_bounds__(TileShape<DH, ROWS>::THREADS) paged_tile_kerne
                 s[n][e] = exp2_approx(s[n][e] - base[e >> 1]);
                 l[e >> 1] += s[n][e];
             }
-        // a value that is not finite may be under a weight of 0 for some rows and seen by others: rare, and then
-        // it is added to the rows that see it and taken out of the tile before the products
+        // a value that is not finite may be under a weight of 0 for some rows and seen by others: rare, and then it is
+        // taken out of the tile before the products, and the results decided by the values themselves
         if (!whole) {
             bool odd = false;
             for (int idx = tid; idx < kTK * (DH / 2); idx += kTThreads)
                 odd |= nonfinite2<F16>(*reinterpret_cast<const uint32_t*>(Vs + (idx / (DH / 2)) * SK + 2 * (idx % (DH / 2))));
             if (__syncthreads_or(odd)) {
-                for (int key = 0; key < kTK; ++key)
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const uint16_t u = Vs[key * SK + 8 * n + 2 * tq + (e & 1)];
-                            if ((u & exponent_mask<F16>()) == exponent_mask<F16>() && seen(e >> 1, key))
-                                acc[n][e] += unpack16<F16>(u);
-                        }
-                __syncthreads();
+                cleaned = true;
                 for (int idx = tid; idx < kTK * DH; idx += kTThreads) {
                     uint16_t* p = Vs + (idx / DH) * SK + idx % DH;
-                    if ((*p & exponent_mask<F16>()) == exponent_mask<F16>()) *p = 0;
+                    if (nonfinite1<F16>(*p)) *p = 0;
                 }
                 __syncthreads();
             }
@@ -237,6 +229,24 @@ __global__ void __launch_bounds__(TileShape<DH, ROWS>::THREADS) paged_tile_kerne
     for (int h = 0; h < 2; ++h) {
         l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
         l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        float x = cleaned ? 1.0f : 0.0f;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) x += acc[n][2 * h] * 0.0f + acc[n][2 * h + 1] * 0.0f;
+        if (x == 0.0f || l[h] != l[h] || r0 + 16 * warp + g + 8 * h >= n_rows) continue;
+        const SeenValues<DH> values = seen_values<DH>(a.c, o.s, j, pr[h]);
+#pragma unroll 1
+        for (int k = 0; k < NT; ++k) {
+            const float4 z = odd_values_call<DH, F16>(values, 8 * k + 4 * (tq >> 1));
+            const float z0 = tq & 1 ? z.z : z.x, z1 = tq & 1 ? z.w : z.y;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                if (n == k && z0 != 0.0f) acc[n][2 * h] = z0;
+                if (n == k && z1 != 0.0f) acc[n][2 * h + 1] = z1;
+            }
+        }
     }
     auto out_row = [&](int rr) { return a.out + (size_t)(o.row0 + rr / G) * a.out_ld + (size_t)(j * G + rr % G) * DH; };
     if (of == 1) {
@@ -269,7 +279,8 @@ __global__ void __launch_bounds__(TileShape<DH, ROWS>::THREADS) paged_tile_kerne
     }
     if (join_later || !last_to_arrive(a.merge + unit, of)) return;
     join_records<DH, F16, kTThreads>(a, a.partial + (size_t)unit * splits * REC, kTR, of, 0, min(kTR, n_rows - r0),
-                                     reinterpret_cast<float*>(smem), [&](int r) { return out_row(r0 + r); });
+                                     reinterpret_cast<float*>(smem), [&](int r) { return out_row(r0 + r); },
+                                     [&](int r, int d) { return odd_values_call<DH, F16>(seen_values<DH>(a.c, o.s, j, o.p0 + (r0 + r) / G), d); });
 }
 
 // ------------------------------------------------------------------------------------------
@@ -298,7 +309,7 @@ __global__ void __launch_bounds__(kJThreads) paged_join_kernel(const PagedAttnAr
     join_records<DH, F16, kJThreads>(a, a.partial + (size_t)unit * splits * (w.rows * (DH + 2)), w.rows, of, first, rows, factor, [&](int r) {
         const int packed = r0 + first + r;
         return a.out + (size_t)(o.row0 + packed / G) * a.out_ld + (size_t)(j * G + packed % G) * DH;
-    });
+    }, [&](int r, int d) { return odd_values_call<DH, F16>(seen_values<DH>(a.c, o.s, j, o.p0 + (r0 + first + r) / G), d); });
 }
 
 template <int DH, int BK>

@@ -162,7 +162,7 @@ VC_DEV KeyBlocks key_blocks(int window, int sinks, int p_lo, int p_hi) {
 
 // What products cannot tell of values that are not finite (0 inf, inf - inf and a weight that is 0 in 32 bits make NaN): the
 // sum of the infinities and NaN among four dimensions, d .. d + 3, of the values that the row at position p sees; 0 where
-// there are none.  Rare, and so a function of its own behind the sums: inlined there it took 7% of the frames' time.
+// there are none.
 template <int DH>
 struct SeenValues {
     const uint16_t* v;   // the layer's values, those of the KV head from here on
@@ -174,7 +174,7 @@ VC_DEV SeenValues<DH> seen_values(const PagedKv& c, int s, int j, int p) {
     return {c.v + (size_t)j * c.page * DH, c.table + (size_t)s * c.columns, c.pages, c.page_shift, c.Hk, p, c.window, c.sinks};
 }
 template <int DH, bool F16>
-__device__ __noinline__ float4 odd_values(const SeenValues<DH> c, int d) {
+VC_DEV float4 odd_values(const SeenValues<DH> c, int d) {
     float4 z = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     for (int t0 = 0; t0 <= c.p; t0 += 16) {   // 16 keys of a page
         if (c.window != 0 && t0 >= c.sinks && t0 + 15 <= c.p - c.window) {   // the window has given them up, and those to its start
@@ -199,12 +199,13 @@ __device__ __noinline__ float4 odd_values(const SeenValues<DH> c, int d) {
     }
     return z;
 }
+// a call of its own where its registers are not to be the products' (not behind setmaxnreg: too few there for a call)
+template <int DH, bool F16>
+__device__ __noinline__ float4 odd_values_call(const SeenValues<DH> c, int d) { return odd_values<DH, F16>(c, d); }
 // whether one of a thread's four results is not finite
 VC_DEV bool odd_results(const float (&v)[4]) { return !(v[0] * 0.0f + v[1] * 0.0f + v[2] * 0.0f + v[3] * 0.0f == 0.0f); }
 // ... and those that a seen infinity or NaN decides, put right (the sum of the weights is a number)
-template <int DH, bool F16>
-VC_DEV void decide_odd(float (&v)[4], const SeenValues<DH>& c, int d) {
-    const float4 z = odd_values<DH, F16>(c, d);
+VC_DEV void decide_odd(float (&v)[4], const float4& z) {
     if (z.x != 0.0f) v[0] = z.x;
     if (z.y != 0.0f) v[1] = z.y;
     if (z.z != 0.0f) v[2] = z.z;
@@ -248,9 +249,11 @@ VC_DEV bool last_to_arrive(int* counter, int of) {
 
 // Joins, in split order, the records of a unit whose key blocks were split into `of` ranges: rows first .. first + rows - 1
 // of the tile, by all THREADS threads of the CTA.  A record: sums [rec_rows][DH], maxima and sums of weights [rec_rows],
-// each under its own maximum; out(r): where row first + r goes; factor: room for [of][rows].
-template <int DH, bool F16, int THREADS, class Out>
-VC_DEV void join_records(const PagedAttnArgs& a, const float* all, int rec_rows, int of, int first, int rows, float* factor, Out out) {
+// each under its own maximum; out(r): where row first + r goes, odd(r, d): odd_values of what it sees; factor: room for
+// [of][rows].
+template <int DH, bool F16, int THREADS, class Out, class Odd>
+VC_DEV void join_records(const PagedAttnArgs& a, const float* all, int rec_rows, int of, int first, int rows, float* factor, Out out,
+                         Odd odd) {
     const int tid = threadIdx.x, rec = rec_rows * (DH + 2);
     const float* tops = all + rec_rows * DH + first;   // a split that saw nothing: maximum -inf, factor 0, sums 0
     if (of <= 4) {   // a thread a row
@@ -319,9 +322,12 @@ VC_DEV void join_records(const PagedAttnArgs& a, const float* all, int rec_rows,
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int idx = base + u * THREADS;
-                if (idx < total)
-                    *reinterpret_cast<uint2*>(out(idx / (DH / 4)) + 4 * (idx % (DH / 4))) =
-                        make_uint2(pack_out<F16>(a.widen, v[u].x, v[u].y), pack_out<F16>(a.widen, v[u].z, v[u].w));
+                if (idx >= total) continue;
+                float y[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+                if (odd_results(y) && factor[idx / (DH / 4)] == factor[idx / (DH / 4)])   // (factors are NaN where the sum is)
+                    decide_odd(y, odd(idx / (DH / 4), 4 * (idx % (DH / 4))));
+                *reinterpret_cast<uint2*>(out(idx / (DH / 4)) + 4 * (idx % (DH / 4))) =
+                    make_uint2(pack_out<F16>(a.widen, y[0], y[1]), pack_out<F16>(a.widen, y[2], y[3]));
             }
         }
     };

@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(FrameShape<DH>::THREADS, 1)
             const SeenValues<DH> values = seen_values<DH>(a.c, me.s, at0.j, me.p);
 #pragma unroll 1
             for (int d = 4 * lane; d < DH; d += 128) {
-                const float4 z = odd_values<DH, F16>(values, d);
+                const float4 z = odd_values_call<DH, F16>(values, d);
 #pragma unroll 1
                 for (int r = 0; r < G; ++r) {
                     if (!((odd >> r) & 1u)) continue;
@@ -508,7 +508,8 @@ __global__ void __launch_bounds__(FrameShape<DH>::THREADS, 1)
     __syncthreads();
     const int rec_floats = (G * (DH + 2) + 3) & ~3;   // 16-byte aligned records
     auto decide = [&](float (&v)[4], float sum, const int4& seg, int d) {   // results of a segment's row (times its sum or not)
-        if (odd_results(v) && sum == sum) decide_odd<DH, F16>(v, seen_values<DH>(a.c, line[seg.z].s, seg.w, line[seg.z].p), d);
+        if (odd_results(v) && sum == sum)
+            decide_odd(v, odd_values_call<DH, F16>(seen_values<DH>(a.c, line[seg.z].s, seg.w, line[seg.z].p), d));
     };
     const int C0 = range_start(range0), C1 = range_start(range0 + kWarps);
     auto join_warps = [&](const int4& seg) {

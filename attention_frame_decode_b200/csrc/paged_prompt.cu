@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     __shared__ uint64_t full[ST], empty[ST], clean[ST / 2], work_ready[2], work_taken[2], q_ready[2], q_free, o_free[2], drained;
     __shared__ uint64_t s_full[S::TILES], p_ready[S::TILES], o_done[S::TILES];
     __shared__ uint32_t tmem_base, block_mapped[16];   // of block g at g % 16: at most ST / 2 are in the ring
-    __shared__ int odd_values[4];
+    __shared__ int odd_piece[4];
     __shared__ TileOrder order;
     __shared__ PromptWork work[4];       // piece t at t % 4: written again when the rows are done with it
     __shared__ float top_x[S::ROWS], l_part[S::SHARES][S::ROWS];   // a row's highest score, between its threads; their sums
@@ -475,7 +475,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 if (t > 1) wait(&work_taken[t & 1], (t - 2) >> 1);
                 if (lane == 0) {
                     work[t & 3] = w;
-                    odd_values[t & 3] = 0;
+                    odd_piece[t & 3] = 0;
                     mbar_arrive(&work_ready[t & 1]);
                 }
                 if (t > 0) wait(&q_free, t - 1);   // the scores of the piece before are complete
@@ -543,7 +543,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                             sweep(clip(a.c.sinks), clip(from), true);
                             sweep(clip(from > a.c.sinks ? from : a.c.sinks), clip(to), false);
                         }
-                        if (odd) odd_values[t & 3] = 1;
+                        if (odd) odd_piece[t & 3] = 1;
                         fence_proxy_async();
                     }
                     __syncwarp();
@@ -688,7 +688,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 wait(&o_done[i], gi - 1);
                 tc_fence_after();
             }
-            const bool odd = odd_values[t & 3] != 0;
+            float odd = odd_piece[t & 3] != 0;   // not 0: infinities or NaN, taken out of the values, or in the results (NaN)
 #pragma unroll 1
             for (int c = half * (DH / S::SHARES); c < (half + 1) * (DH / S::SHARES); c += 32) {
                 float v[32];
@@ -704,18 +704,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 if (!ok) continue;
 #pragma unroll
                 for (int e = 0; e < 32; ++e) v[e] *= inv;
-                if (odd && in)   // the infinities and NaN that were taken out of the values, to the rows that see them
-                    for (int n = 0; n < nb; ++n)
-                        for (int u = 0; u < S::KEYS; ++u) {
-                            const int p = w.kb.block(w.b0 + n) * S::KEYS + u;
-                            if (p > me.p || !(a.c.window == 0 || p < a.c.sinks || p > me.p - a.c.window)) continue;
-                            const int e = page_of(a.c, w.s, p >> a.c.page_shift);
-                            if (e < 0) continue;
-                            const uint16_t* x = a.c.v + (((size_t)e * a.c.Hk + w.j) * a.c.page + (p & (a.c.page - 1))) * DH + c;
 #pragma unroll
-                            for (int q = 0; q < 32; ++q)
-                                if ((x[q] & exponent_mask<F16>()) == exponent_mask<F16>()) v[q] += unpack16<F16>(x[q]);
-                        }
+                for (int e = 0; e < 32; ++e) odd = fmaf(v[e], 0.0f, odd);
                 if (of == 1) {
                     // four lanes exchange the 16-byte pieces of their rows, so that each writes 64 bytes of a row together
                     uint4 x[4];
@@ -736,6 +726,25 @@ __global__ void __launch_bounds__(kPThreads, 1)
 #pragma unroll
                     for (int e = 0; e < 32; e += 4)
                         __stcg(reinterpret_cast<float4*>(rec + at * DH + c + e), make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]));
+                }
+            }
+            if (__any_sync(0xffffffffu, odd != 0.0f)) {   // the rows that see them get them
+                __threadfence_block();
+                __syncwarp();   // (lanes write one another's rows)
+                if (odd != 0.0f && in && ok && l == l) {
+                    const SeenValues<DH> values = seen_values<DH>(a.c, w.s, w.j, me.p);
+#pragma unroll 1
+                    for (int d = half * (DH / S::SHARES); d < (half + 1) * (DH / S::SHARES); d += 4) {
+                        const float4 z = odd_values<DH, F16>(values, d);
+                        float* r4 = rec + at * DH + d;
+                        uint16_t* o4 = a.out + mine + d;
+                        auto put = [&](int u, float x) {
+                            if (x == 0.0f) return;
+                            if (of > 1) __stcg(r4 + u, x);
+                            else o4[u] = (uint16_t)pack_out<F16>(a.widen, x, 0.0f);
+                        };
+                        put(0, z.x); put(1, z.y); put(2, z.z); put(3, z.w);
+                    }
                 }
             }
             if (of > 1 && half == 0 && in) {
@@ -760,7 +769,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     join_records<DH, F16, kPThreads>(a, a.partial + (size_t)(w.record - w.record % w.splits) * (S::ROWS * (DH + 2)), S::ROWS, w.of,
                                      0, w.r1 - w.r0, reinterpret_cast<float*>(smem), [&](int r) {
                                          return a.out + (size_t)((first + r) / G) * a.out_ld + (size_t)(w.j * G + (first + r) % G) * DH;
-                                     });
+                                     }, [&](int r, int d) { return odd_values<DH, F16>(seen_values<DH>(a.c, w.s, w.j, w.p0 + (w.r0 + r) / G), d); });
 }
 
 template <int DH, bool F16>

@@ -83,6 +83,30 @@ def test_frames_of_one_chunk_and_of_many_sessions():
     check(s, s.run(single=True), [(0, 0), (1, 0), (600, 0)])
 
 
+def test_frames_of_more_heads_than_the_frames_form_takes():
+    for dtype, scale in (("bf16", 0.0), ("fp16", 0.0), ("fp16", 30.0)):
+        s = Setup((34, 2, 64), 64, dtype, 129, 5, [800, 40], [1, 1], seed=34)
+        spread(s)
+        check(s, s.run(single=True, scale=scale), [(0, 0), (1, 0)], scale or None)
+
+
+PROMPTS = [((4, 2, 64), 32, 0, 0, 500, 90), ((40, 8, 128), 64, 120, 4, 300, 150), ((8, 2, 32), 16, 100, 30, 300, 60),
+           ((8, 4, 256), 32, 0, 0, 400, 70), ((8, 2, 64), 64, 0, 0, 12000, 5), ((8, 2, 128), 64, 0, 0, 12000, 5),
+           ((8, 2, 32), 64, 0, 0, 12000, 5), ((8, 1, 256), 64, 0, 0, 12000, 5), ((8, 2, 64), 16, 0, 0, 1000, 3),
+           ((8, 2, 128), 32, 0, 0, 2000, 1), ((2, 2, 64), 32, 0, 0, 0, 600), ((300, 1, 64), 32, 0, 0, 200, 3)]
+
+
+@pytest.mark.parametrize("scale", [0.0, 30.0])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("heads,page,window,sinks,ctx,rows", PROMPTS, ids=str)
+def test_prompts(heads, page, window, sinks, ctx, rows, dtype, scale):
+    """blocks that all rows see, blocks at the edges, ranges of keys joined at the end or by a launch of their own"""
+    s = Setup(heads, page, dtype, window, sinks, [ctx, 40], [rows, 33], seed=35)
+    spread(s)
+    out = s.run(scale=scale)
+    check(s, out, [(0, r) for r in sorted({0, rows // 3, rows // 2, rows - 1})] + [(1, 0), (1, 32)], scale or None)
+
+
 @pytest.mark.parametrize("single", [True, False])
 @pytest.mark.parametrize("heads", [(8, 2, 64), (4, 2, 128), (8, 2, 32)])
 def test_a_key_that_is_not_a_number_spoils_its_heads_alone(heads, single):
