@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(TileShape<DH, ROWS>::THREADS) paged_tile_kerne
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-    bool cleaned = false;   // infinities or NaN were taken out of some block's values
+    bool cleaned = false;   // infinities or NaN that some row sees were taken out of a block's values
     const int pr[2] = {o.p0 + (r0 + 16 * warp + g) / G, o.p0 + (r0 + 16 * warp + g + 8) / G};
     const int mi = lane >> 3, lr = lane & 7;
 
@@ -198,12 +198,15 @@ __global__ void __launch_bounds__(TileShape<DH, ROWS>::THREADS) paged_tile_kerne
             for (int idx = tid; idx < kTK * (DH / 2); idx += kTThreads)
                 odd |= nonfinite2<F16>(*reinterpret_cast<const uint32_t*>(Vs + (idx / (DH / 2)) * SK + 2 * (idx % (DH / 2))));
             if (__syncthreads_or(odd)) {
-                cleaned = true;
+                bool some = false;   // (what no page or no later row covers is 0 already)
                 for (int idx = tid; idx < kTK * DH; idx += kTThreads) {
                     uint16_t* p = Vs + (idx / DH) * SK + idx % DH;
-                    if (nonfinite1<F16>(*p)) *p = 0;
+                    if (!nonfinite1<F16>(*p)) continue;
+                    *p = 0;
+                    const int t = t0 + idx / DH;
+                    some |= a.c.window == 0 || t < a.c.sinks || t > p_lo - a.c.window;
                 }
-                __syncthreads();
+                if (__syncthreads_or(some)) cleaned = true;
             }
         }
         // P in 16 bits, as the matrix instruction takes it: 2^-9 (bf16) or 2^-12 (fp16) of each weight
