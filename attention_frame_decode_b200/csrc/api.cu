@@ -118,7 +118,8 @@ struct Workspace {
     FrameProgram* prog;  // the frame kernel's program (device copy)
     int* fk_sync;        // [0] barrier arrivals, [1] abort flag of the frame kernel
     uint16_t* qkv;       // a step's queries, keys and values for a paged cache
-    int *pos, *slots, *pf_pos;   // a paged step's rows: positions granted, slots; a prefill's (kPagedPrefillInts)
+    int *pos, *named, *slots;   // a paged step's rows: positions granted, slots as the call names them, slots in range
+    int* pf_pos;                // a paged prefill's arguments (kPagedPrefillInts)
 };
 
 struct GraphKey {
@@ -161,7 +162,7 @@ struct vc_backbone {
     struct Graph {
         cudaGraph_t graph;
         cudaGraphExec_t exec;
-        cudaGraphNode_t input_node;   // the step-input kernel (the graph's only root)
+        cudaGraphNode_t input_node;   // the step-input kernel
         const void* x;                // frame input the input node currently reads
     };
     std::map<GraphKey, Graph> graphs;
@@ -252,7 +253,7 @@ extern "C" size_t vc_workspace_bytes(const vc_config* cfg) {
     add(sizeof(FrameProgram));                // the frame kernel's program
     add(256);                                 // its barrier and abort words
     add((size_t)B * D.qkv_rows * 2 + 16);     // a paged step's queries, keys and values
-    add((32 + kPagedPrefillInts) * 4);        // positions and slots of a paged cache's calls
+    add((48 + kPagedPrefillInts) * 4);        // positions and slots of a paged cache's calls
     return align_up(total, 256);
 }
 
@@ -295,9 +296,10 @@ static void carve(vc_backbone* h, uint8_t* base) {
     W.prog = (FrameProgram*)take(sizeof(FrameProgram));
     W.fk_sync = (int*)take(256);
     W.qkv = (uint16_t*)take((size_t)B * D.qkv_rows * 2 + 16);
-    W.pos = (int*)take((32 + kPagedPrefillInts) * 4);
-    W.slots = W.pos + 16;
-    W.pf_pos = W.pos + 32;
+    W.pos = (int*)take((48 + kPagedPrefillInts) * 4);
+    W.named = W.pos + 16;
+    W.slots = W.pos + 32;
+    W.pf_pos = W.pos + 48;
 }
 
 static bool qmat_ok(const vc_qmat& m, int fmt, int group, int N, int K) {
@@ -427,8 +429,22 @@ struct StepSink {
 struct LaunchSink : StepSink {
     cudaStream_t s;
     int pdl;
-    LaunchSink(cudaStream_t s_, int pdl_) : s(s_), pdl(pdl_) {}
-    cudaError_t input(const InputArgs& a) override { return launch_input(a, s); }
+    cudaGraphNode_t* input_node;   // where the stream is capturing: gets the input kernel's node
+    LaunchSink(cudaStream_t s_, int pdl_, cudaGraphNode_t* node = nullptr) : s(s_), pdl(pdl_), input_node(node) {}
+    cudaError_t input(const InputArgs& a) override {
+        cudaError_t e = launch_input(a, s);
+        if (e != cudaSuccess || !input_node) return e;
+        cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;   // the last node of a chain of launches is this one
+        unsigned long long id = 0;
+        cudaGraph_t g = nullptr;
+        const cudaGraphNode_t* last = nullptr;
+        size_t n = 0;
+        e = cudaStreamGetCaptureInfo(s, &st, &id, &g, &last, &n);
+        if (e != cudaSuccess) return e;
+        if (st != cudaStreamCaptureStatusActive || n != 1) return cudaErrorUnknown;
+        *input_node = last[0];
+        return cudaSuccess;
+    }
     cudaError_t gemv(const GemvLaunch& l, const GemvArgs& a) override { return launch_gemv(l, a, s); }
     cudaError_t mamba(const MambaStepArgs& a) override { return launch_mamba_step(a, pdl, s); }
     cudaError_t attn(const AttnArgs& a) override { return launch_attn_decode(a, pdl, s); }
@@ -677,30 +693,38 @@ static cudaError_t run_frame(vc_backbone* h, const void* x, int B, const int32_t
     return launch_frame(g, fp, h->num_sms, s);
 }
 
+// the launches of a step; over a paged cache those that ask for the frame's positions come first (slots: the call's, in
+// W.named and W.slots by now)
+static cudaError_t launch_step(vc_backbone* h, const void* x, int B, const int32_t* slots, const vc_state* st, int32_t* tt,
+                               int32_t* tf, const vc_token_embeddings* emb, const vc_paged_kv* kv, LaunchSink& sink) {
+    if (kv) {
+        const cudaError_t e = launch_paged_resize(paged_kernel_kv(*kv), paged_carve(*kv, kv->workspace), B,
+                                                  slots ? h->ws.named : nullptr, nullptr, 1, h->ws.pos, sink.s);
+        if (e != cudaSuccess) return e;
+        if (slots) slots = h->ws.slots;   // a row whose slot is out of range got no position: it is skipped, and reads slot 0
+    }
+    return record_step(h, x, B, slots, st, tt, tf, emb, kv, sink);
+}
+
 static vc_status run_step(vc_backbone* h, const void* x, int B, const int32_t* slots, const vc_state* st, int32_t* tt,
                           int32_t* tf, cudaStream_t s, const vc_token_embeddings* emb = nullptr,
                           const vc_paged_kv* kv = nullptr) {
-    if (kv) {
-        // the frame's positions, outside the graph: the page calls' kernels are not among its nodes
-        cudaError_t e = launch_paged_resize(paged_kernel_kv(*kv), paged_carve(*kv, kv->workspace), B, slots, nullptr, 1,
-                                            h->ws.pos, s);
-        if (e == cudaSuccess && slots) e = launch_step_slots(slots, B, h->D.slots, h->ws.slots, s);
-        if (e != cudaSuccess) return cuda_fail(e, "vc_step_paged resize");
-        if (slots) slots = h->ws.slots;   // a row whose slot is out of range got no position: it is skipped, and reads slot 0
-    }
     if (h->use_frame && !kv) {
         const cudaError_t e = run_frame(h, x, B, slots, st, tt, tf, s, emb);
         if (e == cudaSuccess) return VC_OK;
         if (e != cudaErrorNotSupported) return cuda_fail(e, "vc_step frame kernel");
     }
+    // the call's slots to where the graph reads them (any tensor of slots goes with one graph); no session is touched
+    auto take_slots = [&] { return kv && slots ? launch_step_slots(slots, B, h->D.slots, h->ws.named, h->ws.slots, s) : cudaSuccess; };
     if (!h->use_graph) {
+        CK(take_slots());
         LaunchSink ls(s, h->use_pdl);
-        cudaError_t e = record_step(h, x, B, slots, st, tt, tf, emb, kv, ls);
+        cudaError_t e = launch_step(h, x, B, slots, st, tt, tf, emb, kv, ls);
         return e == cudaSuccess ? VC_OK : cuda_fail(e, "vc_step launch");
     }
     GraphKey key;
     memset(&key, 0, sizeof(key));
-    key.B = B; key.slots = slots; key.st = *st; key.tt = tt; key.tf = tf;
+    key.B = B; key.slots = kv && slots ? h->ws.slots : slots; key.st = *st; key.tt = tt; key.tf = tf;
     key.th = h->tap_hidden; key.tl = h->tap_logits; key.tz = h->tap_zx;
     if (emb) { key.et = emb->emb_text; key.ef = emb->emb_func; }
     if (kv) {   // without the struct's padding
@@ -713,8 +737,9 @@ static vc_status run_step(vc_backbone* h, const void* x, int B, const int32_t* s
         if (h->graphs.size() > 64) clear_graphs(h);
         cudaStream_t cs = h->capture_stream;
         CK(cudaStreamBeginCapture(cs, cudaStreamCaptureModeThreadLocal));
-        LaunchSink ls(cs, h->use_pdl);
-        cudaError_t e = record_step(h, x, B, slots, st, tt, tf, emb, kv, ls);
+        cudaGraphNode_t input = nullptr;
+        LaunchSink ls(cs, h->use_pdl, &input);
+        cudaError_t e = launch_step(h, x, B, slots, st, tt, tf, emb, kv, ls);
         cudaGraph_t g = nullptr;
         cudaError_t e2 = cudaStreamEndCapture(cs, &g);
         if (e != cudaSuccess) {
@@ -722,22 +747,13 @@ static vc_status run_step(vc_backbone* h, const void* x, int B, const int32_t* s
             return cuda_fail(e, "vc_step capture");
         }
         if (e2 != cudaSuccess) return cuda_fail(e2, "cudaStreamEndCapture");
-        // the input kernel is the only root node
-        size_t nroots = 0;
-        CK(cudaGraphGetRootNodes(g, nullptr, &nroots));
-        if (nroots != 1) {
-            cudaGraphDestroy(g);
-            return cuda_fail(cudaErrorUnknown, "vc_step graph shape");
-        }
-        cudaGraphNode_t root;
-        CK(cudaGraphGetRootNodes(g, &root, &nroots));
         cudaGraphExec_t ex = nullptr;
         e = cudaGraphInstantiate(&ex, g, 0);
         if (e != cudaSuccess) {
             cudaGraphDestroy(g);
             return cuda_fail(e, "cudaGraphInstantiate");
         }
-        it = h->graphs.emplace(key, vc_backbone::Graph{g, ex, root, x}).first;
+        it = h->graphs.emplace(key, vc_backbone::Graph{g, ex, input, x}).first;
     }
     vc_backbone::Graph& G = it->second;
     if (G.x != x) {
@@ -751,6 +767,7 @@ static vc_status run_step(vc_backbone* h, const void* x, int B, const int32_t* s
         CK(cudaGraphExecKernelNodeSetParams(G.exec, G.input_node, &kp));
         G.x = x;
     }
+    CK(take_slots());
     CK(cudaGraphLaunch(G.exec, s));
     return VC_OK;
 }

@@ -60,13 +60,15 @@ __global__ void input_kernel(const InputArgs a) {
     }
 }
 
-__global__ void step_slots_kernel(const int* slots, int B, int n_slots, int* out) {
+__global__ void step_slots_kernel(const int* slots, int B, int n_slots, int* named, int* out) {
     const int b = threadIdx.x;
-    if (b < B) out[b] = (unsigned)slots[b] < (unsigned)n_slots ? slots[b] : 0;
+    if (b >= B) return;
+    named[b] = slots[b];
+    out[b] = (unsigned)slots[b] < (unsigned)n_slots ? slots[b] : 0;
 }
 
-cudaError_t launch_step_slots(const int* slots, int B, int n_slots, int* out, cudaStream_t s) {
-    step_slots_kernel<<<1, 32, 0, s>>>(slots, B, n_slots, out);
+cudaError_t launch_step_slots(const int* slots, int B, int n_slots, int* named, int* out, cudaStream_t s) {
+    step_slots_kernel<<<1, 32, 0, s>>>(slots, B, n_slots, named, out);
     return cudaGetLastError();
 }
 

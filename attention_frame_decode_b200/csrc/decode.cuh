@@ -65,8 +65,8 @@ struct AttnArgs {
 static constexpr int kAttnSplit = 128;  // keys per split
 
 cudaError_t launch_input(const InputArgs& a, cudaStream_t s);
-// a paged step's session slots, those out of range (rows that are skipped) replaced by 0
-cudaError_t launch_step_slots(const int* slots, int B, int n_slots, int* out, cudaStream_t s);
+// a paged step's session slots as they are, and with those out of range (rows that are skipped) replaced by 0
+cudaError_t launch_step_slots(const int* slots, int B, int n_slots, int* named, int* out, cudaStream_t s);
 cudaError_t launch_mamba_step(const MambaStepArgs& a, int pdl, cudaStream_t s);
 cudaError_t launch_attn_decode(const AttnArgs& a, int pdl, cudaStream_t s);
 

@@ -1,0 +1,56 @@
+"""What the backbone's calls over a paged cache launch, and what they leave behind when the CUDA runtime fails, on a
+runtime without a GPU."""
+import pytest
+
+import fake_runtime
+import synth
+
+
+@pytest.fixture(scope="module")
+def lib(tmp_path_factory):
+    return fake_runtime.build(tmp_path_factory.mktemp("fake"))
+
+
+@pytest.fixture
+def host(lib):
+    h = fake_runtime.Host(lib, synth.tiny_config())
+    yield h
+    h.close()
+
+
+def plain(x):
+    return x.split("<")[0].split(" ")[0]
+
+
+@pytest.mark.parametrize("slots", [False, True])
+def test_a_step_asks_for_its_positions_first(host, slots):
+    assert host.step(slots) == host.vc.VC_OK
+    first = host.launches()
+    names = [plain(x) for x in first]
+    assert names[:3 + slots] == ["step_slots_kernel"] * slots + ["paged_resize_kernel", "paged_copy_kernel", "input_kernel"]
+    assert names.count("paged_frame_kernel") == host.cfg.pattern.count("*")
+    assert host.step(slots) == host.vc.VC_OK and host.launches() == first      # from the graph that is there
+    host.option(host.vc.OPT_GRAPH, 0)
+    assert host.step(slots) == host.vc.VC_OK and host.launches() == first      # directly
+
+
+def test_any_tensor_of_slots_goes_with_one_graph(host):
+    assert host.step(slots=True) == host.vc.VC_OK
+    host.launches()
+    host.slots = host.pointer()
+    host.fail("cudaStreamBeginCapture", 1)
+    assert host.step(slots=True) == host.vc.VC_OK and len(host.launches()) > 4
+
+
+@pytest.mark.parametrize("function,nth", [("cudaStreamBeginCapture", 1), ("cudaLaunchKernel", 1), ("cudaLaunchKernel", 2),
+                                          ("cudaLaunchKernelExC", 1), ("cudaLaunchKernelExC", 4),
+                                          ("cudaLaunchKernelExC", 9), ("cudaFuncSetAttribute", 2), ("cudaStreamEndCapture", 1),
+                                          ("cudaGraphInstantiate", 1), ("cudaGraphLaunch", 1)])
+@pytest.mark.parametrize("slots", [False, True])
+def test_a_step_that_fails_on_the_host_touches_no_session(host, function, nth, slots):
+    """no length is one ahead of its session: the same call can be made again"""
+    host.fail(function, nth)
+    assert host.step(slots) == host.vc.VC_ERR_CUDA
+    assert [x for x in host.launches() if x != "step_slots_kernel"] == []
+    assert host.step(slots) == host.vc.VC_OK
+    assert "paged_resize_kernel" in host.launches()
