@@ -569,19 +569,23 @@ void carve_mixer(PfMixer& m, uint8_t* base) {
     m.status = (int*)take(4);
 }
 
+// the Mamba-2 shapes that prefill_mixer covers
+static bool prefill_mixer_supported(int H, int P, int N, int G, int W, int NG) {
+    return P % 8 == 0 && P <= 128 && N % 16 == 0 && N <= 256 && H % G == 0 && W <= 8 && NG <= 32 &&
+           ssd_layout(N, P).total <= 227 * 1024;
+}
+
 cudaError_t prefill_mixer(const PfMixer& m, cudaStream_t s) {
     const int T = m.T, E = m.E, Cx = m.Cx, H = m.H, P = m.P, N = m.N, W = m.W;
     const int zxw = E + Cx + H;
     const int nch = (T + kChunk - 1) / kChunk;
     const vc_layer_weights& Lw = *m.Lw;
-    if (P % 8 || P > 128 || N % 16 || N > 256 || H % m.G) return cudaErrorNotSupported;
+    if (!prefill_mixer_supported(H, P, N, m.G, W, m.NG)) return cudaErrorNotSupported;
     const SsdLayout SL = ssd_layout(N, P);
-    if (SL.total > 227 * 1024) return cudaErrorNotSupported;
     cudaError_t e = cudaFuncSetAttribute(pf_ssd_out_mma_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)SL.total);
     if (e != cudaSuccess) return e;
     if ((e = cudaMemsetAsync(m.ring, 0, (size_t)W * Cx * 2, s)) != cudaSuccess) return e;
-    if (W > 8 || m.NG > 32) return cudaErrorNotSupported;
     const dim3 cg((Cx + 255) / 256, (T + kConvTF - 1) / kConvTF);
     if (W == 4 && E % 4 == 0 && Cx % 4 == 0 && zxw % 4 == 0)
         pf_conv4x4_kernel<<<dim3((Cx / 4 + 255) / 256, (T + kConvTF - 1) / kConvTF), 256, 0, s>>>(
@@ -689,6 +693,7 @@ cudaError_t run_prefill(const PrefillCtx& c, const uint16_t* x, int T, int slot,
     const int zxw = E + Cx + H;
     if (T < 1 || T > c.cap) return cudaErrorInvalidValue;
     if (strchr(c.cfg->pattern, '*') && (c.Dh % 32 || c.Dh > 256)) return cudaErrorNotSupported;
+    if (strchr(c.cfg->pattern, 'M') && !prefill_mixer_supported(H, P, N, c.G, W, c.NG)) return cudaErrorNotSupported;
     const PfBufs b = carve_pf(c.ws, T, d, E, Cx, H, P, N, c.Hq, c.Hk, c.Dh, c.F, nullptr);
     const int f16 = c.cfg->wfmt != VC_W_BF16;   // quantized weights: fp16 operands, as in the decode GEMV
     PfGemm gemm{c, b, f16, s, {}, 0};

@@ -54,3 +54,11 @@ def test_a_step_that_fails_on_the_host_touches_no_session(host, function, nth, s
     assert [x for x in host.launches() if x != "step_slots_kernel"] == []
     assert host.step(slots) == host.vc.VC_OK
     assert "paged_resize_kernel" in host.launches()
+
+
+@pytest.mark.parametrize("shape", [dict(ssm_head_dim=12, ssm_heads=32), dict(ssm_state=20)], ids=str)
+def test_a_prefill_of_shapes_that_it_does_not_cover_runs_nothing(lib, shape):
+    h = fake_runtime.Host(lib, synth.tiny_config(**shape))
+    assert h.prefill() == h.vc.VC_ERR_UNSUPPORTED and h.launches() == []
+    assert h.lib.vc_prefill(h.h, h.x, 20, 0, h.state, None) == h.vc.VC_ERR_UNSUPPORTED and h.launches() == []
+    h.close()
