@@ -693,13 +693,29 @@ static cudaError_t run_frame(vc_backbone* h, const void* x, int B, const int32_t
     return launch_frame(g, fp, h->num_sms, s);
 }
 
+// what a backbone keeps of its sessions beside the pages
+static PagedFrames paged_frames(const Dims& D, const vc_state& st) {
+    PagedFrames f{};
+    auto part = [&](void* base, int64_t bytes, int outer) {
+        f.parts[f.n_parts++] = vc_session_part{base, bytes, bytes, bytes * D.slots, outer};
+    };
+    f.count = st.ctx_len;
+    part(st.ctx_len, 4, 1);
+    if (D.nm) {
+        part(st.ssm, (int64_t)D.H * D.P * D.N * 4, D.nm);
+        part(st.conv, (int64_t)D.W * D.Cx * 2, D.nm);
+    }
+    return f;
+}
+
 // the launches of a step; over a paged cache those that ask for the frame's positions come first (slots: the call's, in
 // W.named and W.slots by now)
 static cudaError_t launch_step(vc_backbone* h, const void* x, int B, const int32_t* slots, const vc_state* st, int32_t* tt,
                                int32_t* tf, const vc_token_embeddings* emb, const vc_paged_kv* kv, LaunchSink& sink) {
     if (kv) {
+        const PagedFrames frames = paged_frames(h->D, *st);
         const cudaError_t e = launch_paged_resize(paged_kernel_kv(*kv), paged_carve(*kv, kv->workspace), B,
-                                                  slots ? h->ws.named : nullptr, nullptr, 1, h->ws.pos, sink.s);
+                                                  slots ? h->ws.named : nullptr, nullptr, 1, h->ws.pos, sink.s, &frames);
         if (e != cudaSuccess) return e;
         if (slots) slots = h->ws.slots;   // a row whose slot is out of range got no position: it is skipped, and reads slot 0
     }

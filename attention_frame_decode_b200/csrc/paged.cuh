@@ -16,11 +16,11 @@ struct PagedKv {
 };
 
 struct PagedWorkspace {
-    int* head;        // [0] copies listed by a resize or fork, [1], [2] a compaction's moves and live pages
+    int* head;        // [0] copies listed by a resize or fork, [1], [2] a compaction's moves and live pages, [3] rows to clear
     int* ticket;      // work handed out by attention (zero between calls)
     int* merge;       // arrival counters of split attention work [kMaxSplitCtas] (zero between calls)
     int* copies;      // [seqs][3]: source page, destination page, positions to copy
-    int* ok;          // [seqs]: rows of a fork that are done
+    int* ok;          // [seqs]: rows of a fork that are done, of a step whose sessions start anew
     int* first;       // [seqs]: the lowest row that names a session
     int4* rows;       // [seqs]: a resize's rows
     int* need;        // [seqs][2]: a row's first page request and how many it has
@@ -85,8 +85,16 @@ cudaError_t launch_paged_prompts(const PagedAttnArgs& a, cudaStream_t s);
 // one row per session, appended and attended in one launch; cudaErrorNotSupported: the shape is not covered
 cudaError_t launch_paged_frames(const PagedAttnArgs& a, cudaStream_t s);
 
+// the state that a backbone keeps beside the pages: frames of each session, and dense parts (frames among them)
+struct PagedFrames {
+    const int* count;
+    vc_session_part parts[3];
+    int n_parts;
+};
+// frames: null, or a backbone's step: a session that starts at position 0 with frames behind it (it was ended) starts anew,
+// its parts zero
 cudaError_t launch_paged_resize(const PagedKv& c, const PagedWorkspace& w, int n, const int* seqs, const int* lens,
-                                int add, int* pos, cudaStream_t s);
+                                int add, int* pos, cudaStream_t s, const PagedFrames* frames = nullptr);
 cudaError_t launch_paged_fork(const PagedKv& c, const PagedWorkspace& w, int n, const int* src, const int* dst,
                               const vc_session_part* parts, int n_parts, int* done, cudaStream_t s);
 cudaError_t launch_paged_compact(const PagedKv& c, const PagedWorkspace& w, int* live, cudaStream_t s);

@@ -129,9 +129,10 @@ VC_DEV int4 resize_row(const PagedKv& c, const int* seqs, const int* lens, int a
 }
 
 __global__ void __launch_bounds__(kPT) paged_resize_kernel(const PagedKv c, const PagedWorkspace w, int n,
-                                                           const int* seqs, const int* lens, int add, int* pos) {
+                                                           const int* seqs, const int* lens, int add, int* pos,
+                                                           const int* frames) {
     __shared__ int warp_sums[32];
-    __shared__ int copies;
+    __shared__ int copies, anew;
     const int tid = threadIdx.x;
     pdl_trigger();
     if (seqs) mark_first(seqs, n, c.seqs, w.first);
@@ -168,7 +169,7 @@ __global__ void __launch_bounds__(kPT) paged_resize_kernel(const PagedKv c, cons
             }
         }
     }
-    if (tid == 0) copies = 0;
+    if (tid == 0) copies = anew = 0;
     __syncthreads();
 
     // 2. requests, numbered in row order; w.need[i]: the row's first request, w.need[n + i]: how many
@@ -230,10 +231,17 @@ __global__ void __launch_bounds__(kPT) paged_resize_kernel(const PagedKv c, cons
             if (granted) c.len[s] = to;
             if (pos) pos[i] = granted ? min(have, to) : -1;
             if (!granted) atomicOr(c.status, s < 0 ? VC_DEV_INVALID : VC_DEV_CAPACITY);
+            if (frames) {   // a step's session that was ended
+                w.ok[i] = granted && have == 0 && frames[s] != 0;
+                if (w.ok[i]) atomicAdd(&anew, 1);
+            }
         }
     }
     __syncthreads();
-    if (tid == 0) w.head[0] = copies;
+    if (tid == 0) {
+        w.head[0] = copies;
+        w.head[3] = anew;
+    }
 }
 
 // ------------------------------------------------------------------------------------------
@@ -348,6 +356,17 @@ VC_DEV void copy_bytes16(uint8_t* to, const uint8_t* from, int bytes) {
     }
 }
 
+// bytes of one session (a multiple of 4) to zero, by the whole grid
+VC_DEV void clear_bytes(uint8_t* to, long long bytes, bool wide) {
+    const long long first = ((long long)blockIdx.x * kCopyThreads + threadIdx.x) * 16, step = (long long)gridDim.x * kCopyThreads * 16;
+    for (long long b = first; b < bytes; b += step) {
+        if (wide) *reinterpret_cast<uint4*>(to + b) = make_uint4(0u, 0u, 0u, 0u);
+        else
+            for (int q = 0; q < 16 && b + q < bytes; q += 4) *reinterpret_cast<uint32_t*>(to + b + q) = 0u;
+    }
+}
+
+// src null: a step's sessions (dst, null: row i is session i) that start anew have their parts cleared
 __global__ void __launch_bounds__(kCopyThreads) paged_copy_kernel(const PagedKv c, const PagedWorkspace w, int n,
                                                                   const int* src, const int* dst, const CopyParts parts) {
     pdl_wait();
@@ -360,6 +379,19 @@ __global__ void __launch_bounds__(kCopyThreads) paged_copy_kernel(const PagedKv 
         const size_t from = (((size_t)layer * c.pages + cp[0]) * c.Hk + j) * c.page * c.Dh;
         const size_t to = (((size_t)layer * c.pages + cp[1]) * c.Hk + j) * c.page * c.Dh;
         copy_bytes16((uint8_t*)(pool + to), (const uint8_t*)(pool + from), cp[2] * c.Dh * 2);
+    }
+    if (!src) {
+        if (parts.n == 0 || w.head[3] == 0) return;
+        for (int i = 0; i < n; ++i) {
+            if (!w.ok[i]) continue;
+            for (int k = 0; k < parts.n; ++k) {
+                const vc_session_part& p = parts.p[k];
+                uint8_t* mine = (uint8_t*)p.base + (long long)(dst ? dst[i] : i) * p.stride;
+                const bool wide = (((uintptr_t)p.base | p.bytes | p.stride | p.outer_stride) & 15) == 0;
+                for (int o = 0; o < p.outer; ++o) clear_bytes(mine + o * p.outer_stride, p.bytes, wide);
+            }
+        }
+        return;
     }
     for (int k = 0; k < parts.n; ++k) {
         const vc_session_part& p = parts.p[k];
@@ -497,14 +529,16 @@ static cudaError_t launch_after(void (*kern)(KArgs...), int grid, int threads, c
 }
 
 cudaError_t launch_paged_resize(const PagedKv& c, const PagedWorkspace& w, int n, const int* seqs, const int* lens,
-                                int add, int* pos, cudaStream_t s) {
+                                int add, int* pos, cudaStream_t s, const PagedFrames* frames) {
     int sms = 0;
     cudaError_t e = sm_count(&sms);
     if (e != cudaSuccess) return e;
-    paged_resize_kernel<<<1, kPT, 0, s>>>(c, w, n, seqs, lens, add, pos);
+    CopyParts cp{};
+    if (frames)
+        for (cp.n = 0; cp.n < frames->n_parts; ++cp.n) cp.p[cp.n] = frames->parts[cp.n];
+    paged_resize_kernel<<<1, kPT, 0, s>>>(c, w, n, seqs, lens, add, pos, frames ? frames->count : nullptr);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    return launch_after(paged_copy_kernel, sms, kCopyThreads, s, c, w, n, (const int*)nullptr, (const int*)nullptr,
-                        CopyParts{});
+    return launch_after(paged_copy_kernel, sms, kCopyThreads, s, c, w, n, (const int*)nullptr, seqs, cp);
 }
 
 cudaError_t launch_paged_fork(const PagedKv& c, const PagedWorkspace& w, int n, const int* src, const int* dst,
