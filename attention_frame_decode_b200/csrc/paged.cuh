@@ -92,7 +92,7 @@ struct PagedFrames {
     int n_parts;
 };
 // frames: null, or a backbone's step: a session that starts at position 0 with frames behind it (it was ended) starts anew,
-// its parts zero
+// its parts zero; one that holds another number of positions than frames is a bad row
 cudaError_t launch_paged_resize(const PagedKv& c, const PagedWorkspace& w, int n, const int* seqs, const int* lens,
                                 int add, int* pos, cudaStream_t s, const PagedFrames* frames = nullptr);
 cudaError_t launch_paged_fork(const PagedKv& c, const PagedWorkspace& w, int n, const int* src, const int* dst,

@@ -111,13 +111,14 @@ VC_DEV void mark_first(const int* idx, int n, int seqs, int* first) {
 // resize
 // ------------------------------------------------------------------------------------------
 // a row's session (< 0: the row is bad), its length, the length asked for (INT32_MAX: more than the columns hold)
-VC_DEV int4 resize_row(const PagedKv& c, const int* seqs, const int* lens, int add, const int* first, int i) {
+VC_DEV int4 resize_row(const PagedKv& c, const int* seqs, const int* lens, int add, const int* first, int i, const int* frames) {
     int4 r = make_int4(-1, 0, 0, 0);
     const int s = seqs ? seqs[i] : i, most = c.columns << c.page_shift;
     if ((unsigned)s >= (unsigned)c.seqs || (seqs && __ldcg(first + s) != i)) return r;
     const int have = c.len[s];
     const long long to = (long long)(lens ? lens[i] : have) + add;
     if (to < 0 || have < 0 || have > most) return r;
+    if (frames && have > 0 && frames[s] != have) return r;   // its recurrent state belongs to another position
     r.y = have;
     r.z = to <= most ? (int)to : INT32_MAX;
     // the page that is written next has to be there (it is not where a length ends in positions given up)
@@ -136,7 +137,7 @@ __global__ void __launch_bounds__(kPT) paged_resize_kernel(const PagedKv c, cons
     const int tid = threadIdx.x;
     pdl_trigger();
     if (seqs) mark_first(seqs, n, c.seqs, w.first);
-    for (int i = tid; i < n; i += kPT) w.rows[i] = resize_row(c, seqs, lens, add, w.first, i);
+    for (int i = tid; i < n; i += kPT) w.rows[i] = resize_row(c, seqs, lens, add, w.first, i, frames);
     __syncthreads();
 
     // 1. releases

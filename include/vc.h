@@ -437,7 +437,8 @@ vc_status vc_paged_attend(const vc_paged_kv* kv, int layer, const vc_attn_rows* 
  * has the reason (kv->status and state->status may be one word).  kv->len and state->ctx_len of a session start equal and go on together; a session is ended by
  * vc_paged_resize to length 0 and copied by vc_paged_fork with ssm, conv and ctx_len as parts.  The first frame in a session
  * of length 0 whose ctx_len is not 0 (one that was ended, or whose fork had no room) starts it anew: its ssm, conv and
- * ctx_len are cleared before the frame.  One kernel per
+ * ctx_len are cleared before the frame.  A session whose length is neither 0 nor its ctx_len (cut back in the cache, or forked
+ * without its parts) is skipped as a bad row (VC_DEV_INVALID): its state belongs to another position.  One kernel per
  * operation whatever VC_OPT_FRAME says; with VC_OPT_GRAPH 0 the call can be captured into a graph of the caller's.  kv's
  * workspace is in use: order the call with the other calls on kv.  After VC_ERR_CUDA the sessions are as they were, the
  * positions asked for among them; with VC_OPT_GRAPH 0 the launches before the one that failed have run, and the call's

@@ -71,3 +71,59 @@ def test_a_first_frame_keeps_a_state_that_was_put_there(cuda):
     run.bb.step_paged(x, run.st, run.cache, run.tt, run.tf)
     rows.bb.step(x, rows.st, rows.tt, rows.tf)
     assert same_row(run, rows, 0, 0)
+
+
+@pytest.mark.parametrize("graph", [0, 1])
+def test_a_state_of_another_position_is_not_stepped(cuda, graph):
+    """a session cut back in the cache alone, one forked without its parts, one whose count was changed: each is skipped
+    and stays as it is, the last goes on; with the state of their position they go on too"""
+    import attention_frame_decode_b200 as vc
+    cfg = synth.tiny_config()
+    run, alone = PagedRun(cfg, 8, 4, 64), PagedRun(cfg, 8, 4, 64)
+    run.bb.set_option(vc.OPT_GRAPH, graph)
+    run.bb.set_taps(run.hid, run.lg)
+    step = lambda r, t: r.bb.step_paged(bits(synth.frame_inputs(cfg, 8, t, 4)), r.st, r.cache, r.tt, r.tf)  # noqa: E731
+    for t in range(10):
+        step(run, t)
+        step(alone, t)
+    saved = [x.clone() for x in (run.st.ssm, run.st.conv)]
+    for t in range(10, 20):
+        step(run, t)
+        step(alone, t)
+    run.cache.resize(seqs=i32([0]), lens=i32([10]))
+    run.st.ctx_len[1] = 3
+    run.cache.resize(seqs=i32([2]), lens=i32([0]))
+    run.cache.fork(i32([3]), i32([2]))                      # pages alone
+    run.st.ctx_len[2] = 0
+    keep = [x.clone() for x in (run.st.ssm[:, :3], run.st.conv[:, :3], run.st.ctx_len[:3], run.cache.lens[:3], run.cache.table[:3])]
+    step(run, 20)
+    step(alone, 20)
+    assert run.tt.tolist()[:3] == [-1] * 3 == run.tf.tolist()[:3] and int(run.tt[3]) >= 0
+    assert same_row(run, alone, 3, 3) and int(run.cache.status[0]) == INVALID and int(run.st.status[0]) == 0
+    for a, b in zip(keep, (run.st.ssm[:, :3], run.st.conv[:, :3], run.st.ctx_len[:3], run.cache.lens[:3], run.cache.table[:3])):
+        assert torch.equal(a, b)
+    assert run.cache.lens.tolist() == [10, 20, 20, 21]
+    # the state of the position that session 0 was cut back to
+    run.st.ssm[:, 0], run.st.conv[:, 0] = saved[0][:, 0], saved[1][:, 0]
+    run.st.ctx_len[0] = 10
+    run.st.ctx_len[1] = 20
+    for t in range(10, 14):
+        step(run, t)
+        assert int(run.tt[0]) >= 0 and int(run.tt[1]) >= 0
+    assert run.cache.lens.tolist()[:2] == [14, 24] == run.st.ctx_len.tolist()[:2]
+
+
+def test_a_session_cut_back_with_its_state_repeats_its_frames(cuda):
+    cfg = synth.tiny_config()
+    run = PagedRun(cfg, 8, 1, 64)
+    for t in range(12):
+        run.bb.step_paged(bits(synth.frame_inputs(cfg, 8, t, 1)), run.st, run.cache, run.tt, run.tf)
+        if t == 6:
+            saved = run.st.ssm.clone(), run.st.conv.clone()
+        if t == 7:
+            hid = run.hid.clone()
+    run.cache.resize(lens=i32([7]))
+    run.st.ssm.copy_(saved[0]), run.st.conv.copy_(saved[1])
+    run.st.ctx_len.fill_(7)
+    run.bb.step_paged(bits(synth.frame_inputs(cfg, 8, 7, 1)), run.st, run.cache, run.tt, run.tf)
+    assert float((run.hid - hid).abs().max()) <= TOL * float(hid.square().mean().sqrt())
