@@ -520,19 +520,32 @@ __global__ void __launch_bounds__(256) pf_attn_scalar_kernel(const uint16_t* q, 
     }
 }
 
-// pos: null, or the paged cache's answer (< 0: it had no room)
-__global__ void pf_finish_kernel(int32_t* ctx_len, int slot, int T, const int* pos) {
-    ctx_len[slot] = pos && *pos < 0 ? 0 : T;
+__global__ void pf_finish_kernel(int32_t* ctx_len, int slot, int T) { ctx_len[slot] = T; }
+
+// over a paged cache: pos is its answer.  Without room (< 0) the slot stays empty, and what the frames left in its state
+// goes: n floats of ssm and m words of the ring in each of the layers, `stride` and `ring_stride` apart
+__global__ void __launch_bounds__(256) pf_paged_finish_kernel(int32_t* ctx_len, int slot, int T, const int* pos, int layers, float* ssm,
+                                                              long long n, long long stride, uint32_t* ring, int m,
+                                                              long long ring_stride) {
+    const bool room = *pos >= 0;
+    if (blockIdx.x == 0 && threadIdx.x == 0) ctx_len[slot] = room ? T : 0;
+    if (room) return;
+    for (int l = 0; l < layers; ++l) {
+        for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256) ssm[l * stride + i] = 0.0f;
+        for (int i = blockIdx.x * 256 + (int)threadIdx.x; i < m; i += (int)gridDim.x * 256) ring[l * ring_stride + i] = 0u;
+    }
 }
 
-__global__ void pf_paged_args_kernel(int* w, int slot, int T) {
+// the slot has no frames until the call's end: one that fails in between leaves a slot that no step takes
+__global__ void pf_paged_args_kernel(int* w, int slot, int T, int32_t* ctx_len) {
     w[0] = slot; w[1] = 0; w[2] = T; w[3] = -1; w[4] = 0; w[5] = T;
+    ctx_len[slot] = 0;
 }
 
 // the slot gives its pages back and asks for those of T positions
 static cudaError_t pf_paged_begin(const PrefillCtx& c, int slot, int T, cudaStream_t s) {
     int* w = c.kv_pos;
-    pf_paged_args_kernel<<<1, 1, 0, s>>>(w, slot, T);
+    pf_paged_args_kernel<<<1, 1, 0, s>>>(w, slot, T, c.ctx_len);
     cudaError_t e = cudaGetLastError();
     const PagedKv kv = paged_kernel_kv(*c.kv);
     const PagedWorkspace ws = paged_carve(*c.kv, c.kv->workspace);
@@ -772,7 +785,14 @@ cudaError_t run_prefill(const PrefillCtx& c, const uint16_t* x, int T, int slot,
         if (c.tap && (e = cudaMemcpyAsync(c.tap + (size_t)(l + 1) * T * d, b.r, rbytes, cudaMemcpyDeviceToDevice, s)))
             return e;
     }
-    pf_finish_kernel<<<1, 1, 0, s>>>(c.ctx_len, slot, T, c.kv ? c.kv_pos + 3 : nullptr);
+    if (c.kv) {
+        const long long n = (long long)H * P * N;
+        const int m = W * Cx / 2;   // (Cx is even)
+        pf_paged_finish_kernel<<<c.num_sms, 256, 0, s>>>(c.ctx_len, slot, T, c.kv_pos + 3, mi, c.ssm + slot * n, n, c.n_slots * n,
+                                                         (uint32_t*)c.conv + (long long)slot * m, m, (long long)c.n_slots * m);
+    } else {
+        pf_finish_kernel<<<1, 1, 0, s>>>(c.ctx_len, slot, T);
+    }
     return cudaGetLastError();
 }
 

@@ -450,9 +450,10 @@ vc_status vc_step_paged(vc_backbone* h, const void* x, const vc_token_embeddings
 /* Prefill as vc_prefill with the keys and values in the paged cache kv (as in vc_step_paged): the slot gives
  * its pages back, takes those of T positions and attends with the cache's window and sinks; the pages that the
  * window has left behind go back with the session's next step.  Too few free pages (known on the device only):
- * the slot is left empty, ctx_len 0, its ssm and conv without meaning, VC_DEV_CAPACITY in kv->status.  T at most
+ * the slot is left empty, its ssm, conv and ctx_len cleared, VC_DEV_CAPACITY in kv->status.  T at most
  * kv_capacity and columns * page_size (else VC_ERR_CAPACITY).  Calls on kv run one after another, so this one,
- * unlike vc_prefill, does not overlap vc_step_paged. */
+ * unlike vc_prefill, does not overlap vc_step_paged.  After VC_ERR_CUDA, where a launch failed between others, the slot holds
+ * pages and no frames (ctx_len 0): steps skip it until it is ended or prefilled again. */
 vc_status vc_prefill_paged(vc_backbone* h, const void* x, int T, int slot, const vc_state* state,
                            const vc_paged_kv* kv, vc_stream_t stream);
 

@@ -127,3 +127,24 @@ def test_a_session_cut_back_with_its_state_repeats_its_frames(cuda):
     run.st.ctx_len.fill_(7)
     run.bb.step_paged(bits(synth.frame_inputs(cfg, 8, 7, 1)), run.st, run.cache, run.tt, run.tf)
     assert float((run.hid - hid).abs().max()) <= TOL * float(hid.square().mean().sqrt())
+
+
+def test_a_slot_whose_prefill_had_no_room_is_a_fresh_one(cuda):
+    """a used slot, then one that was never used: after a prefill without room their frames are a fresh session's"""
+    cfg = synth.tiny_config()
+    run, fresh = PagedRun(cfg, 8, 3, 64, pages=4), PagedRun(cfg, 8, 3, 64)
+    x = bits(synth.prefill_inputs(cfg, 8, 64))
+    run.bb.prefill_paged(x[:20], 0, run.st, run.cache)
+    run.bb.prefill_paged(x[:16], 1, run.st, run.cache)
+    other = [t[:, 1].clone() for t in (run.st.ssm, run.st.conv)]
+    for slot in (0, 2):
+        run.bb.prefill_paged(x[:60], slot, run.st, run.cache)
+        assert int(run.cache.status[0]) == CAPACITY
+        assert run.cache.lens.tolist() == [0, 16, 0] == run.st.ctx_len.tolist()
+        assert not bool(run.st.ssm[:, slot].any()) and not bool(run.st.conv[:, slot].any())
+        assert all(torch.equal(t[:, 1], o) for t, o in zip((run.st.ssm, run.st.conv), other))
+    for t in range(3):
+        for r in (run, fresh):
+            r.bb.step_paged(bits(synth.frame_inputs(cfg, 8, t, 3)), r.st, r.cache, r.tt, r.tf)
+        assert same_row(run, fresh, 0, 0) and same_row(run, fresh, 2, 2)
+    assert run.st.ctx_len.tolist() == [3, 19, 3] == run.cache.lens.tolist()

@@ -62,3 +62,15 @@ def test_a_prefill_of_shapes_that_it_does_not_cover_runs_nothing(lib, shape):
     assert h.prefill() == h.vc.VC_ERR_UNSUPPORTED and h.launches() == []
     assert h.lib.vc_prefill(h.h, h.x, 20, 0, h.state, None) == h.vc.VC_ERR_UNSUPPORTED and h.launches() == []
     h.close()
+
+
+@pytest.mark.parametrize("nth", [6, 12, 20])
+def test_a_prefill_that_fails_between_launches_has_taken_the_slots_frames(host, nth):
+    """the slot's count is cleared before its pages change hands, and set by the last launch: no step takes it in between"""
+    assert host.prefill() == host.vc.VC_OK
+    names = [plain(x) for x in host.launches()]
+    assert names.index("pf_paged_args_kernel") < names.index("paged_resize_kernel")
+    assert names[-1] == "pf_paged_finish_kernel" and names.count("pf_paged_finish_kernel") == 1
+    host.fail("cudaLaunchKernel", nth)
+    assert host.prefill() == host.vc.VC_ERR_CUDA
+    assert "pf_paged_finish_kernel" not in [plain(x) for x in host.launches()]
