@@ -327,7 +327,7 @@ vc_status vc_gemv_noalloc_reset(vc_stream_t stream);
 /* ---- paged KV cache: windowed attention and page calls --------------------------------- */
 
 /* A KV cache in pages, shared by the sessions of a server (device memory, caller-owned).  It has what
- * sessions that run without end need next to vc_state's fixed rows: attention over a sliding window
+ * sessions that outlast kv_capacity need next to vc_state's fixed rows: attention over a sliding window
  * with a few first frames that stay visible (sinks), pages given back as the window leaves them, and
  * sessions that share the pages of a common opening context.  The backbone's attention has no
  * positional encoding ("pre-RMSNorm residual stack ..." above), so that a window needs no rotation.
@@ -344,7 +344,10 @@ vc_status vc_gemv_noalloc_reset(vc_stream_t stream);
  * 128 or 256; kv_heads divides q_heads; columns * page_size is at most 2^30; seqs * columns, seqs * kv_heads and
  * pages * kv_heads * page_size are below 2^31.  window: a query at position p sees the keys
  * t <= p with t < sinks or t > p - window; 0: every t <= p.  window and sinks stay as they are while
- * sessions hold pages.  A key whose page is not in the table is not seen. */
+ * sessions hold pages.  A key whose page is not in the table is not seen.  A column stands for its positions for good:
+ * a session has at most columns * page_size positions over its whole life, those that the window gave up among them, and
+ * more are VC_DEV_CAPACITY (an entry is 4 bytes for page_size frames: a day of 80 ms frames is 1.08 million positions, 68 KB
+ * of table at pages of 64). */
 typedef struct {
     void *k, *v;
     int32_t *table, *len, *refs, *status;
@@ -431,7 +434,7 @@ vc_status vc_paged_attend(const vc_paged_kv* kv, int layer, const vc_attn_rows* 
  * hold the previous tokens on entry), with the attention layers' keys and values in the paged cache kv in place of
  * state->k and state->v, which are not used and may be NULL.  kv: this backbone's attention layers in pattern order
  * (layers = how many, its KV and query heads and head_dim, bf16), seqs = n_slots; its window and sinks apply in every
- * layer, so that a session whose window is full goes on without an end (kv_capacity does not bound it).  The call
+ * layer, so that a session goes on past kv_capacity with the pages of its window, up to columns * page_size frames.  The call
  * first asks for the frame's position of each row as vc_paged_resize(n = B, add = 1) does; a row that gets none (no page,
  * a slot out of range or named by an earlier row) is skipped: its tokens are -1, its state and length stay, kv->status
  * has the reason (kv->status and state->status may be one word).  kv->len and state->ctx_len of a session start equal and go on together; a session is ended by

@@ -148,3 +148,30 @@ def test_a_slot_whose_prefill_had_no_room_is_a_fresh_one(cuda):
             r.bb.step_paged(bits(synth.frame_inputs(cfg, 8, t, 3)), r.st, r.cache, r.tt, r.tf)
         assert same_row(run, fresh, 0, 0) and same_row(run, fresh, 2, 2)
     assert run.st.ctx_len.tolist() == [3, 19, 3] == run.cache.lens.tolist()
+
+
+def test_a_session_at_its_tables_end(cuda):
+    """a windowed session has columns * page_size frames over its life, however few pages it holds: the next one is
+    refused and changes nothing, others go on, and ended it starts anew"""
+    cfg = synth.tiny_config()
+    run = PagedRun(cfg, 8, 2, 64, page=16, window=20, sinks=3, pages=8, columns=5)
+    run.bb.prefill_paged(bits(synth.prefill_inputs(cfg, 8, 60)), 0, run.st, run.cache)
+    step = lambda t: run.bb.step_paged(bits(synth.frame_inputs(cfg, 8, t, 2)), run.st, run.cache, run.tt, run.tf)  # noqa: E731
+    for t in range(20):
+        step(t)
+    assert run.cache.lens.tolist() == [80, 20] == run.st.ctx_len.tolist() and int(run.cache.status[0]) == 0
+    step(20)                                                # (its window gives a page back all the same)
+    assert run.tt.tolist()[0] == -1 == run.tf.tolist()[0] and int(run.tt[1]) >= 0
+    keep = [x.clone() for x in (run.st.ssm[:, 0], run.st.conv[:, 0], run.cache.table[0])]
+    held = (run.cache.table[0] >= 0).tolist()
+    for t in range(21, 24):
+        step(t)
+        assert run.tt.tolist()[0] == -1 == run.tf.tolist()[0] and int(run.tt[1]) >= 0
+    assert run.cache.lens.tolist() == [80, 24] == run.st.ctx_len.tolist()
+    assert int(run.cache.status[0]) == CAPACITY and int(run.st.status[0]) == 0
+    assert held == [True, False, False, True, True]
+    for a, b in zip(keep, (run.st.ssm[:, 0], run.st.conv[:, 0], run.cache.table[0])):
+        assert torch.equal(a, b)
+    run.cache.resize(seqs=i32([0]), lens=i32([0]))
+    step(24)
+    assert int(run.tt[0]) >= 0 and run.cache.lens.tolist() == [1, 25] == run.st.ctx_len.tolist()
