@@ -581,7 +581,7 @@ static cudaError_t record_step(vc_backbone* h, const void* x, int B, const int32
                 a.out = W.qkv; a.out_ld = D.qkv_rows; a.out_f16 = 0;
                 gl.epi = EPI_STORE;
                 if ((e = sink.gemv(gl, a)) != cudaSuccess) return e;
-                PagedAttnArgs pa = paged_rows(W.qkv, D.qkv_rows, D.Hq, D.Hk, D.Dh, W.act_o, W.ldo, act_f16);
+                PagedAttnArgs pa = paged_rows(W.qkv, D.qkv_rows, D.Hq, D.Hk, D.Dh, W.act_o, W.ldo, act_f16, h->use_pdl);
                 pa.seqs = slots; pa.pos = W.pos; pa.batch = pa.rows = B;
                 if ((e = sink.paged_attn(*kv, ai, pa)) != cudaSuccess) return e;
             } else {
@@ -715,7 +715,7 @@ static cudaError_t launch_step(vc_backbone* h, const void* x, int B, const int32
     if (kv) {
         const PagedFrames frames = paged_frames(h->D, *st);
         const cudaError_t e = launch_paged_resize(paged_kernel_kv(*kv), paged_carve(*kv, kv->workspace), B,
-                                                  slots ? h->ws.named : nullptr, nullptr, 1, h->ws.pos, sink.s, &frames);
+                                                  slots ? h->ws.named : nullptr, nullptr, 1, h->ws.pos, h->use_pdl, sink.s, &frames);
         if (e != cudaSuccess) return e;
         if (slots) slots = h->ws.slots;   // a row whose slot is out of range got no position: it is skipped, and reads slot 0
     }
@@ -862,6 +862,7 @@ static vc_status prefill(vc_backbone* h, const void* x, int T, int slot, const v
     for (int i = 0; i < 5; ++i) c.ev[i] = h->pf_ev[i];
     c.kv = kv;
     c.kv_pos = h->ws.pf_pos;
+    c.pdl = h->use_pdl;
     cudaError_t e = run_prefill(c, (const uint16_t*)x, T, slot, (cudaStream_t)stream);
     if (e == cudaErrorNotSupported) return VC_ERR_UNSUPPORTED;
     if (e == cudaErrorInvalidValue) return VC_ERR_INVALID_ARG;

@@ -52,6 +52,7 @@ struct PagedAttnArgs {
     long long q_ld, k_ld, v_ld, out_ld;
     const int *seqs, *pos, *cu_rows;
     int batch, rows, f16, num_sms;
+    int pdl;                     // 1: launches may begin while the one before ends (programmatic dependent launch)
     int widen;                   // store bf16 results in fp16's format (the input of a quantized projection)
     float scale_log2;            // scale * log2(e)
     int* merge;
@@ -64,7 +65,7 @@ struct PagedAttnArgs {
 cudaError_t paged_attend(const vc_paged_kv& kv, int layer, PagedAttnArgs a, cudaStream_t s);
 
 // rows of a fused projection [q | k | v] of ld elements a row, 1 / sqrt(Dh), results of out_ld elements a row
-PagedAttnArgs paged_rows(const uint16_t* qkv, int ld, int Hq, int Hk, int Dh, uint16_t* out, int out_ld, int widen);
+PagedAttnArgs paged_rows(const uint16_t* qkv, int ld, int Hq, int Hk, int Dh, uint16_t* out, int out_ld, int widen, int pdl);
 
 // joins the records of tiles of attention whose key blocks were split over CTAs
 struct JoinShape {
@@ -94,7 +95,7 @@ struct PagedFrames {
 // frames: null, or a backbone's step: a session that starts at position 0 with frames behind it (it was ended) starts anew,
 // its parts zero; one that holds another number of positions than frames is a bad row
 cudaError_t launch_paged_resize(const PagedKv& c, const PagedWorkspace& w, int n, const int* seqs, const int* lens,
-                                int add, int* pos, cudaStream_t s, const PagedFrames* frames = nullptr);
+                                int add, int* pos, int pdl, cudaStream_t s, const PagedFrames* frames = nullptr);
 cudaError_t launch_paged_fork(const PagedKv& c, const PagedWorkspace& w, int n, const int* src, const int* dst,
                               const vc_session_part* parts, int n_parts, int* done, cudaStream_t s);
 cudaError_t launch_paged_compact(const PagedKv& c, const PagedWorkspace& w, int* live, cudaStream_t s);

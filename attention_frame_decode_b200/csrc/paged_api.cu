@@ -71,12 +71,13 @@ static float scale_to_log2(float scale, int head_dim) {
     return (scale != 0.0f ? scale : 1.0f / sqrtf((float)head_dim)) * 1.4426950408889634f;
 }
 
-PagedAttnArgs paged_rows(const uint16_t* qkv, int ld, int Hq, int Hk, int Dh, uint16_t* out, int out_ld, int widen) {
+PagedAttnArgs paged_rows(const uint16_t* qkv, int ld, int Hq, int Hk, int Dh, uint16_t* out, int out_ld, int widen, int pdl) {
     PagedAttnArgs a{};
     a.q = qkv; a.kn = qkv + (size_t)Hq * Dh; a.vn = a.kn + (size_t)Hk * Dh; a.out = out;
     a.q_ld = a.k_ld = a.v_ld = ld; a.out_ld = out_ld;
     a.scale_log2 = scale_to_log2(0.0f, Dh);
     a.widen = widen;
+    a.pdl = pdl;
     return a;
 }
 
@@ -126,7 +127,7 @@ extern "C" vc_status vc_paged_resize(const vc_paged_kv* kv, int n, const int32_t
     if (!paged_kv_ok(kv) || n < 1 || n > kv->seqs || !aligned4(seqs) || !aligned4(lens) || !aligned4(pos))
         return VC_ERR_INVALID_ARG;
     CKP(launch_paged_resize(paged_kernel_kv(*kv), paged_carve(*kv, kv->workspace), n, seqs, lens, add, pos,
-                            (cudaStream_t)stream));
+                            1, (cudaStream_t)stream));
     return VC_OK;
 }
 
@@ -174,6 +175,7 @@ extern "C" vc_status vc_paged_attend(const vc_paged_kv* kv, int layer, const vc_
     a.seqs = r.seqs; a.pos = r.pos; a.cu_rows = r.cu_rows;
     a.batch = r.batch; a.rows = r.rows;
     a.scale_log2 = scale_to_log2(r.scale, kv->head_dim);
+    a.pdl = 1;
     CKP(paged_attend(*kv, layer, a, (cudaStream_t)stream));
     return VC_OK;
 }

@@ -325,7 +325,7 @@ static cudaError_t launch_join_t(const PagedAttnArgs& a, const JoinShape& w, cud
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[0].val.programmaticStreamSerializationAllowed = a.pdl;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return a.f16 ? cudaLaunchKernelEx(&cfg, paged_join_kernel<DH, true, BK>, a, w)

@@ -514,23 +514,23 @@ static cudaError_t sm_count(int* sms) {
     return e == cudaSuccess ? cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) : e;
 }
 
-// a launch that may begin while the one before it on the stream ends (its kernel waits for that one's results)
+// a launch that (pdl 1) may begin while the one before it on the stream ends (its kernel waits for that one's results)
 template <typename... KArgs, typename... Args>
-static cudaError_t launch_after(void (*kern)(KArgs...), int grid, int threads, cudaStream_t s, Args... args) {
+static cudaError_t launch_after(void (*kern)(KArgs...), int grid, int threads, int pdl, cudaStream_t s, Args... args) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3((unsigned)threads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[0].val.programmaticStreamSerializationAllowed = pdl;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 cudaError_t launch_paged_resize(const PagedKv& c, const PagedWorkspace& w, int n, const int* seqs, const int* lens,
-                                int add, int* pos, cudaStream_t s, const PagedFrames* frames) {
+                                int add, int* pos, int pdl, cudaStream_t s, const PagedFrames* frames) {
     int sms = 0;
     cudaError_t e = sm_count(&sms);
     if (e != cudaSuccess) return e;
@@ -539,7 +539,7 @@ cudaError_t launch_paged_resize(const PagedKv& c, const PagedWorkspace& w, int n
         for (cp.n = 0; cp.n < frames->n_parts; ++cp.n) cp.p[cp.n] = frames->parts[cp.n];
     paged_resize_kernel<<<1, kPT, 0, s>>>(c, w, n, seqs, lens, add, pos, frames ? frames->count : nullptr);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    return launch_after(paged_copy_kernel, sms, kCopyThreads, s, c, w, n, (const int*)nullptr, seqs, cp);
+    return launch_after(paged_copy_kernel, sms, kCopyThreads, pdl, s, c, w, n, (const int*)nullptr, seqs, cp);
 }
 
 cudaError_t launch_paged_fork(const PagedKv& c, const PagedWorkspace& w, int n, const int* src, const int* dst,
@@ -552,7 +552,7 @@ cudaError_t launch_paged_fork(const PagedKv& c, const PagedWorkspace& w, int n, 
     for (int i = 0; i < n_parts; ++i) cp.p[i] = parts[i];
     paged_fork_kernel<<<1, kPT, 0, s>>>(c, w, n, src, dst, done);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    return launch_after(paged_copy_kernel, 8 * sms, kCopyThreads, s, c, w, n, src, dst, cp);
+    return launch_after(paged_copy_kernel, 8 * sms, kCopyThreads, 1, s, c, w, n, src, dst, cp);
 }
 
 cudaError_t launch_paged_compact(const PagedKv& c, const PagedWorkspace& w, int* live, cudaStream_t s) {
@@ -562,8 +562,8 @@ cudaError_t launch_paged_compact(const PagedKv& c, const PagedWorkspace& w, int*
     const int chunks = (c.pages + kCompactChunk - 1) / kCompactChunk;
     paged_count_kernel<<<chunks, kCT, 0, s>>>(c, w);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    if ((e = launch_after(paged_list_kernel, chunks, kCT, s, c, w, live)) != cudaSuccess) return e;
-    return launch_after(paged_move_kernel, 8 * sms, kCopyThreads, s, c, w);
+    if ((e = launch_after(paged_list_kernel, chunks, kCT, 1, s, c, w, live)) != cudaSuccess) return e;
+    return launch_after(paged_move_kernel, 8 * sms, kCopyThreads, 1, s, c, w);
 }
 
 }  // namespace vc

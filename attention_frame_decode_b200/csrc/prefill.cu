@@ -549,8 +549,8 @@ static cudaError_t pf_paged_begin(const PrefillCtx& c, int slot, int T, cudaStre
     cudaError_t e = cudaGetLastError();
     const PagedKv kv = paged_kernel_kv(*c.kv);
     const PagedWorkspace ws = paged_carve(*c.kv, c.kv->workspace);
-    if (e == cudaSuccess) e = launch_paged_resize(kv, ws, 1, w, w + 1, 0, nullptr, s);
-    if (e == cudaSuccess) e = launch_paged_resize(kv, ws, 1, w, w + 2, 0, w + 3, s);
+    if (e == cudaSuccess) e = launch_paged_resize(kv, ws, 1, w, w + 1, 0, nullptr, c.pdl, s);
+    if (e == cudaSuccess) e = launch_paged_resize(kv, ws, 1, w, w + 2, 0, w + 3, c.pdl, s);
     return e;
 }
 
@@ -754,7 +754,7 @@ cudaError_t run_prefill(const PrefillCtx& c, const uint16_t* x, int T, int slot,
         } else if (kind == '*' && c.kv) {
             const int qkv = (c.Hq + 2 * c.Hk) * c.Dh;
             if ((e = gemm(GE_ROWSCALE, b.act_d, b.ld_d, T, Lw.qkv, b.inv, b.q, qkv, nullptr, 0))) return e;
-            PagedAttnArgs pa = paged_rows(b.q, qkv, c.Hq, c.Hk, c.Dh, b.act_big, b.ld_big, f16);
+            PagedAttnArgs pa = paged_rows(b.q, qkv, c.Hq, c.Hk, c.Dh, b.act_big, b.ld_big, f16, c.pdl);
             pa.seqs = c.kv_pos; pa.pos = c.kv_pos + 3; pa.cu_rows = c.kv_pos + 4;
             pa.batch = 1; pa.rows = T;
             if ((e = paged_attend(*c.kv, ai, pa, s))) return e;

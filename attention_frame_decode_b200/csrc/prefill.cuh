@@ -25,6 +25,7 @@ struct PrefillCtx {
     cudaEvent_t ev[5];   // unpacked[2], gemm done[2], call start
     const vc_paged_kv* kv;   // the paged cache that takes the keys and values; null: k, v
     int* kv_pos;             // its call's arguments (kPagedPrefillInts)
+    int pdl;                 // programmatic dependent launch of its kernels
 };
 static constexpr int kPagedPrefillInts = 8;   // slot, lengths 0 and T, first position granted, row offsets 0 and T
 

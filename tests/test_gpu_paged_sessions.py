@@ -175,3 +175,20 @@ def test_a_session_at_its_tables_end(cuda):
     run.cache.resize(seqs=i32([0]), lens=i32([0]))
     step(24)
     assert int(run.tt[0]) >= 0 and run.cache.lens.tolist() == [1, 25] == run.st.ctx_len.tolist()
+
+
+@pytest.mark.parametrize("graph", [0, 1])
+def test_without_programmatic_launches(cuda, graph):
+    import attention_frame_decode_b200 as vc
+    cfg = synth.tiny_config()
+    run, other = PagedRun(cfg, 5, 2, 96, window=30, sinks=2), PagedRun(cfg, 5, 2, 96, window=30, sinks=2)
+    run.bb.set_option(vc.OPT_PDL, 0)
+    run.bb.set_option(vc.OPT_GRAPH, graph)
+    run.bb.set_taps(run.hid, run.lg)
+    for r in (run, other):
+        r.bb.prefill_paged(bits(synth.prefill_inputs(cfg, 5, 50)), 1, r.st, r.cache)
+    for t in range(20):
+        for r in (run, other):
+            r.bb.step_paged(bits(synth.frame_inputs(cfg, 5, t, 2)), r.st, r.cache, r.tt, r.tf)
+        assert same_row(run, other, 0, 0) and same_row(run, other, 1, 1)
+    assert run.cache.lens.tolist() == [20, 70] and int(run.cache.status[0]) == 0

@@ -74,3 +74,16 @@ def test_a_prefill_that_fails_between_launches_has_taken_the_slots_frames(host, 
     host.fail("cudaLaunchKernel", nth)
     assert host.prefill() == host.vc.VC_ERR_CUDA
     assert "pf_paged_finish_kernel" not in [plain(x) for x in host.launches()]
+
+
+@pytest.mark.parametrize("graph", [0, 1])
+def test_programmatic_launches_are_an_option(host, graph):
+    """VC_OPT_PDL 0: no launch of a step or a prefill over a paged cache begins before the one before it ends"""
+    host.option(host.vc.OPT_GRAPH, graph)
+    for value in (0, 1):
+        host.option(host.vc.OPT_PDL, value)
+        for call in (host.step, host.prefill):
+            assert call() == host.vc.VC_OK
+            early = {plain(x) for x in host.launches() if x.endswith(" pdl")}
+            assert bool(early) == bool(value)
+            assert {"paged_copy_kernel"} <= early if value else not early
