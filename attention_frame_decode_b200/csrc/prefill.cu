@@ -41,6 +41,7 @@ static size_t al(size_t v) { return (v + 255) / 256 * 256; }
 struct PfBufs {
     float *r, *inv, *xc, *dt, *lam, *y, *schunk;
     uint16_t *act_d, *act_big, *zx, *q, *xc16, *sin16;
+    uint16_t* qkv;         // with a paged cache: rows of queries, keys and values, over zx where they fit (else q has their size)
     uint16_t* wdense[2];   // double buffer: the GEMM reads one while the next weight is unpacked
     int ld_d, ld_big;
 };
@@ -64,7 +65,9 @@ static PfBufs carve_pf(uint8_t* base, int T, int d, int E, int Cx, int H, int P,
     b.act_d = (uint16_t*)take((size_t)T * b.ld_d * 2);
     b.act_big = (uint16_t*)take((size_t)T * b.ld_big * 2);
     b.zx = (uint16_t*)take((size_t)T * std::max(zxw, 1) * 2);
-    b.q = (uint16_t*)take((size_t)T * std::max((Hq + 2 * Hk) * Dh, 1) * 2);   // with a paged cache k and v too
+    const int qkv = (Hq + 2 * Hk) * Dh;
+    b.q = (uint16_t*)take((size_t)T * std::max(qkv <= zxw ? Hq * Dh : qkv, 1) * 2);
+    b.qkv = qkv <= zxw ? b.zx : b.q;
     b.xc = (float*)take((size_t)T * std::max(Cx, 1) * 4);
     b.dt = (float*)take((size_t)T * std::max(H, 1) * 4);
     b.lam = (float*)take((size_t)T * std::max(H, 1) * 4);
@@ -753,8 +756,8 @@ cudaError_t run_prefill(const PrefillCtx& c, const uint16_t* x, int T, int slot,
             mi++;
         } else if (kind == '*' && c.kv) {
             const int qkv = (c.Hq + 2 * c.Hk) * c.Dh;
-            if ((e = gemm(GE_ROWSCALE, b.act_d, b.ld_d, T, Lw.qkv, b.inv, b.q, qkv, nullptr, 0))) return e;
-            PagedAttnArgs pa = paged_rows(b.q, qkv, c.Hq, c.Hk, c.Dh, b.act_big, b.ld_big, f16, c.pdl);
+            if ((e = gemm(GE_ROWSCALE, b.act_d, b.ld_d, T, Lw.qkv, b.inv, b.qkv, qkv, nullptr, 0))) return e;
+            PagedAttnArgs pa = paged_rows(b.qkv, qkv, c.Hq, c.Hk, c.Dh, b.act_big, b.ld_big, f16, c.pdl);
             pa.seqs = c.kv_pos; pa.pos = c.kv_pos + 3; pa.cu_rows = c.kv_pos + 4;
             pa.batch = 1; pa.rows = T;
             if ((e = paged_attend(*c.kv, ai, pa, s))) return e;

@@ -87,3 +87,23 @@ def test_programmatic_launches_are_an_option(host, graph):
             early = {plain(x) for x in host.launches() if x.endswith(" pdl")}
             assert bool(early) == bool(value)
             assert {"paged_copy_kernel"} <= early if value else not early
+
+
+@pytest.mark.parametrize("cfg", [synth.nano_config(), synth.tiny_config(attn_q_heads=8, attn_head_dim=64, ssm_heads=4)],
+                         ids=["nano", "projection wider than the Mamba-2 rows"])
+def test_a_dense_prefills_scratch_has_no_room_for_pages(cfg):
+    """bytes of workspace a frame of kv_capacity costs: the prefill's buffers and the split attention's records.  A paged
+    prefill's queries, keys and values lie over the Mamba-2 layers' rows where these are as wide"""
+    import ctypes
+    import attention_frame_decode_b200 as vc
+    size = lambda cap: vc.lib().vc_workspace_bytes(ctypes.byref(vc.make_config(cfg, 1, cap, 1)))  # noqa: E731
+    up = lambda n: -(-n // 128) * 128  # noqa: E731
+    E, Cx, H, d = cfg.d_inner, cfg.conv_dim, cfg.ssm_heads, cfg.d_model
+    q, kv = cfg.attn_q_heads * cfg.attn_head_dim, cfg.attn_kv_heads * cfg.attn_head_dim
+    zx, rows = E + Cx + H, q + 2 * kv
+    big = up(max(E, cfg.mlp_hidden, q))
+    a_frame = 4 * d + 4 + 2 * up(d) + 2 * big + 2 * zx + 2 * (q if rows <= zx else rows) + 4 * Cx + 8 * H + 4 * E + 2 * Cx
+    a_chunk = 6 * H * cfg.ssm_head_dim * cfg.ssm_state                 # of 256 frames
+    a_split = 4 * cfg.attn_q_heads * (cfg.attn_head_dim + 2)           # of 32 frames
+    n = 4096
+    assert size(2 * n) - size(n) == n * a_frame + n // 256 * a_chunk + n // 32 * a_split
