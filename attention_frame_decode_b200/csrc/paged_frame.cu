@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(FrameShape<DH>::THREADS, 1)
         const LineSession me = line[b];
         const int s0 = me.first + at0.j * me.blocks, s1 = s0 + me.blocks, end = min(s1, c1);
         const KeyBlocks kb = key_blocks<BK>(a.c.window, a.c.sinks, me.p, me.p);
-        const int row = a.cu_rows ? a.cu_rows[b] : b;
+        const int row = b;
         uint32_t qb[MT][NH][2];   // Q^T: dims 16 ks + 2 tq .. of heads 8 h + g
         {
             const uint16_t* q0 = a.q + (size_t)row * a.q_ld + (size_t)(at0.j * G) * DH + 2 * tq;
