@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(TileShape<DH, ROWS>::THREADS) paged_tile_kerne
                 if (__syncthreads_or(some)) cleaned = true;
             }
         }
-        // P in 16 bits, as the matrix instruction takes it: 2^-9 (bf16) or 2^-12 (fp16) of each weight
+        // P in 16 bits, as the matrix instruction takes it: off by up to 2^-8 (bf16) or 2^-11 (fp16) of each weight
 #pragma unroll
         for (int ks = 0; ks < kTK / 16; ++ks) {
             uint32_t pa[4];

@@ -572,6 +572,10 @@ __global__ void __launch_bounds__(FrameShape<DH>::THREADS, 1)
     __syncthreads();
     // up to twelve contributors: a thread takes four columns of a row with everything that it needs in flight at once
     // (the maxima and sums are the same addresses for the row's threads)
+    // Twelve, since room for more (registers) costs every join: one session, 40 heads over 8 of 128, under a window of 1024
+    // with 64 sinks (10 contributors to a KV head) 13.5 us, 14.8 with room for 20, 15.7 in the form below; without a window
+    // behind 2000 positions (17) 16.2 (the form below), 15.3 with room for 20; 16 sessions behind 4096 (2 or 3) 56.3, 57.6,
+    // 58.5.
     constexpr int kFew = 12;
     const int pieces = G * (DH / 4);
     auto record_of = [&](const int4& seg, int cta) { return (2 * cta + (seg.x <= range_start(cta * kWarps) ? 0 : 1)) * rec_floats; };

@@ -595,7 +595,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                     }
                 };
                 // the weights 2^(z scale - base): added to the sum, and rounded to 16 bits as the tensor core takes them
-                // (2^-9 of a weight in bf16, 2^-12 in fp16); 0 where not seen
+                // (up to 2^-8 of a weight in bf16, 2^-11 in fp16); 0 where not seen
                 auto weigh = [&](uint32_t (&u)[16], float2 off) {
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
