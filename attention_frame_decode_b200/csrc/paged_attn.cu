@@ -70,10 +70,12 @@ __global__ void __launch_bounds__(TileShape<DH, ROWS>::THREADS) paged_tile_kerne
     extern __shared__ __align__(16) uint8_t smem[];
     uint16_t* Qs = reinterpret_cast<uint16_t*>(smem);   // [rows][SK]
     uint16_t* KV = Qs + kTR * SK;                         // [2 stages][K, V][64][SK]
+    __shared__ uint32_t cleaned;   // chunks of 8 dimensions: infinities or NaN that some row sees were taken out of the values
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tq = lane & 3;
     const int G = a.c.Hq / a.c.Hk;
 
     int session, tile;
+    if (tid == 0) cleaned = 0;   // (barriers come before its use)
     if (blockIdx.x == 0)   // reports every session whose indices do not fit
         for (int i = tid; i < a.batch; i += kTThreads) {
             AttnSession o;
@@ -125,7 +127,6 @@ __global__ void __launch_bounds__(TileShape<DH, ROWS>::THREADS) paged_tile_kerne
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-    bool cleaned = false;   // infinities or NaN that some row sees were taken out of a block's values
     const int pr[2] = {o.p0 + (r0 + 16 * warp + g) / G, o.p0 + (r0 + 16 * warp + g + 8) / G};
     const int mi = lane >> 3, lr = lane & 7;
 
@@ -198,15 +199,16 @@ __global__ void __launch_bounds__(TileShape<DH, ROWS>::THREADS) paged_tile_kerne
             for (int idx = tid; idx < kTK * (DH / 2); idx += kTThreads)
                 odd |= nonfinite2<F16>(*reinterpret_cast<const uint32_t*>(Vs + (idx / (DH / 2)) * SK + 2 * (idx % (DH / 2))));
             if (__syncthreads_or(odd)) {
-                bool some = false;   // (what no page or no later row covers is 0 already)
+                uint32_t some = 0;   // (what no page or no later row covers is 0 already)
                 for (int idx = tid; idx < kTK * DH; idx += kTThreads) {
                     uint16_t* p = Vs + (idx / DH) * SK + idx % DH;
                     if (!nonfinite1<F16>(*p)) continue;
                     *p = 0;
                     const int t = t0 + idx / DH;
-                    some |= a.c.window == 0 || t < a.c.sinks || t > p_lo - a.c.window;
+                    if (a.c.window == 0 || t < a.c.sinks || t > p_lo - a.c.window) some |= 1u << (idx % DH / 8);
                 }
-                if (__syncthreads_or(some)) cleaned = true;
+                if (some) atomicOr(&cleaned, some);
+                __syncthreads();
             }
         }
         // P in 16 bits, as the matrix instruction takes it: off by up to 2^-8 (bf16) or 2^-11 (fp16) of each weight
@@ -235,13 +237,15 @@ __global__ void __launch_bounds__(TileShape<DH, ROWS>::THREADS) paged_tile_kerne
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        float x = cleaned ? 1.0f : 0.0f;
+        uint32_t odd = cleaned;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) x += acc[n][2 * h] * 0.0f + acc[n][2 * h + 1] * 0.0f;
-        if (x == 0.0f || l[h] != l[h] || r0 + 16 * warp + g + 8 * h >= n_rows) continue;
+        for (int n = 0; n < NT; ++n)
+            if (acc[n][2 * h] * 0.0f + acc[n][2 * h + 1] * 0.0f != 0.0f) odd |= 1u << n;
+        if (odd == 0 || l[h] != l[h] || r0 + 16 * warp + g + 8 * h >= n_rows) continue;
         const SeenValues<DH> values = seen_values<DH>(a.c, o.s, j, pr[h]);
 #pragma unroll 1
         for (int k = 0; k < NT; ++k) {
+            if (!((odd >> k) & 1u)) continue;
             const float4 z = odd_values_call<DH, F16>(values, 8 * k + 4 * (tq >> 1));
             const float z0 = tq & 1 ? z.z : z.x, z1 = tq & 1 ? z.w : z.y;
 #pragma unroll

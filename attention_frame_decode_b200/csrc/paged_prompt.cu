@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     __shared__ uint64_t full[ST], empty[ST], clean[ST / 2], work_ready[2], work_taken[2], q_ready[2], q_free, o_free[2], drained;
     __shared__ uint64_t s_full[S::TILES], p_ready[S::TILES], o_done[S::TILES];
     __shared__ uint32_t tmem_base, block_mapped[16];   // of block g at g % 16: at most ST / 2 are in the ring
-    __shared__ int odd_piece[4];
+    __shared__ uint32_t odd_piece[4];   // of piece t at t % 4: 8-dimension chunks of which values were taken out
     __shared__ TileOrder order;
     __shared__ PromptWork work[4];       // piece t at t % 4: written again when the rows are done with it
     __shared__ float top_x[S::ROWS], l_part[S::SHARES][S::ROWS];   // a row's highest score, between its threads; their sums
@@ -512,7 +512,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                     if (!whole && ok) {
                         uint8_t* Vs = ring + s * S::TILE;
                         constexpr int ROW = S::HALVES * 8;   // 16-byte chunks of a row (their order does not matter)
-                        bool odd = false;
+                        uint32_t odd = 0;   // chunks of 8 dimensions
                         // rows first .. last - 1 of the block: seen by none, or by some
                         auto sweep = [&](int first, int last, bool none) {
                             const int n_chunks = max(last - first, 0) * ROW;
@@ -525,7 +525,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                                 } else {
                                     const uint4 x = *at;
                                     if (any_nonfinite<F16>(x)) {
-                                        odd = true;
+                                        odd |= 1u << ((c & 8) | ((c ^ (first + k / ROW)) & 7));   // (swizzled rows)
                                         *at = make_uint4(finite2<F16>(x.x), finite2<F16>(x.y), finite2<F16>(x.z), finite2<F16>(x.w));
                                     }
                                 }
@@ -543,7 +543,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                             sweep(clip(a.c.sinks), clip(from), true);
                             sweep(clip(from > a.c.sinks ? from : a.c.sinks), clip(to), false);
                         }
-                        if (odd) odd_piece[t & 3] = 1;
+                        if (odd) atomicOr(&odd_piece[t & 3], odd);
                         fence_proxy_async();
                     }
                     __syncwarp();
@@ -688,7 +688,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 wait(&o_done[i], gi - 1);
                 tc_fence_after();
             }
-            float odd = odd_piece[t & 3] != 0;   // not 0: infinities or NaN, taken out of the values, or in the results (NaN)
+            // bits: chunks of 8 dimensions with infinities or NaN, taken out of the values or in the thread's results
+            uint32_t odd = odd_piece[t & 3];
 #pragma unroll 1
             for (int c = half * (DH / S::SHARES); c < (half + 1) * (DH / S::SHARES); c += 32) {
                 float v[32];
@@ -705,7 +706,12 @@ __global__ void __launch_bounds__(kPThreads, 1)
 #pragma unroll
                 for (int e = 0; e < 32; ++e) v[e] *= inv;
 #pragma unroll
-                for (int e = 0; e < 32; ++e) odd = fmaf(v[e], 0.0f, odd);
+                for (int k = 0; k < 4; ++k) {
+                    float x = v[8 * k] * 0.0f;
+#pragma unroll
+                    for (int e = 1; e < 8; ++e) x = fmaf(v[8 * k + e], 0.0f, x);
+                    if (x != 0.0f) odd |= 1u << (c / 8 + k);
+                }
                 if (of == 1) {
                     // four lanes exchange the 16-byte pieces of their rows, so that each writes 64 bytes of a row together
                     uint4 x[4];
@@ -728,13 +734,14 @@ __global__ void __launch_bounds__(kPThreads, 1)
                         __stcg(reinterpret_cast<float4*>(rec + at * DH + c + e), make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]));
                 }
             }
-            if (__any_sync(0xffffffffu, odd != 0.0f)) {   // the rows that see them get them
+            if (__any_sync(0xffffffffu, odd != 0)) {   // the rows that see them get them
                 __threadfence_block();
                 __syncwarp();   // (lanes write one another's rows)
-                if (odd != 0.0f && in && ok && l == l) {
+                if (in && ok && l == l) {
                     const SeenValues<DH> values = seen_values<DH>(a.c, w.s, w.j, me.p);
 #pragma unroll 1
                     for (int d = half * (DH / S::SHARES); d < (half + 1) * (DH / S::SHARES); d += 4) {
+                        if (!((odd >> (d / 8)) & 1u)) continue;
                         const float4 z = odd_values<DH, F16>(values, d);
                         float* r4 = rec + at * DH + d;
                         uint16_t* o4 = a.out + mine + d;

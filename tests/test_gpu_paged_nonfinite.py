@@ -51,15 +51,16 @@ def check(s, out, rows, scale=None):
 
 def spread(s):
     """values that are not finite all over what session 0's rows see, sinks, window's edge, old pages, the newest row: one
-    sign in dimensions 0 to 5, both in 6, NaN in 7"""
+    sign in six dimensions, both in another, NaN in another"""
     n = s.ctx[0] + s.rows[0]
     first = 0 if not s.window else max(s.ctx[0] - s.window + 1, 0)
     at = [0, first, first + (n - first) // 3, (first + n) // 2, n - 20, s.ctx[0]]
-    for k, p in enumerate(at):
-        place(s, 0, p, 0, k, INF if k % 2 else -INF)
-    place(s, 0, at[2], 0, 6, INF)
-    place(s, 0, at[4], 0, 6, -INF)
-    place(s, 0, at[3], 0, 7, NAN)
+    dims = [0, s.d // 2 + 1, s.d - 1, s.d // 4 + 2, 5, s.d // 2 - 2]
+    for k, (p, dim) in enumerate(zip(at, dims)):
+        place(s, 0, p, 0, dim, INF if k % 2 else -INF)
+    place(s, 0, at[2], 0, s.d // 2 + 4, INF)
+    place(s, 0, at[4], 0, s.d // 2 + 4, -INF)
+    place(s, 0, at[3], 0, s.d - 9, NAN)
 
 
 FRAMES = [((4, 2, 64), 32, 0, 0, 700), ((40, 8, 128), 64, 300, 5, 2100), ((8, 2, 32), 16, 100, 30, 517),
