@@ -16,8 +16,9 @@
 // their way 600 to 1300, weights 1100 alone, their way back 200 -- against the other tiles' chains: about 3400 cycles
 // at head dim 128, whose tensor memory has no room for a third tile, and 2800 at head dim 64 with four tiles (with two
 // tiles of 128 keys and two threads a row 3700: 219 us where four tiles take 198).
-// Measured on a B200: 8192 rows of 40 heads over 8 of 128, window 4096, 64 sinks: 494 us, 1060 TFLOP/s of what the rows
-// see; 12 blocks of 1 to 900 rows, 32 heads over 8 of 64, window 2048: 147 us with the longest tiles first (splitting the
+// Measured on a B200: 8192 rows of 40 heads over 8 of 128, window 4096, 64 sinks: 490 us at 1965 MHz, 1060 TFLOP/s of what
+// the rows see, and 554 us, 941 TFLOP/s, in a loop of seconds (1725 MHz under the power cap); 12 blocks of 1 to 900 rows,
+// 32 heads over 8 of 64, window 2048: 150 us with the longest tiles first (splitting the
 // last round's key blocks gave back in records and joins what it evened out, and cost the other launch 2%).  A polynomial
 // on the FMA units for every fourth or eighth exponential: 4 to 9% slower (issue slots).
 // Warps: 0 copies K and V page by page (TMA, 128-byte swizzle) into a ring; 1 issues the MMAs; 2 hands out pieces and

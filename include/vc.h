@@ -399,7 +399,8 @@ vc_status vc_paged_fork(const vc_paged_kv* kv, int n, const int32_t* src, const 
 
 /* Moves the pages in use to the front: with L pages in use, the k-th lowest of those at L and above goes to
  * the k-th lowest free page below L, in every layer; the tables and refs follow.  live[0] = L (device int32, or NULL):
- * the pages from L on are free and may be given back.  Freed pages keep their bytes. */
+ * the pages from L on are free.  Layers are the outermost index, so these are a tail of each layer: a smaller cache
+ * is the first L pages of every layer copied, with refs[0..L-1] and the same table and len.  Freed pages keep their bytes. */
 vc_status vc_paged_compact(const vc_paged_kv* kv, int32_t* live, vc_stream_t stream);
 
 /* Rows of one attention call: row r of session i (cu_rows[i] <= r < cu_rows[i + 1]; cu_rows NULL: row i)
@@ -424,8 +425,11 @@ typedef struct {
 /* Appends the rows' keys and values to one layer's pages and attends, for prompts (many rows of a session) and
  * single frames (cu_rows NULL): out = sum_t softmax_t(scale q.k_t) v_t over the keys that the row
  * sees, GQA (query head i reads KV head i kv_heads / q_heads).  Products accumulate in fp32 and so do
- * the softmax's maximum and sum; out is rounded once.  A row that sees no key gets 0; keys that a
- * row does not see do not touch it, whatever they hold.  A session is skipped, and its rows of out left, where pos < 0, or
+ * the softmax's maximum and sum; out is rounded once.  A weight goes into its product with a value in the cache's 16 bits
+ * (off by up to 2^-8 of it in bf16, 2^-11 in fp16); in single frames of up to 16 query heads to a KV head and 2048 sessions
+ * the 16-bit rest of it goes in too (2^-16 in bf16).  A row that sees no key gets 0; keys that a
+ * row does not see do not touch it, whatever they hold.  Among the values that it sees infinities of one sign are the
+ * output's, both signs or NaN make it NaN; a seen key that is not finite may make the whole row NaN.  A session is skipped, and its rows of out left, where pos < 0, or
  * where its index, rows, length or columns do not fit (VC_DEV_INVALID).  1 <= batch <= kv->seqs,
  * 1 <= rows (rows == batch where cu_rows is NULL). */
 vc_status vc_paged_attend(const vc_paged_kv* kv, int layer, const vc_attn_rows* rows, vc_stream_t stream);

@@ -192,3 +192,26 @@ def test_without_programmatic_launches(cuda, graph):
             r.bb.step_paged(bits(synth.frame_inputs(cfg, 5, t, 2)), r.st, r.cache, r.tt, r.tf)
         assert same_row(run, other, 0, 0) and same_row(run, other, 1, 1)
     assert run.cache.lens.tolist() == [20, 70] and int(run.cache.status[0]) == 0
+
+
+def test_a_smaller_pool_after_compact(cuda):
+    """the first pages of every layer, refs cut to them, the same table and lengths: sessions go on over it"""
+    import attention_frame_decode_b200 as vc
+    cfg = synth.tiny_config()
+    run, whole = PagedRun(cfg, 8, 3, 64, pages=40), PagedRun(cfg, 8, 3, 64, pages=40)
+    for r in (run, whole):
+        for slot, n in enumerate((40, 21, 33)):
+            r.bb.prefill_paged(bits(synth.prefill_inputs(cfg, 8, n)), slot, r.st, r.cache)
+        r.cache.resize(seqs=i32([0]), lens=i32([0]))
+    live = i32([0])
+    run.cache.compact(live=live)
+    n = int(live) + 3
+    c = run.cache
+    run.cache = vc.PagedCache(c.k[:, :n].contiguous(), c.v[:, :n].contiguous(), c.table, c.lens, c.refs[:n].contiguous(),
+                              q_heads=c.q_heads, window=c.window, sinks=c.sinks)
+    for t in range(15):
+        for r in (run, whole):
+            r.bb.step_paged(bits(synth.frame_inputs(cfg, 8, t, 3)), r.st, r.cache, r.tt, r.tf)
+        assert all(same_row(run, whole, i, i) for i in range(3))
+    assert run.cache.lens.tolist() == [15, 36, 48] == run.st.ctx_len.tolist() and int(run.cache.status[0]) == 0
+    assert int((run.cache.refs > 0).sum()) == 1 + 3 + 3
