@@ -340,6 +340,8 @@ vc_status vc_gemv_noalloc_reset(vc_stream_t stream);
  *              leaves its counters zero.  Calls that share it run one after another (one stream, or
  *              ordered streams; that goes for captured graphs too).  A call that set VC_DEV_TIMEOUT
  *              leaves it undefined: zero it again.
+ * After VC_ERR_CUDA from a call on the cache, where one launch failed behind others, the sessions that it named are to be
+ * ended (resized to 0): their tables may name pages whose positions were not copied.
  * A new cache has table -1, len 0 and refs 0.  page_size: a power of two, 16..256; head_dim: 32, 64,
  * 128 or 256; kv_heads divides q_heads; columns * page_size is at most 2^30; seqs * columns, seqs * kv_heads and
  * pages * kv_heads * page_size are below 2^31.  window: a query at position p sees the keys
@@ -367,7 +369,8 @@ size_t vc_paged_workspace_bytes(const vc_paged_kv* kv);
  *      position on can see: whole pages behind the sinks and at or below (that position - window).
  *   2. A row that grows asks for its new pages, and, where the page that it will write next is shared,
  *      for a copy of that page (the positions it holds are copied in every layer).  Requests are
- *      served in row order, each session's in order of position, from the lowest free page up.
+ *      served in row order, each session's in order of position, from the lowest free page up.  A row whose pages are
+ *      not all there gets none, and neither does any row behind it that asks for some.
  *   3. pos[i] = the first position whose rows the caller may write now, min(old, new length), or -1:
  *      too few free pages or columns (the length stays; VC_DEV_CAPACITY) or a bad row (a session out
  *      of range or named by an earlier row, a length below 0 or inside a page that the window has

@@ -215,3 +215,51 @@ def test_a_smaller_pool_after_compact(cuda):
         assert all(same_row(run, whole, i, i) for i in range(3))
     assert run.cache.lens.tolist() == [15, 36, 48] == run.st.ctx_len.tolist() and int(run.cache.status[0]) == 0
     assert int((run.cache.refs > 0).sum()) == 1 + 3 + 3
+
+
+def test_a_session_whose_fork_found_no_page_starts_anew(cuda):
+    import attention_frame_decode_b200 as vc
+    cfg = synth.tiny_config()
+    run, fresh = PagedRun(cfg, 8, 3, 64, pages=4), PagedRun(cfg, 8, 3, 64)
+    x = bits(synth.prefill_inputs(cfg, 8, 40))
+    run.bb.prefill_paged(x[:40], 0, run.st, run.cache)
+    run.bb.prefill_paged(x[:9], 1, run.st, run.cache)
+    parts = vc.session_parts([run.st.ssm, run.st.conv, run.st.ctx_len])
+    done = i32([7, 7])
+    run.cache.fork(i32([0, 0]), i32([1, 2]), parts=parts, done=done)      # one page is free once session 1's went back
+    assert done.tolist() == [1, 0] and run.cache.lens.tolist() == [40, 40, 0] and int(run.cache.status[0]) == CAPACITY
+    run.st.ctx_len[2] = 5                                                   # as if it had held frames
+    run.st.ssm[:, 2] = 1.0
+    run.cache.resize(seqs=i32([0, 1]), lens=i32([0, 0]))                    # four pages are free
+    for t in range(3):
+        for r in (run, fresh):
+            r.bb.step_paged(bits(synth.frame_inputs(cfg, 8, t, 3)), r.st, r.cache, r.tt, r.tf)
+        assert all(same_row(run, fresh, i, i) for i in range(3))
+    assert run.cache.lens.tolist() == [3, 3, 3] == run.st.ctx_len.tolist()
+
+
+@pytest.mark.parametrize("graph", [0, 1])
+def test_every_session_ends_at_once(cuda, graph):
+    """all sixteen rows start anew in one step, while slots that the step does not name keep their state"""
+    import attention_frame_decode_b200 as vc
+    cfg = synth.tiny_config()
+    run, fresh = PagedRun(cfg, 8, 16, 64, pages=40), PagedRun(cfg, 8, 16, 64, pages=40)
+    for r in (run, fresh):
+        r.bb.set_option(vc.OPT_GRAPH, graph)
+        r.bb.set_taps(r.hid, r.lg)
+    step = lambda r, t, B=16: r.bb.step_paged(bits(synth.frame_inputs(cfg, 8, t, 16))[:B], r.st, r.cache, r.tt[:B], r.tf[:B])  # noqa: E731
+    for t in range(5):
+        step(run, t)
+    run.cache.resize(lens=torch.zeros(16, dtype=torch.int32, device="cuda"))
+    keep = [run.st.ssm[:, 12:].clone(), run.st.conv[:, 12:].clone(), run.st.ctx_len[12:].clone()]
+    for r in (run, fresh):
+        r.bb.set_taps(None, None)
+        step(r, 0, 12)
+        r.bb.set_taps(r.hid, r.lg)
+    assert all(torch.equal(a, b[:, 12:] if b.dim() > 1 else b[12:]) for a, b in zip(keep, (run.st.ssm, run.st.conv, run.st.ctx_len)))
+    for t in range(1, 4):
+        for r in (run, fresh):
+            step(r, t)
+        assert all(same_row(run, fresh, i, i) for i in range(16))
+    assert run.cache.lens.tolist() == [4] * 12 + [3] * 4 == run.st.ctx_len.tolist()
+    assert fresh.st.ctx_len.tolist() == [4] * 12 + [3] * 4
