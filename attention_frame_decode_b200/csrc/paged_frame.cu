@@ -25,7 +25,9 @@ namespace vc {
 static constexpr int kFMaxStages = 4;   // below eight (see look_up)
 static constexpr int kFMaxBatch = 2048;
 // Whole (session, KV head)s go to warps, and no join is needed, where that gives no warp more than this many units
-// over an equal share: a join costs about as much as four units (2 us).
+// over an equal share: a join costs about as much as four units (2 us).  64 sessions, 40 heads over 8 of 128, whole and cut:
+// behind 100 positions (4 units over the share) 13.7 and 19.2 us, 130 (6) 16.0 and 19.8, 200 (8) 20.2 and 21.7, 300 (11) 27.2
+// and 25.4; one share or less a warp (16 sessions): 100 (6) 12.4 and 13.7, 200 (12) 17.8 and 16.8.
 static constexpr int kWholeUnits = 4;
 
 template <int DH>
